@@ -2,7 +2,8 @@
 
 The computation runs in hand-written HIP kernels inside libmoe.so, reached
 through its C ABI (include/moe.h, include/moe_mxfp8.h, include/moe_backward.h,
-include/moe_variants.h). This package is the thin Python binding
+include/moe_variants.h, include/moe_norm.h, include/moe_update.h). This package
+is the thin Python binding
 (same function names as the C entry points) plus owners of device buffers.
 Importing it does not load the library; the first call does, and it raises
 if libmoe.so has not been built (there is no fallback implementation).
@@ -22,5 +23,8 @@ from ._binding import (  # noqa: F401
     moe_ffn_tile_shape, moe_pack_expert_weights, pack_expert_weights, MOE_WEIGHTS_PACKED,
     MOE_WEIGHTS_STACKED, moe_permute_noalloc, moe_down_workspace_size, moe_gate_up_workspace_size,
     moe_route_workspace_size,
+    moe_layer_norm, moe_layer_norm_backward, moe_layer_norm_backward_workspace_size,
+    moe_orthogonalize, moe_orthogonalize_workspace_size, moe_muon_update, moe_matrices,
+    moe_muon_desc,
 )
 from .layer import EPRankShareForward, LayerForward, LayerForwardMXFP8, LayerTrain  # noqa: F401

@@ -1,5 +1,6 @@
 """ctypes binding of libmoe (include/moe.h, include/moe_mxfp8.h,
-include/moe_backward.h, include/moe_variants.h): one Python function per C entry
+include/moe_backward.h, include/moe_variants.h, include/moe_norm.h,
+include/moe_update.h): one Python function per C entry
 point, with the same name. Arguments are torch tensors (device memory) or
 None; the binding checks their device, dtype, shape and contiguity, passes
 their addresses and torch's current HIP stream, and raises MoeError on a
@@ -50,6 +51,10 @@ EXPORTS = (
     "moe_layer_backward", "moe_backward_workspace_size",
     # interface variants
     "moe_route_typed", "moe_expert_ffn_ptrs",
+    # layer norm
+    "moe_layer_norm", "moe_layer_norm_backward", "moe_layer_norm_backward_workspace_size",
+    # optimiser step of the expert matrices
+    "moe_orthogonalize", "moe_orthogonalize_workspace_size", "moe_muon_update",
 )
 
 
@@ -82,8 +87,19 @@ def make_desc(T: int, D: int, E: int, top_k: int, I: int, ep_size: int = 1, ep_r
                     MOE_F16 if y_fp16 else MOE_F32)
 
 
+class moe_matrices(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ld", ctypes.c_int64),
+                ("stride", ctypes.c_int64)]
+
+
+class moe_muon_desc(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_float) for n in ("lr", "mu", "weight_decay", "scale", "eps")]
+                + [(n, ctypes.c_int32) for n in ("nesterov", "steps")])
+
+
 _P = ctypes.c_void_p
 _D = ctypes.POINTER(moe_desc)
+_M = ctypes.POINTER(moe_matrices)
 _SIGS = {
     "moe_route": (ctypes.c_int32, [_D, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "moe_route_workspace_size": (ctypes.c_size_t, [_D]),
@@ -147,6 +163,20 @@ _SIGS = {
     "moe_route_typed": (ctypes.c_int32, [_D, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P]),
     "moe_expert_ffn_ptrs": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64,
                                              _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "moe_layer_norm": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P, _P, _P,
+                                        ctypes.c_float, _P, _P, _P, _P]),
+    "moe_layer_norm_backward": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                                 _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                                 ctypes.c_size_t, _P]),
+    "moe_layer_norm_backward_workspace_size": (ctypes.c_size_t, [ctypes.c_int64,
+                                                                 ctypes.c_int32]),
+    "moe_orthogonalize": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _M,
+                                           ctypes.c_int32, ctypes.c_float, _M, _P,
+                                           ctypes.c_size_t, _P]),
+    "moe_orthogonalize_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 4),
+    "moe_muon_update": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                         ctypes.POINTER(moe_muon_desc), _M, _M, _M, _P,
+                                         ctypes.c_size_t, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -814,3 +844,146 @@ def moe_expert_ffn_ptrs(d: moe_desc, n_experts, inter, cap_rows, x_perm, offsets
            lib.moe_expert_ffn_ptrs(ctypes.byref(d), int(n_experts), int(inter), int(cap_rows),
                                    *args, _stream(stream)))
 
+
+# ---------------------------------------------------------------------------
+# Layer norm (include/moe_norm.h).
+# ---------------------------------------------------------------------------
+_ACT_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _same_device(named) -> torch.device:
+    """The one GPU all given tensors are on."""
+    dev = None
+    for name, t in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name}: must be a GPU tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
+        dev = t.device
+    return dev
+
+
+def _act_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _ACT_DTYPES:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected float32 or bfloat16")
+    return _ACT_DTYPES[t.dtype]
+
+
+def _rows(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name}: expected [rows, D]")
+    return t.shape
+
+
+def moe_layer_norm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
+    """x, y [rows, D] fp32 or bf16; gamma, beta [D] fp32 or None; mean, rstd
+    [rows] fp32 or None. Runs on x's device."""
+    lib = load_library()
+    rows, D = _rows(x, "x")
+    f32 = torch.float32
+    dev = _same_device((("x", x), ("gamma", gamma), ("beta", beta), ("y", y), ("mean", mean),
+                        ("rstd", rstd)))
+    args = (
+        int(rows), int(D), _act_code(x, "x"),
+        _ptr(x, "x"),
+        _ptr(gamma, "gamma", f32, (D,)),
+        _ptr(beta, "beta", f32, (D,)),
+        float(eps),
+        _ptr(y, "y", x.dtype, (rows, D)),
+        _ptr(mean, "mean", f32, (rows,)),
+        _ptr(rstd, "rstd", f32, (rows,)),
+    )
+    with torch.cuda.device(dev):
+        _check("moe_layer_norm", lib.moe_layer_norm(*args, _stream(stream)))
+
+
+def moe_layer_norm_backward_workspace_size(rows: int, D: int) -> int:
+    return int(load_library().moe_layer_norm_backward_workspace_size(int(rows), int(D)))
+
+
+def moe_layer_norm_backward(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
+    """Shapes and dtypes as in moe_layer_norm (dy, dres, dx like x); dres,
+    dgamma and dbeta may be None, and ws with both of the last two."""
+    lib = load_library()
+    rows, D = _rows(x, "x")
+    f32 = torch.float32
+    dev = _same_device((("x", x), ("dy", dy), ("gamma", gamma), ("mean", mean), ("rstd", rstd),
+                        ("dres", dres), ("dx", dx), ("dgamma", dgamma), ("dbeta", dbeta),
+                        ("ws", ws)))
+    args = (
+        int(rows), int(D), _act_code(x, "x"),
+        _ptr(x, "x"),
+        _ptr(dy, "dy", x.dtype, (rows, D)),
+        _ptr(gamma, "gamma", f32, (D,)),
+        _ptr(mean, "mean", f32, (rows,)),
+        _ptr(rstd, "rstd", f32, (rows,)),
+        _ptr(dres, "dres", x.dtype, (rows, D)),
+        _ptr(dx, "dx", x.dtype, (rows, D)),
+        _ptr(dgamma, "dgamma", f32, (D,)),
+        _ptr(dbeta, "dbeta", f32, (D,)),
+        _ptr(ws, "ws", torch.uint8),
+        ws.numel() if ws is not None else 0,
+    )
+    with torch.cuda.device(dev):
+        _check("moe_layer_norm_backward", lib.moe_layer_norm_backward(*args, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Orthogonalisation and the Muon update (include/moe_update.h). Batches of
+# matrices are tensors [n, rows, cols] (or [rows, cols]) whose columns are
+# adjacent in memory; rows and matrices may be spaced (views of the gate or up
+# columns of a gate_up tensor).
+# ---------------------------------------------------------------------------
+def _matrices(t, name: str, shape=None):
+    """(moe_matrices, (n, rows, cols)) of a tensor of matrices."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+        raise ValueError(f"{name}: expected [n, rows, cols] or [rows, cols]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    v = t.detach() if t.dim() == 3 else t.detach().unsqueeze(0)
+    n, rows, cols = v.shape
+    if cols > 1 and v.stride(2) != 1:
+        raise ValueError(f"{name}: the columns of a row must be adjacent in memory")
+    # The stride of a dimension of size 1 means nothing.
+    ld = v.stride(1) if rows > 1 else cols
+    stride = v.stride(0) if n > 1 else (rows - 1) * ld + cols
+    return moe_matrices(v.data_ptr(), _act_code(t, name), ld, stride), (n, rows, cols)
+
+
+def moe_orthogonalize_workspace_size(n: int, rows: int, cols: int, steps: int = 5) -> int:
+    return int(load_library().moe_orthogonalize_workspace_size(int(n), int(rows), int(cols),
+                                                               int(steps)))
+
+
+def moe_orthogonalize(g, out, ws, steps=5, eps=1e-7, stream=None):
+    """out <- the Newton-Schulz orthogonalisation of each matrix of g (fp32 or
+    bf16 each; out may be g)."""
+    lib = load_library()
+    dev = _same_device((("g", g), ("out", out), ("ws", ws)))
+    mg, (n, rows, cols) = _matrices(g, "g")
+    mo, _ = _matrices(out, "out", g.shape)
+    args = (n, rows, cols, ctypes.byref(mg), int(steps), float(eps), ctypes.byref(mo),
+            _ptr(ws, "ws", torch.uint8), ws.numel() if ws is not None else 0)
+    with torch.cuda.device(dev):
+        _check("moe_orthogonalize", lib.moe_orthogonalize(*args, _stream(stream)))
+
+
+def moe_muon_update(g, momentum, w, ws, lr, mu=0.95, weight_decay=0.0, scale=1.0, nesterov=True,
+                    steps=5, eps=1e-7, stream=None):
+    """One Muon step on the matrices of w (fp32 or bf16), in place, from the
+    gradients g (fp32 or bf16) and the fp32 momentum, updated too."""
+    lib = load_library()
+    dev = _same_device((("g", g), ("momentum", momentum), ("w", w), ("ws", ws)))
+    mg, (n, rows, cols) = _matrices(g, "g")
+    mm, _ = _matrices(momentum, "momentum", g.shape)
+    mw, _ = _matrices(w, "w", g.shape)
+    d = moe_muon_desc(float(lr), float(mu), float(weight_decay), float(scale), float(eps),
+                      int(bool(nesterov)), int(steps))
+    args = (n, rows, cols, ctypes.byref(d), ctypes.byref(mg), ctypes.byref(mm), ctypes.byref(mw),
+            _ptr(ws, "ws", torch.uint8), ws.numel() if ws is not None else 0)
+    with torch.cuda.device(dev):
+        _check("moe_muon_update", lib.moe_muon_update(*args, _stream(stream)))

@@ -4,6 +4,7 @@
 // nullness and runs before any HIP call, so a rejected call needs no GPU.
 // The library allocates nothing, keeps no pointer and never synchronises.
 #include <limits.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -11,6 +12,8 @@
 #include "moe_internal.h"
 #include "moe_backward.h"
 #include "moe_mxfp8.h"
+#include "moe_norm.h"
+#include "moe_update.h"
 #include "moe_variants.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -1011,3 +1014,127 @@ MOE_API moe_status moe_layer_backward(const moe_desc* desc, const void* x, const
   return hip_status(e);
 }
 
+// ---------------------------------------------------------------------------
+// Layer norm (include/moe_norm.h)
+// ---------------------------------------------------------------------------
+namespace {
+
+moe_status check_norm(int64_t rows, int32_t D, int32_t dtype) {
+  if (rows < 0 || D < 1) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (D > MOE_MAX_WIDTH || rows >= (int64_t(1) << 40) / D) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t norm_bwd_ws(int64_t rows, int32_t D) {
+  return align_up(moe::norm_bwd_part_floats(rows, D) * sizeof(float));
+}
+
+}  // namespace
+
+MOE_API moe_status moe_layer_norm(int64_t rows, int32_t D, int32_t dtype, const void* x,
+                                  const float* gamma, const float* beta, float eps, void* y,
+                                  float* mean, float* rstd, void* stream) {
+  moe_status st = check_norm(rows, D, dtype);
+  if (st != MOE_OK) return st;
+  if (!(eps >= 0.f) || isinf(eps)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (x == nullptr || y == nullptr) return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_norm(dtype == MOE_BF16, rows, D, x, gamma, beta, eps, y, mean,
+                                     rstd, static_cast<hipStream_t>(stream)));
+}
+
+MOE_API size_t moe_layer_norm_backward_workspace_size(int64_t rows, int32_t D) {
+  return check_norm(rows, D, MOE_F32) == MOE_OK ? norm_bwd_ws(rows, D) : 0;
+}
+
+MOE_API moe_status moe_layer_norm_backward(int64_t rows, int32_t D, int32_t dtype, const void* x,
+                                           const void* dy, const float* gamma, const float* mean,
+                                           const float* rstd, const void* dres, void* dx,
+                                           float* dgamma, float* dbeta, void* ws, size_t ws_bytes,
+                                           void* stream) {
+  moe_status st = check_norm(rows, D, dtype);
+  if (st != MOE_OK) return st;
+  if (rows > 0 && (x == nullptr || dy == nullptr || mean == nullptr || rstd == nullptr ||
+                   dx == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (dgamma != nullptr || dbeta != nullptr)) {
+    if (ws == nullptr) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < norm_bwd_ws(rows, D)) return MOE_ERR_WORKSPACE;
+  }
+  return hip_status(moe::launch_norm_bwd(dtype == MOE_BF16, rows, D, x, dy, gamma, mean, rstd,
+                                         dres, dx, dgamma, dbeta, static_cast<float*>(ws),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// Orthogonalisation and the Muon update (include/moe_update.h)
+// ---------------------------------------------------------------------------
+namespace {
+
+moe_status check_orth_sizes(int32_t n, int32_t rows, int32_t cols, int32_t steps) {
+  if (n < 0 || rows < 1 || cols < 1 || steps < 1 || steps > MOE_MAX_ORTH_STEPS)
+    return MOE_ERR_INVALID_ARG;
+  if (n > 65535 || rows > MOE_MAX_WIDTH || cols > MOE_MAX_WIDTH || std::min(rows, cols) > 32768 ||
+      moe::orth_tiles(n, rows, cols) >= (int64_t(1) << 30))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_matrices(const moe_matrices* m, int32_t n, int32_t cols, bool bf16_ok) {
+  if (m == nullptr || m->data == nullptr || m->ld < cols || (n > 1 && m->stride < cols))
+    return MOE_ERR_INVALID_ARG;
+  if (m->dtype != MOE_F32 && !(bf16_ok && m->dtype == MOE_BF16)) return MOE_ERR_UNSUPPORTED;
+  // Offsets stay far inside 64 bits.
+  if (m->ld >= (int64_t(1) << 40) || m->stride >= (int64_t(1) << 44)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_orth_ws(int32_t n, int32_t rows, int32_t cols, const void* ws,
+                         size_t ws_bytes) {
+  if (ws == nullptr || reinterpret_cast<uintptr_t>(ws) % 256 != 0) return MOE_ERR_INVALID_ARG;
+  return ws_bytes < align_up(moe::orth_ws_bytes(n, rows, cols)) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+}  // namespace
+
+MOE_API size_t moe_orthogonalize_workspace_size(int32_t n, int32_t rows, int32_t cols,
+                                                int32_t steps) {
+  if (check_orth_sizes(n, rows, cols, steps) != MOE_OK) return 0;
+  return align_up(moe::orth_ws_bytes(n, rows, cols));
+}
+
+MOE_API moe_status moe_orthogonalize(int32_t n, int32_t rows, int32_t cols, const moe_matrices* g,
+                                     int32_t steps, float eps, const moe_matrices* out, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  moe_status st = check_orth_sizes(n, rows, cols, steps);
+  if (st != MOE_OK) return st;
+  if (!(eps >= 0.f) || isinf(eps)) return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if ((st = check_matrices(g, n, cols, true)) != MOE_OK) return st;
+  if ((st = check_matrices(out, n, cols, true)) != MOE_OK) return st;
+  if ((st = check_orth_ws(n, rows, cols, ws, ws_bytes)) != MOE_OK) return st;
+  const moe_muon_desc d{0.f, 0.f, 0.f, 0.f, eps, 0, steps};
+  return hip_status(moe::launch_orth(n, rows, cols, *g, nullptr, *out, d, ws,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_muon_update(int32_t n, int32_t rows, int32_t cols,
+                                   const moe_muon_desc* desc, const moe_matrices* g,
+                                   const moe_matrices* momentum, const moe_matrices* w, void* ws,
+                                   size_t ws_bytes, void* stream) {
+  if (desc == nullptr) return MOE_ERR_INVALID_ARG;
+  moe_status st = check_orth_sizes(n, rows, cols, desc->steps);
+  if (st != MOE_OK) return st;
+  if (!isfinite(desc->lr) || !isfinite(desc->mu) || !isfinite(desc->weight_decay) ||
+      !isfinite(desc->scale) || !(desc->eps >= 0.f) || isinf(desc->eps) ||
+      (desc->nesterov != 0 && desc->nesterov != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (n == 0) return MOE_OK;
+  if ((st = check_matrices(g, n, cols, true)) != MOE_OK) return st;
+  if ((st = check_matrices(momentum, n, cols, false)) != MOE_OK) return st;
+  if ((st = check_matrices(w, n, cols, true)) != MOE_OK) return st;
+  if ((st = check_orth_ws(n, rows, cols, ws, ws_bytes)) != MOE_OK) return st;
+  return hip_status(moe::launch_orth(n, rows, cols, *g, momentum, *w, *desc, ws,
+                                     static_cast<hipStream_t>(stream)));
+}

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "moe.h"
+#include "moe_update.h"
 
 namespace moe {
 
@@ -218,5 +219,24 @@ hipError_t launch_swiglu_bwd_f32(int64_t rows, int inter, const float* dh, float
 hipError_t launch_combine(const moe_desc& d, const void* y_perm, const int32_t* pos,
                           const float* topk_w, const void* residual, const void* shared_out,
                           int res_begin, int res_rows, void* out, hipStream_t s);
+
+// Layer norm (norm.hip). part: norm_bwd_part_floats() floats (NULL when
+// dgamma and dbeta are). rows > 0 in launch_norm.
+size_t norm_bwd_part_floats(int64_t rows, int D);
+hipError_t launch_norm(bool bf16, int64_t rows, int D, const void* x, const float* gamma,
+                       const float* beta, float eps, void* y, float* mean, float* rstd,
+                       hipStream_t s);
+hipError_t launch_norm_bwd(bool bf16, int64_t rows, int D, const void* x, const void* dy,
+                           const float* gamma, const float* mean, const float* rstd,
+                           const void* dres, void* dx, float* dgamma, float* dbeta, float* part,
+                           hipStream_t s);
+
+// Newton-Schulz orthogonalisation (orth.hip) of g into w, or, with a momentum,
+// a Muon step on w. ws: orth_ws_bytes() bytes. orth_tiles bounds the
+// workgroups of any launch (the caller keeps it below 2^30).
+size_t orth_ws_bytes(int n, int rows, int cols);
+int64_t orth_tiles(int n, int rows, int cols);
+hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const moe_matrices* mom,
+                       const moe_matrices& w, const moe_muon_desc& d, void* ws, hipStream_t s);
 
 }  // namespace moe
