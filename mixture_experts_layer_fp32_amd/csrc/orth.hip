@@ -50,6 +50,7 @@ typedef __attribute__((address_space(3))) unsigned char lds_u8;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 4096.f, kScaleA = 4096.f, kScaleP = 1024.f;
 constexpr int kXcds = 8;
+constexpr int kSmallTiles = 128, kMidTiles = 512;
 
 struct Mats {  // moe_matrices on the device side
   void* data;
@@ -172,7 +173,11 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voff, int
 }
 #pragma clang diagnostic pop
 
+// s_waitcnt immediates: at most n vector memory operations outstanding; none,
+// and no LDS operation either.
 constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >> 4) << 14); }
+constexpr int kVm0Lgkm0 = 7 << 4;
+constexpr int kOutOfRange = 0x7FFF0000;  // past every operand tile (below 2^28 bytes)
 
 // 4x4 transpose inside each group of 4 lanes: before, lane l's v[s] is row
 // 4 (l / 32) + s, column l % 32; after, it is row 4 (l / 32) + l % 4, column
@@ -215,7 +220,7 @@ struct Product {
   const uint16_t* aux;  // kSym: symmetric operand added with factor beta
   float alpha, beta, gamma;
 };
-struct Out {  // kOut: matrix row j, column i
+struct Out {  // kOut: matrix row i, column j
   Mats w;
   int rows, cols;
   float keep, add;  // w <- keep w + add O (muon), or w <- add O
@@ -224,31 +229,22 @@ struct Out {  // kOut: matrix row j, column i
 
 enum Epilogue { kSym = 0, kOperand = 1, kOut = 2 };
 
-// kSym: the result is symmetric: tiles on and below the diagonal only;
-//   alpha D + beta aux + gamma I is stored into out_t, and its mirror image.
-// kOperand: alpha D is stored into out_t and out_n.
-// kOut: to the caller's matrices.
-// blockIdx.y: one of two independent products.
-template <int EPI, int WM, int WN, int WR, int WC>
-__global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, Product p1,
-                                                                   Out o, int n, int ra, int rb,
-                                                                   int KS) {
-  constexpr int BA = WR * WM, BB = WC * WN;    // 32-row blocks per tile
-  constexpr int NW = WR * WC;
-  constexpr int kStage = (BA + BB) * 4096;     // K = 32, both parts
-  constexpr int NC = (BA + BB) * 4 / NW;       // 1 KB copies per wave and step
-  static_assert((BA + BB) * 4 % NW == 0, "copies are shared out evenly");
-  static_assert(EPI != kSym || BA == BB, "symmetric results use square tiles");
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kStage];
-
-  const Product& p = blockIdx.y == 0 ? p0 : p1;
+// Tile of this workgroup: matrix, first 32-row blocks of a and b; false past
+// the last tile. Tiles of B x B blocks in eight runs, one an XCD (workgroup b
+// runs on XCD b % 8), matrix by matrix; symmetric results have the tiles on
+// and below the diagonal only.
+struct Tile {
+  int mat, a0, b0;
+};
+template <int EPI, int BA, int BB>
+__device__ __forceinline__ bool find_tile(int n, int ra, int rb, Tile& t) {
   const int ta = (ra + BA - 1) / BA, tb = (rb + BB - 1) / BB;
   const int per_mat = EPI == kSym ? ta * (ta + 1) / 2 : ta * tb;
-  // The tiles in eight runs, one an XCD (workgroup b runs on XCD b % 8).
   const int total = per_mat * n, per = (total + kXcds - 1) / kXcds;
-  const int t = (static_cast<int>(blockIdx.x) % kXcds) * per + static_cast<int>(blockIdx.x) / kXcds;
-  if (t >= total) return;
-  const int mat = t / per_mat, lt = t - mat * per_mat;
+  const int u = (static_cast<int>(blockIdx.x) % kXcds) * per + static_cast<int>(blockIdx.x) / kXcds;
+  if (u >= total) return false;
+  t.mat = u / per_mat;
+  const int lt = u - t.mat * per_mat;
   int ti, tj;
   if constexpr (EPI == kSym) {
     ti = static_cast<int>((sqrtf(8.f * lt + 1.f) - 1.f) * 0.5f);
@@ -259,31 +255,132 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
     ti = lt / tb;
     tj = lt - ti * tb;
   }
+  t.a0 = ti * BA;
+  t.b0 = tj * BB;
+  return true;
+}
+
+// Register groups q0 .. q0 + NQ - 1 of one 32 x 32 block (ib, jb): acc[q][s]
+// of lane l is row 8 (q0 + q) + 4 (l / 32) + s of the a block and row l % 32
+// of the b block. mirror: kSym, a tile off the diagonal.
+template <int EPI, int NQ>
+__device__ __forceinline__ void store_block(const Product& p, const Out& o, int mat, int ra,
+                                            int rb, int ib, int jb, bool mirror, int q0,
+                                            const float (&acc)[NQ][4], int lane) {
+  const int half = lane >> 5, l32 = lane & 31;
+  if constexpr (EPI == kOut) {
+    // Lanes run along the caller's columns: runs of 64 (bf16) or 128 bytes.
+    const int r0 = ib * 32 + 8 * q0 + 4 * half, c = jb * 32 + l32;
+    const int64_t at = mat * o.w.stride + r0 * o.w.ld + c;
+    const bool whole = (ib + 1) * 32 <= o.rows && (jb + 1) * 32 <= o.cols;
+    auto ok = [&](int q, int s) { return whole || (r0 + 8 * q + s < o.rows && c < o.cols); };
+    auto off = [&](int q, int s) { return at + (8 * q + s) * o.w.ld; };
+    float w[NQ][4];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        w[q][s] = o.muon && ok(q, s) ? load_el(o.w, off(q, s)) : 0.f;
+#pragma unroll
+    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float v = fmaf(o.keep, w[q][s], o.add * (acc[q][s] * p.alpha));
+        if (!ok(q, s)) continue;
+        if (o.w.bf16)
+          static_cast<uint16_t*>(o.w.data)[off(q, s)] = f32_to_bf16(v);
+        else
+          static_cast<float*>(o.w.data)[off(q, s)] = v;
+      }
+  } else {
+    // Operand with rows j, its depth i: four adjacent values a lane.
+    auto frag = [&](int q) {
+      return (static_cast<int64_t>(jb) * (2 * ra) + 2 * ib + ((q0 + q) >> 1)) * 1024;
+    };
+    auto slot = [&](int q) { return l32 + 32 * ((q0 + q) & 1); };
+    union Half4 {
+      uint2 w;
+      _Float16 h[4];
+    };
+    Half4 hi[NQ], lo[NQ];
+    const bool add = EPI == kSym && p.aux != nullptr;
+    if (add) {
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const uint16_t* x = p.aux + mat * p.so + frag(q) + slot(q) * 8 + 4 * half;
+        hi[q].w = *reinterpret_cast<const uint2*>(x);
+        lo[q].w = *reinterpret_cast<const uint2*>(x + 512);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float v[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[s] = acc[q][s] * p.alpha;
+      if (add) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const float x = static_cast<float>(hi[q].h[s]) + static_cast<float>(lo[q].h[s]);
+          v[s] = fmaf(p.beta, x, v[s]);
+          if (ib == jb && 8 * (q0 + q) + 4 * half + s == l32) v[s] += p.gamma;
+        }
+      }
+      store_parts(p.out_t + mat * p.so + frag(q), slot(q), 4 * half, v);
+      if (EPI == kOperand || mirror) {
+        // Operand with rows i, its depth j.
+        transpose4(v, lane & 3);
+        const int j0 = 4 * (l32 >> 2), row = 8 * (q0 + q) + 4 * half + (lane & 3);
+        const int64_t fn = (static_cast<int64_t>(ib) * (2 * rb) + 2 * jb + (j0 >> 4)) * 1024;
+        store_parts(p.out_n + mat * p.so + fn, row + 32 * ((j0 >> 3) & 1), j0 & 7, v);
+      }
+    }
+  }
+}
+
+// kSym: the result is symmetric: tiles on and below the diagonal only;
+//   alpha D + beta aux + gamma I is stored into out_t, and its mirror image.
+// kOperand: alpha D is stored into out_t and out_n.
+// kOut: to the caller's matrices (rows i, columns j).
+// blockIdx.y: one of two independent products.
+template <int EPI, int WM, int WN, int WR, int WC>
+__global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, Product p1,
+                                                                   Out o, int n, int ra, int rb,
+                                                                   int KS) {
+  constexpr int BA = WR * WM, BB = WC * WN;    // 32-row blocks per tile
+  constexpr int NW = WR * WC;
+  constexpr int kStage = (BA + BB) * 4096;     // K = 32, both parts
+  constexpr int NC = (BA + BB) * 4 / NW;       // 1 KB copies per wave and step
+  static_assert((BA + BB) * 4 % NW == 0 && BA * 4 % NC == 0, "copies are shared out evenly");
+  static_assert(EPI != kSym || BA == BB, "symmetric results use square tiles");
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * kStage];
+
+  const Product& p = blockIdx.y == 0 ? p0 : p1;
+  Tile t;
+  if (!find_tile<EPI, BA, BB>(n, ra, rb, t)) return;
+  const int mat = t.mat, a0 = t.a0, b0 = t.b0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / WC, wc = wave % WC;
-  const int a0 = ti * BA, b0 = tj * BB;  // first 32-row blocks
 
-  // ---- copies: piece c of a step is 1 KB, four pieces a row block ----
+  // ---- copies: a step is 4 (BA + BB) pieces of 1 KB, four a row block; each
+  // wave copies NC of them, all of one operand ----
   const int row_bytes = KS * 2048;
-  const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(p.a + mat * p.sa + static_cast<int64_t>(a0) * KS * 1024), 0,
-      min(BA, ra - a0) * row_bytes, 0x00020000);
-  const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(p.b + mat * p.sb + static_cast<int64_t>(b0) * KS * 1024), 0,
-      min(BB, rb - b0) * row_bytes, 0x00020000);
-  const unsigned lds0 = (unsigned)(uintptr_t)(lds_u8*)smem;
-  auto copy_step = [&](int kt, int slot) {
+  const bool copy_a = wave * NC < BA * 4;
+  const int piece0 = wave * NC - (copy_a ? 0 : BA * 4);
+  const uint16_t* src = copy_a ? p.a + mat * p.sa + static_cast<int64_t>(a0) * KS * 1024
+                               : p.b + mat * p.sb + static_cast<int64_t>(b0) * KS * 1024;
+  const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)src, 0, (copy_a ? min(BA, ra - a0) : min(BB, rb - b0)) * row_bytes, 0x00020000);
+  int voff[NC];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-      const int c = wave * NC + i;
-      const int blk = c >> 2;
-      const unsigned dst = lds0 + slot * kStage + c * 1024;
-      if (blk < BA)
-        dma16(a_rsrc, blk * row_bytes + (c & 3) * 1024 + lane * 16, kt * 4096, dst);
-      else
-        dma16(b_rsrc, (blk - BA) * row_bytes + (c & 3) * 1024 + lane * 16, kt * 4096, dst);
-    }
+  for (int i = 0; i < NC; ++i)
+    voff[i] = ((piece0 + i) >> 2) * row_bytes + ((piece0 + i) & 3) * 1024 + lane * 16;
+  const unsigned lds_w = (unsigned)(uintptr_t)(lds_u8*)smem + wave * NC * 1024;
+  const int nk = KS / 2;
+  // A copy past the last step is still issued, out of range (it writes zeros
+  // into a finished slot), so the K loop has no branch around it.
+  auto copy = [&](int i, int kt) {
+    dma16(rsrc, kt < nk ? voff[i] : kOutOfRange, kt * 4096, lds_w + (kt & 1) * kStage + i * 1024);
   };
 
   f32x16 acc[WM][WN];
@@ -294,44 +391,56 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  const int nk = KS / 2;
-  copy_step(0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    // This wave's copies of step kt have landed; after the barrier every
-    // wave's have, and every wave is done with the other slot.
-    __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");  // no LDS read moves above the barrier
-    if (kt + 1 < nk) copy_step(kt + 1, (kt + 1) & 1);
-    const unsigned char* s = smem + (kt & 1) * kStage + lane * 16;
+  // Fragments of one slice: WM of a, then WN of b, [hi, lo] each.
+  constexpr int NF = 2 * (WM + WN), NM = 3 * WM * WN;
+  f16x8 fr[2][NF];
+  auto read = [&](int f, int kt, int ks) {
+    const int blk = f / 2 < WM ? wr * WM + f / 2 : BA + wc * WN + f / 2 - WM;
+    fr[ks][f] = *reinterpret_cast<const f16x8*>(smem + (kt & 1) * kStage + blk * 4096 + ks * 2048 +
+                                                (f & 1) * 1024 + lane * 16);
+  };
+  // Products of slice ks in the order lo hi, hi lo, hi hi; `side(x)` for x in
+  // [0, n) is spread between them.
+  auto multiply = [&](int ks, int n, auto side) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      f16x8 fa[WM][2], fb[WN][2];
+    for (int x = 0; x < NM; ++x) {
+      const int q = x / (WM * WN), i = x / WN % WM, j = x % WN;
 #pragma unroll
-      for (int i = 0; i < WM; ++i)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          fa[i][q] = *reinterpret_cast<const f16x8*>(s + (wr * WM + i) * 4096 + ks * 2048 + q * 1024);
-#pragma unroll
-      for (int j = 0; j < WN; ++j)
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-          fb[j][q] = *reinterpret_cast<const f16x8*>(s + (BA + wc * WN + j) * 4096 + ks * 2048 +
-                                                     q * 1024);
-#pragma unroll
-      for (int q = 0; q < 3; ++q)  // lo hi, hi lo, hi hi
-#pragma unroll
-        for (int i = 0; i < WM; ++i)
-#pragma unroll
-          for (int j = 0; j < WN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i][q == 0], fb[j][q == 1],
-                                                               acc[i][j], 0, 0, 0);
+      for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
+      __builtin_amdgcn_sched_barrier(0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + (q == 0)],
+                                                         fr[ks][2 * (WM + j) + (q == 1)],
+                                                         acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
+  };
+#pragma unroll
+  for (int i = 0; i < NC; ++i) copy(i, 0);
+#pragma unroll
+  for (int i = 0; i < NC; ++i) copy(i, 1);
+  __builtin_amdgcn_s_waitcnt(vmcnt_imm(NC));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");  // no LDS read moves above the barrier
+#pragma unroll
+  for (int f = 0; f < NF; ++f) read(f, 0, 0);
+  for (int kt = 0; kt < nk; ++kt) {
+    // First slice, with the reads of the second in between.
+    multiply(0, NF, [&](int f) { read(f, kt, 1); });
+    // This wave's reads of the step's slot are done and its copies of the
+    // next step have landed; after the barrier every wave's. The slot takes
+    // step kt + 2, a whole step before it is needed, while the second slice
+    // is multiplied and the next step's first slice is read.
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    multiply(1, NF + NC, [&](int y) {
+      if (y < NF)
+        read(y, kt + 1, 0);
+      else
+        copy(y - NF, kt + 2);
+    });
   }
 
-  // ---- epilogue: register 4 q + s of lane l is row 8 q + 4 (l / 32) + s of
-  // the a block and row l % 32 of the b block ----
-  const int half = lane >> 5, l32 = lane & 31;
 #pragma unroll
   for (int i = 0; i < WM; ++i) {
     const int ib = a0 + wr * WM + i;
@@ -340,56 +449,228 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
     for (int j = 0; j < WN; ++j) {
       const int jb = b0 + wc * WN + j;
       if (jb >= rb) continue;
+      float v[4][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float v[4];
+      for (int r = 0; r < 16; ++r) v[r / 4][r % 4] = acc[i][j][r];
+      store_block<EPI, 4>(p, o, mat, ra, rb, ib, jb, a0 != b0, 0, v, lane);
+    }
+  }
+}
+
+// ---- products with few tiles ---------------------------------------------------
+// 64 x 64 tiles whose depth is shared out over the 8 waves of a workgroup,
+// slice by slice; each wave reads its fragments straight into registers (two
+// buffers of two slices), so there is no barrier until the waves' sums meet
+// in LDS, and the time is that of a few loads. Also the more exact sum: eight
+// parts instead of one chain.
+template <int EPI>
+__global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Product p1, Out o,
+                                                                 int n, int ra, int rb, int KS) {
+  __shared__ __attribute__((aligned(16))) float part[8][4][4][64][4];  // wave, block, q, lane
+  const Product& p = blockIdx.y == 0 ? p0 : p1;
+  Tile t;
+  if (!find_tile<EPI, 2, 2>(n, ra, rb, t)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Row blocks past the last read the last one again (they are not stored).
+  const uint16_t* src[4];
 #pragma unroll
-        for (int s = 0; s < 4; ++s) v[s] = acc[i][j][4 * q + s] * p.alpha;
-        if constexpr (EPI == kOut) {
-          const int r = jb * 32 + l32, c = ib * 32 + 8 * q + 4 * half;
-          if (r >= o.rows) continue;
-          const int64_t at = mat * o.w.stride + r * o.w.ld + c;
+  for (int i = 0; i < 2; ++i) {
+    src[i] = p.a + t.mat * p.sa + static_cast<int64_t>(min(t.a0 + i, ra - 1)) * KS * 1024 + lane * 8;
+    src[2 + i] = p.b + t.mat * p.sb + static_cast<int64_t>(min(t.b0 + i, rb - 1)) * KS * 1024 + lane * 8;
+  }
+  f32x16 acc[2][2];
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            if (c + s >= o.cols) continue;
-            float w = o.add * v[s];
-            if (o.muon) w = fmaf(o.keep, load_el(o.w, at + s), w);
-            if (o.w.bf16)
-              static_cast<uint16_t*>(o.w.data)[at + s] = f32_to_bf16(w);
-            else
-              static_cast<float*>(o.w.data)[at + s] = w;
-          }
-        } else {
-          // Operand with rows j: depth KT slices (that of i's blocks).
-          const int64_t ft = (static_cast<int64_t>(jb) * (2 * ra) + 2 * ib + (q >> 1)) * 1024;
-          const int lt2 = l32 + 32 * (q & 1);
-          if constexpr (EPI == kSym) {
-            if (p.aux != nullptr) {
-              const uint16_t* x = p.aux + mat * p.so + ft + lt2 * 8 + 4 * half;
-              union {
-                uint2 w;
-                _Float16 h[4];
-              } hi, lo;
-              hi.w = *reinterpret_cast<const uint2*>(x);
-              lo.w = *reinterpret_cast<const uint2*>(x + 512);
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
-              for (int s = 0; s < 4; ++s) {
-                const float av = static_cast<float>(hi.h[s]) + static_cast<float>(lo.h[s]);
-                v[s] = fmaf(p.beta, av, v[s]);
-                if (ib == jb && 8 * q + 4 * half + s == l32) v[s] += p.gamma;
-              }
-            }
-          }
-          store_parts(p.out_t + mat * p.so + ft, lt2, 4 * half, v);
-          if (EPI == kOperand || ti != tj) {
-            transpose4(v, lane & 3);
-            const int j0 = 4 * (l32 >> 2), row = 8 * q + 4 * half + (lane & 3);
-            const int64_t fn = (static_cast<int64_t>(ib) * (2 * rb) + 2 * jb + (j0 >> 4)) * 1024;
-            store_parts(p.out_n + mat * p.so + fn, row + 32 * ((j0 >> 3) & 1), j0 & 7, v);
-          }
-        }
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  f16x8 fr[2][2][4][2];  // buffer, slice, operand block, part
+  auto load = [&](int buf, int ks) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (ks + 8 * u < KS) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            fr[buf][u][b][q] =
+                *reinterpret_cast<const f16x8*>(src[b] + static_cast<int64_t>(ks + 8 * u) * 1024 + q * 512);
+      }
+  };
+  auto multiply = [&](int buf, int ks) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (ks + 8 * u < KS) {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                  fr[buf][u][i][q == 0], fr[buf][u][2 + j][q == 1], acc[i][j], 0, 0, 0);
+      }
+  };
+  load(0, wave);
+  load(1, wave + 16);
+  for (int ks = wave; ks < KS; ks += 32) {
+    multiply(0, ks);
+    load(0, ks + 32);
+    multiply(1, ks + 16);
+    load(1, ks + 48);
+  }
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(part[wave][b][q][lane]) =
+          make_float4(acc[b / 2][b % 2][4 * q], acc[b / 2][b % 2][4 * q + 1],
+                      acc[b / 2][b % 2][4 * q + 2], acc[b / 2][b % 2][4 * q + 3]);
+  __syncthreads();
+  // Wave w sums and stores half of block w / 2.
+  const int b = wave / 2, q0 = 2 * (wave & 1);
+  const int ib = t.a0 + b / 2, jb = t.b0 + b % 2;
+  if (ib >= ra || jb >= rb) return;
+  float v[2][4];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      v[q][s] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[q][s] += part[w][b][q0 + q][lane][s];
+    }
+  store_block<EPI, 2>(p, o, t.mat, ra, rb, ib, jb, t.a0 != t.b0, q0, v, lane);
+}
+
+// ---- short sides up to 128: a segment after its Gram product in one launch ------
+// Every workgroup holds A and P of its matrix in LDS (MB 32-row blocks, at
+// most 64 KB each), takes the segment's steps (1 or 2) there, and multiplies
+// its share of X: group g of XB 32-row blocks of X^T, g = blockIdx.x,
+// blockIdx.x + gridDim.x, ... The steps are repeated by every workgroup of a
+// matrix: they take a few microseconds, a launch each would take more. A wave
+// has one 32 x 32 block: of the m x m products those on and below the
+// diagonal (10 of 16 waves for MB = 4, at most 3 on a SIMD).
+// SWAP: the result's rows are those of Q (kOut of a wide matrix).
+template <int MB, int EPI, bool SWAP>
+__global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk) {
+  constexpr int KS = 2 * MB, MP = MB == 3 ? 4 : MB, XB = 16 / MP;
+  constexpr int kOp = MB * KS * 1024;  // values of an operand
+  __shared__ __attribute__((aligned(16))) uint16_t bufs[2][kOp];
+  uint16_t *ba = bufs[0], *bp = bufs[1];
+  const int mat = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  auto frag = [&](const uint16_t* op, int rb, int ks, int part) {
+    return *reinterpret_cast<const f16x8*>(op + ((rb * KS + ks) * 2 + part) * 512 + lane * 8);
+  };
+  f32x16 acc;
+  // acc += (hi + lo of a) (hi + lo of b)
+  auto mma = [&](const f16x8& ah, const f16x8& al, const f16x8& bh, const f16x8& bl) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh, acc, 0, 0, 0);
+  };
+  auto zero = [&]() {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+  };
+  // A block of X^T.
+  f16x8 x[KS][2];
+  auto load_x = [&](int xb) {
+    const uint16_t* src = p.a + mat * p.sa + static_cast<int64_t>(xb) * (KS * 1024) + lane * 8;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        x[ks][q] = *reinterpret_cast<const f16x8*>(src + (ks * 2 + q) * 512);
+  };
+  for (int i = tid; i < kOp / 8; i += 1024)
+    reinterpret_cast<uint4*>(ba)[i] = reinterpret_cast<const uint4*>(p.b + mat * p.sb)[i];
+  __syncthreads();
+
+  // Block (ib, jb), jb <= ib, of the m x m results: wave 0 (0, 0), 1 (1, 0),
+  // 2 (1, 1), 3 (2, 0), ...
+  const int ib = wave >= 6 ? 3 : wave >= 3 ? 2 : wave >= 1 ? 1 : 0, jb = wave - ib * (ib + 1) / 2;
+  const bool mine = wave < MB * (MB + 1) / 2;
+  auto product = [&](const uint16_t* a, const uint16_t* b) {
+    zero();
+    if (!mine) return;
+#pragma unroll 4
+    for (int ks = 0; ks < KS; ++ks)
+      mma(frag(a, ib, ks, 0), frag(a, ib, ks, 1), frag(b, jb, ks, 0), frag(b, jb, ks, 1));
+  };
+  // Values of register group q, rows jb and depth ib of the operand's layout.
+  auto place = [&](int q) {
+    return ((jb * KS + 2 * ib + (q >> 1)) * 2) * 512 + (l32 + 32 * (q & 1)) * 8 + 4 * half;
+  };
+  auto polynomial = [&](const uint16_t* a) {  // acc <- a I + b A + c A^2, as kScaleP holds it
+    if (!mine) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const _Float16* h = reinterpret_cast<const _Float16*>(a + place(q));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const float av = static_cast<float>(h[s]) + static_cast<float>(h[512 + s]);
+        float v = fmaf(kB * kScaleP / kScaleA, av,
+                       acc[4 * q + s] * (kC * kScaleP / (kScaleA * kScaleA)));
+        if (ib == jb && 8 * q + 4 * half + s == l32) v += kA * kScaleP;
+        acc[4 * q + s] = v;
       }
     }
+  };
+  auto store = [&](uint16_t* op, float alpha) {  // and the mirror image
+    if (!mine) return;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[s] = acc[4 * q + s] * alpha;
+      store_parts(op + place(q), 0, 0, v);
+      if (ib != jb) {
+        transpose4(v, lane & 3);
+        const int j0 = 4 * (l32 >> 2), row = 8 * q + 4 * half + (lane & 3);
+        store_parts(op + ((ib * KS + 2 * jb + (j0 >> 4)) * 2) * 512, row + 32 * ((j0 >> 3) & 1),
+                    j0 & 7, v);
+      }
+    }
+  };
+  // P = f(A, A^2); with two steps then U = A P and A_2 = U P, each over its
+  // first factor, P_2 over A_2, and Q = P_2 P over P. One copy of the code:
+  // it runs once a launch, so its size is time (fetching instructions).
+#pragma unroll 1
+  for (int ph = 0; ph < (steps == 2 ? 5 : 1); ++ph) {
+    const bool poly = ph == 0 || ph == 3;
+    product(ba, poly ? ba : bp);
+    if (poly) polynomial(ba);
+    __syncthreads();
+    store(ph == 0 || ph == 4 ? bp : ba, poly ? 1.f : 1.f / kScaleP);
+    __syncthreads();
+  }
+
+  const int qb = wave % MP;
+  int xb = blockIdx.x * XB + wave / MP;
+  if (qb >= MB) return;
+#pragma unroll 1
+  for (; xb < rk; xb += gridDim.x * XB) {
+    load_x(xb);
+    zero();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      __builtin_amdgcn_sched_barrier(0);  // not all of Q's fragments at once
+      const f16x8 qh = frag(bp, qb, ks, 0), ql = frag(bp, qb, ks, 1);
+      if constexpr (SWAP)
+        mma(qh, ql, x[ks][0], x[ks][1]);
+      else
+        mma(x[ks][0], x[ks][1], qh, ql);
+    }
+    float v[4][4];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) v[r / 4][r % 4] = acc[r];
+    store_block<EPI, 4>(p, o, mat, SWAP ? MB : rk, SWAP ? rk : MB, SWAP ? qb : xb, SWAP ? xb : qb,
+                        false, 0, v, lane);
   }
 }
 
@@ -418,32 +699,69 @@ Space space(int n, int rows, int cols) {
 
 // Most steps of the first segment and of the later ones. Relative Frobenius
 // error of fp32 results against 64 bits (gradients of 1.5 m tokens; plain
-// torch fp32 / steps one by one / 2 + 2 + 1 / 3 + 2, in 1e-6):
-//   8 x 128 x 512    1.7 / 1.2 / 2.4 / 2.6     4 x 512 x 512     2.1 / 1.8 / 3.4 / 5.2
-//   4 x 256 x 1024   2.1 / 1.4 / 3.4 / 2.4     4 x 1024 x 1024   2.7 / 2.3 / 3.4 / 7.7
-//   2 x 1024 x 4096  3.5 / 2.6 / 4.1 / 5.3     1 x 2048 x 2048   3.5 / 2.9 / 3.4 / 9.4
-// A bf16 result rounds by 1.7e-3, so it takes the fewest operations. An fp32
-// result keeps plain fp32's accuracy: single steps, and pairs from m = 1024
-// on. In a Muon step with fp32 weights the update is a small part of the
-// weight, and with it the error: pairs.
+// torch fp32 / single steps / 2 + 2 + 1 / 3 + 2, in 1e-6):
+//   8 x 128 x 512    1.7 / 0.9 / 2.0 /  -      4 x 512 x 512     2.1 / 0.9 /  -  /  -
+//   8 x 128 x 128    1.3 / 1.0 / 2.8 /  -      4 x 1024 x 1024   2.7 / 2.3 / 3.4 / 7.7
+//   2 x 1024 x 4096  3.5 / 2.6 / 1.9 / 5.3     1 x 2048 x 2048   3.5 / 2.9 / 3.4 / 9.4
+// A bf16 result rounds by 1.7e-3, so it takes the fewest operations (pairs up
+// to m = 128, where a launch holds two steps). An fp32 result keeps plain
+// fp32's accuracy: single steps, and pairs from m = 1024 on. In a Muon step
+// with fp32 weights the update is a small part of the weight, and with it the
+// error: pairs.
 struct Segments {
   int first, later;
 };
 Segments segment_rule(bool bf16_out, bool muon, int m) {
-  if (bf16_out) return {3, 2};
-  if (muon || m >= 1024) return {2, 2};
-  return {1, 1};
+  if (bf16_out) return {m <= 128 ? 2 : 3, 2};
+  return muon || m >= 1024 ? Segments{2, 2} : Segments{1, 1};
 }
 
 template <int EPI>
+int64_t tile_count(int B, int n, int ra, int rb) {
+  const int64_t ta = (ra + B - 1) / B, tb = (rb + B - 1) / B;
+  return n * (EPI == kSym ? ta * (ta + 1) / 2 : ta * tb);
+}
+
+// Tile shapes: 64 x 64 with the depth split over the waves, 128 x 128 (two
+// workgroups a CU), 256 x 256 (one). Measured, whole calls (small / 128 / 256):
+// 2 x 1024^2 (72 tiles of 128) 384 / 455 / - us; 2048^2 (136) 1052 / 913 / -;
+// 16 x 1024 x 2048 (576) 2410 / 2090 / 2047; 4096 x 14336 (528) 9998 / 8003 /
+// 7640. So: the small tiles up to half a 128-tile a CU, 128-tiles while one
+// round holds them all, then 256-tiles unless they would compute more than
+// 5/4 of the 128-tiles' area (sides just past a multiple of 256). Small tiles
+// too where 128-tiles would compute twice their area (256 x 64 x 256: 134 us,
+// 157 with 128-tiles).
+template <int EPI>
 hipError_t launch_product(const Product& p0, const Product* p1, const Out& o, int n, int ra,
                           int rb, int KS, hipStream_t s) {
-  constexpr int B = 4;
-  const int ta = (ra + B - 1) / B, tb = (rb + B - 1) / B;
-  const int64_t total = static_cast<int64_t>(n) * (EPI == kSym ? ta * (ta + 1) / 2 : ta * tb);
-  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
-  orth_product_kernel<EPI, 2, 2, 2, 2><<<dim3(static_cast<unsigned>(grid), p1 ? 2 : 1), 256, 0, s>>>(
-      p0, p1 ? *p1 : p0, o, n, ra, rb, KS);
+  auto grid = [&](int B) {
+    const int64_t t = (tile_count<EPI>(B, n, ra, rb) + kXcds - 1) / kXcds * kXcds;
+    return dim3(static_cast<unsigned>(t), p1 ? 2 : 1);
+  };
+  const Product& q = p1 ? *p1 : p0;
+  const int64_t t64 = tile_count<EPI>(2, n, ra, rb), t128 = tile_count<EPI>(4, n, ra, rb);
+  const int64_t t256 = tile_count<EPI>(8, n, ra, rb);
+  if (t128 <= kSmallTiles || t64 <= 2 * t128)
+    orth_product_small_kernel<EPI><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
+  else if (t128 <= kMidTiles || 16 * t256 > 5 * t128)
+    orth_product_kernel<EPI, 2, 2, 2, 2><<<grid(4), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
+  else
+    orth_product_kernel<EPI, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
+  return hipGetLastError();
+}
+
+// p.a: X^T, p.b: A (after the Gram product).
+template <int EPI, bool SWAP>
+hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm, int rk,
+                        hipStream_t s) {
+  const int xb = rm == 1 ? 16 : rm == 2 ? 8 : 4;
+  const dim3 grid(std::min((rk + xb - 1) / xb, std::max(1, 256 / n)), n);
+  switch (rm) {
+    case 1: orth_steps_kernel<1, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
+    case 2: orth_steps_kernel<2, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
+    case 3: orth_steps_kernel<3, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
+    default: orth_steps_kernel<4, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
+  }
   return hipGetLastError();
 }
 
@@ -452,7 +770,7 @@ hipError_t launch_product(const Product& p0, const Product* p1, const Out& o, in
 size_t orth_ws_bytes(int n, int rows, int cols) { return space(n, rows, cols).bytes; }
 
 int64_t orth_tiles(int n, int rows, int cols) {
-  const int64_t m = (std::min(rows, cols) + 127) / 128, k = (std::max(rows, cols) + 127) / 128;
+  const int64_t m = (std::min(rows, cols) + 63) / 64, k = (std::max(rows, cols) + 63) / 64;
   return n * m * k;
 }
 
@@ -489,6 +807,8 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
   if (e != hipSuccess) return e;
 
   const Out none{};
+  const Out out{wm, rows, cols, mom ? 1.f - d.lr * d.weight_decay : 0.f,
+                mom ? -d.lr * d.scale : 1.f, mom != nullptr};
   // Symmetric m x m product: out = so (a b / (sa sb) + beta aux + gamma I).
   auto sym_args = [&](const uint16_t* a, const uint16_t* b, float sa, float sb, uint16_t* out,
                       float so, float alpha) {
@@ -509,6 +829,19 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     left -= L;
     Product gram{X, X, sp.x, sp.x, A, A, sp.mm, nullptr, kScaleA / (kScaleX * kScaleX), 0.f, 0.f};
     if ((e = launch_product<kSym>(gram, nullptr, none, n, rm, rm, 2 * rk, s)) != hipSuccess) return e;
+    if (rm <= 4) {  // the rest of the segment in one launch
+      Product x{XT, A, sp.x, sp.mm, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
+      if (left > 0) {
+        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, s);
+        std::swap(XT, XT2);
+      } else {
+        x.alpha = 1.f / (kScaleP * kScaleX);
+        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, s)
+                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, s);
+      }
+      if (e != hipSuccess) return e;
+      continue;
+    }
     uint16_t *q = Q, *q2 = Q2;
     if ((e = poly(q)) != hipSuccess) return e;
     const uint16_t* pl = q;  // the last P
@@ -528,20 +861,19 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
       if ((e = sym(sym_args(pl, q, kScaleP, kScaleP, q2, kScaleP, 1.f))) != hipSuccess) return e;
       q = q2;
     }
-    // X <- Q X: rows i and j of the result such that the caller's rows are j.
-    const uint16_t *a = tall ? q : XT, *b = tall ? XT : q;
-    Product x{a, b, tall ? sp.mm : sp.x, tall ? sp.x : sp.mm, tall ? XT2 : X, tall ? X : XT2,
-              sp.x, nullptr, 0.f, 0.f, 0.f};
-    const int ra = tall ? rm : rk, rb = tall ? rk : rm;
+    // X <- Q X. An operand for the next segment takes either orientation; the
+    // caller's matrix has its rows at i and its columns at j.
+    Product x{XT, q, sp.x, sp.mm, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
     if (left > 0) {
-      x.alpha = 1.f / kScaleP;
-      e = launch_product<kOperand>(x, nullptr, none, n, ra, rb, 2 * rm, s);
+      e = launch_product<kOperand>(x, nullptr, none, n, rk, rm, 2 * rm, s);
       std::swap(XT, XT2);
     } else {
       x.alpha = 1.f / (kScaleP * kScaleX);
-      const Out o{wm, rows, cols, mom ? 1.f - d.lr * d.weight_decay : 0.f,
-                  mom ? -d.lr * d.scale : 1.f, mom != nullptr};
-      e = launch_product<kOut>(x, nullptr, o, n, ra, rb, 2 * rm, s);
+      if (!tall) {
+        std::swap(x.a, x.b);
+        std::swap(x.sa, x.sb);
+      }
+      e = launch_product<kOut>(x, nullptr, out, n, tall ? rk : rm, tall ? rm : rk, 2 * rm, s);
     }
     if (e != hipSuccess) return e;
   }
