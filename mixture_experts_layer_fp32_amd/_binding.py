@@ -851,26 +851,33 @@ def moe_expert_ffn_ptrs(d: moe_desc, n_experts, inter, cap_rows, x_perm, offsets
 _ACT_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _same_device(named) -> torch.device:
-    """The one GPU all given tensors are on."""
-    dev = None
-    for name, t in named:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: must be a GPU tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, the other tensors on {dev}")
-        dev = t.device
-    return dev
+def _device_of(t, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
+    return t.device
+
+
+def _ptr_on(dev: torch.device, t, name: str, dtype: torch.dtype, shape=None):
+    """_ptr for a call that runs on dev: the same refusals, and tensors of
+    other devices. (These calls are short next to their launches: what is
+    checked is checked in the fewest steps.)"""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.device == dev and t.dtype == dtype
+            and t.is_contiguous() and (shape is None or t.shape == shape)):
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, other tensors on {dev}")
+        return _ptr(t, name, dtype, shape)  # raises, naming what is wrong
+    return t.data_ptr()
 
 
 def _act_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype not in _ACT_DTYPES:
+    code = _ACT_DTYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name}: dtype {t.dtype}, expected float32 or bfloat16")
-    return _ACT_DTYPES[t.dtype]
+    return code
 
 
 def _rows(t, name: str):
@@ -879,26 +886,39 @@ def _rows(t, name: str):
     return t.shape
 
 
+def _launch(name: str, dev: torch.device, args, stream):
+    """Call entry point `name` with dev current, on `stream` (None: torch's
+    current stream of dev)."""
+    fn = getattr(load_library(), name)
+    if dev.index == torch._C._cuda_getDevice():
+        status = fn(*args, _raw_stream(dev.index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _stream(stream))
+    if status != MOE_OK:
+        _check(name, status)
+
+
+def _raw_stream(index: int) -> int:
+    # torch.cuda.current_stream(index).cuda_stream without the Stream object.
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def moe_layer_norm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
     """x, y [rows, D] fp32 or bf16; gamma, beta [D] fp32 or None; mean, rstd
     [rows] fp32 or None. Runs on x's device."""
-    lib = load_library()
-    rows, D = _rows(x, "x")
-    f32 = torch.float32
-    dev = _same_device((("x", x), ("gamma", gamma), ("beta", beta), ("y", y), ("mean", mean),
-                        ("rstd", rstd)))
-    args = (
-        int(rows), int(D), _act_code(x, "x"),
-        _ptr(x, "x"),
-        _ptr(gamma, "gamma", f32, (D,)),
-        _ptr(beta, "beta", f32, (D,)),
+    rows, D = shape = _rows(x, "x")
+    dev, dt, f32 = _device_of(x, "x"), x.dtype, torch.float32
+    _launch("moe_layer_norm", dev, (
+        rows, D, _act_code(x, "x"),
+        _ptr_on(dev, x, "x", dt),
+        _ptr_on(dev, gamma, "gamma", f32, (D,)),
+        _ptr_on(dev, beta, "beta", f32, (D,)),
         float(eps),
-        _ptr(y, "y", x.dtype, (rows, D)),
-        _ptr(mean, "mean", f32, (rows,)),
-        _ptr(rstd, "rstd", f32, (rows,)),
-    )
-    with torch.cuda.device(dev):
-        _check("moe_layer_norm", lib.moe_layer_norm(*args, _stream(stream)))
+        _ptr_on(dev, y, "y", dt, shape),
+        _ptr_on(dev, mean, "mean", f32, (rows,)),
+        _ptr_on(dev, rstd, "rstd", f32, (rows,)),
+    ), stream)
 
 
 def moe_layer_norm_backward_workspace_size(rows: int, D: int) -> int:
@@ -908,28 +928,22 @@ def moe_layer_norm_backward_workspace_size(rows: int, D: int) -> int:
 def moe_layer_norm_backward(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, ws, stream=None):
     """Shapes and dtypes as in moe_layer_norm (dy, dres, dx like x); dres,
     dgamma and dbeta may be None, and ws with both of the last two."""
-    lib = load_library()
-    rows, D = _rows(x, "x")
-    f32 = torch.float32
-    dev = _same_device((("x", x), ("dy", dy), ("gamma", gamma), ("mean", mean), ("rstd", rstd),
-                        ("dres", dres), ("dx", dx), ("dgamma", dgamma), ("dbeta", dbeta),
-                        ("ws", ws)))
-    args = (
-        int(rows), int(D), _act_code(x, "x"),
-        _ptr(x, "x"),
-        _ptr(dy, "dy", x.dtype, (rows, D)),
-        _ptr(gamma, "gamma", f32, (D,)),
-        _ptr(mean, "mean", f32, (rows,)),
-        _ptr(rstd, "rstd", f32, (rows,)),
-        _ptr(dres, "dres", x.dtype, (rows, D)),
-        _ptr(dx, "dx", x.dtype, (rows, D)),
-        _ptr(dgamma, "dgamma", f32, (D,)),
-        _ptr(dbeta, "dbeta", f32, (D,)),
-        _ptr(ws, "ws", torch.uint8),
+    rows, D = shape = _rows(x, "x")
+    dev, dt, f32 = _device_of(x, "x"), x.dtype, torch.float32
+    _launch("moe_layer_norm_backward", dev, (
+        rows, D, _act_code(x, "x"),
+        _ptr_on(dev, x, "x", dt),
+        _ptr_on(dev, dy, "dy", dt, shape),
+        _ptr_on(dev, gamma, "gamma", f32, (D,)),
+        _ptr_on(dev, mean, "mean", f32, (rows,)),
+        _ptr_on(dev, rstd, "rstd", f32, (rows,)),
+        _ptr_on(dev, dres, "dres", dt, shape),
+        _ptr_on(dev, dx, "dx", dt, shape),
+        _ptr_on(dev, dgamma, "dgamma", f32, (D,)),
+        _ptr_on(dev, dbeta, "dbeta", f32, (D,)),
+        _ptr_on(dev, ws, "ws", torch.uint8),
         ws.numel() if ws is not None else 0,
-    )
-    with torch.cuda.device(dev):
-        _check("moe_layer_norm_backward", lib.moe_layer_norm_backward(*args, _stream(stream)))
+    ), stream)
 
 
 # ---------------------------------------------------------------------------
@@ -938,20 +952,25 @@ def moe_layer_norm_backward(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, w
 # adjacent in memory; rows and matrices may be spaced (views of the gate or up
 # columns of a gate_up tensor).
 # ---------------------------------------------------------------------------
-def _matrices(t, name: str, shape=None):
-    """(moe_matrices, (n, rows, cols)) of a tensor of matrices."""
+def _matrices(dev: torch.device, t, name: str, shape=None):
+    """moe_matrices of a tensor of matrices on dev."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
         raise ValueError(f"{name}: expected [n, rows, cols] or [rows, cols]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on {dev}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    v = t.detach() if t.dim() == 3 else t.detach().unsqueeze(0)
-    n, rows, cols = v.shape
-    if cols > 1 and v.stride(2) != 1:
+    rows, cols = t.shape[-2:]
+    if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the columns of a row must be adjacent in memory")
     # The stride of a dimension of size 1 means nothing.
-    ld = v.stride(1) if rows > 1 else cols
-    stride = v.stride(0) if n > 1 else (rows - 1) * ld + cols
-    return moe_matrices(v.data_ptr(), _act_code(t, name), ld, stride), (n, rows, cols)
+    ld = t.stride(-2) if rows > 1 else cols
+    stride = t.stride(0) if t.dim() == 3 and t.shape[0] > 1 else rows * ld
+    return moe_matrices(t.data_ptr(), _act_code(t, name), ld, stride)
+
+
+def _sizes(t):
+    return t.shape if t.dim() == 3 else (1, *t.shape)
 
 
 def moe_orthogonalize_workspace_size(n: int, rows: int, cols: int, steps: int = 5) -> int:
@@ -962,28 +981,22 @@ def moe_orthogonalize_workspace_size(n: int, rows: int, cols: int, steps: int = 
 def moe_orthogonalize(g, out, ws, steps=5, eps=1e-7, stream=None):
     """out <- the Newton-Schulz orthogonalisation of each matrix of g (fp32 or
     bf16 each; out may be g)."""
-    lib = load_library()
-    dev = _same_device((("g", g), ("out", out), ("ws", ws)))
-    mg, (n, rows, cols) = _matrices(g, "g")
-    mo, _ = _matrices(out, "out", g.shape)
-    args = (n, rows, cols, ctypes.byref(mg), int(steps), float(eps), ctypes.byref(mo),
-            _ptr(ws, "ws", torch.uint8), ws.numel() if ws is not None else 0)
-    with torch.cuda.device(dev):
-        _check("moe_orthogonalize", lib.moe_orthogonalize(*args, _stream(stream)))
+    dev = _device_of(g, "g")
+    mg, mo = _matrices(dev, g, "g"), _matrices(dev, out, "out", g.shape)
+    _launch("moe_orthogonalize", dev, (
+        *_sizes(g), ctypes.byref(mg), int(steps), float(eps), ctypes.byref(mo),
+        _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0), stream)
 
 
 def moe_muon_update(g, momentum, w, ws, lr, mu=0.95, weight_decay=0.0, scale=1.0, nesterov=True,
                     steps=5, eps=1e-7, stream=None):
     """One Muon step on the matrices of w (fp32 or bf16), in place, from the
     gradients g (fp32 or bf16) and the fp32 momentum, updated too."""
-    lib = load_library()
-    dev = _same_device((("g", g), ("momentum", momentum), ("w", w), ("ws", ws)))
-    mg, (n, rows, cols) = _matrices(g, "g")
-    mm, _ = _matrices(momentum, "momentum", g.shape)
-    mw, _ = _matrices(w, "w", g.shape)
+    dev = _device_of(g, "g")
+    mats = [_matrices(dev, t, name, g.shape)
+            for t, name in ((g, "g"), (momentum, "momentum"), (w, "w"))]
     d = moe_muon_desc(float(lr), float(mu), float(weight_decay), float(scale), float(eps),
                       int(bool(nesterov)), int(steps))
-    args = (n, rows, cols, ctypes.byref(d), ctypes.byref(mg), ctypes.byref(mm), ctypes.byref(mw),
-            _ptr(ws, "ws", torch.uint8), ws.numel() if ws is not None else 0)
-    with torch.cuda.device(dev):
-        _check("moe_muon_update", lib.moe_muon_update(*args, _stream(stream)))
+    _launch("moe_muon_update", dev, (
+        *_sizes(g), ctypes.byref(d), *(ctypes.byref(m) for m in mats),
+        _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0), stream)

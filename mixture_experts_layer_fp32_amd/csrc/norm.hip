@@ -5,9 +5,16 @@
 //   dgamma = sum_rows dy h,  dbeta = sum_rows dy
 //
 // Both passes are bound by memory: a few operations per value. A row belongs
-// to a group of G threads (one wave, or one workgroup of G threads) that hold
-// it in registers, so x (and dy) are read once; gamma and beta, and in the
-// backward the column sums, stay in registers over all rows of the group.
+// to a group of G threads (one wave, or one workgroup of G threads), 16 values
+// a thread, that hold it in registers, so x (and dy) are read once; gamma and
+// beta, and in the backward the column sums, stay in registers over all rows
+// of the group. Measured (a copy of 1 GiB moves 5.1 TB/s): forward 8192 x 4096
+// bf16 27 us, 4.9 TB/s; backward with the residual 16384 x 2048 bf16 56 us,
+// 4.8 TB/s, 4096 x 7168 fp32 93 us, 5.0 TB/s. What it took: the row's two sums
+// across the lanes in registers and one barrier a row (44 -> 34 us forward),
+// non-temporal stores (34 -> 32; backward 64 -> 57), the hardware's bf16
+// conversion (32 -> 27). Tried and slower: two rows in flight ahead,
+// non-temporal loads of bf16 rows, fewer or one row per workgroup.
 #include <algorithm>
 
 #include "moe_internal.h"
@@ -20,6 +27,8 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 template <typename T>
 struct Vec;
@@ -49,10 +58,12 @@ struct Vec<uint16_t> {  // bf16
     }
   }
   static __device__ __forceinline__ u32x4 pack(const float (&f)[N]) {
+    // v_cvt_pk_bf16_f32: two values an instruction, to nearest even, NaN kept.
     u32x4 r;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      r[i] = f32_to_bf16(f[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(f[2 * i + 1])) << 16);
+      r[i] = __builtin_bit_cast(
+          uint32_t, __builtin_convertvector(f32x2{f[2 * i], f[2 * i + 1]}, bf16x2));
     return r;
   }
   static __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
@@ -80,45 +91,140 @@ __device__ __forceinline__ void store_vec(T* row, int v, int nfull, int D,
                                           const float (&f)[Vec<T>::N]) {
   constexpr int N = Vec<T>::N;
   if (v < nfull) {
-    *reinterpret_cast<typename Vec<T>::raw_a*>(row + static_cast<int64_t>(v) * N) =
-        Vec<T>::pack(f);
+    __builtin_nontemporal_store(Vec<T>::pack(f), reinterpret_cast<typename Vec<T>::raw_a*>(row + static_cast<int64_t>(v) * N));
   } else if (v == nfull) {
 #pragma unroll
     for (int e = 0; e < N; ++e)
       if (e < D - nfull * N) Vec<T>::store1(row + nfull * N + e, f[e]);
   }
 }
-// N fp32 parameters of vector v, `pad` where there are none.
+// N fp32 parameters of vector v, `pad` without any (zeros past D).
 template <int N>
 __device__ __forceinline__ void load_param(const float* p, int v, int D, float pad,
                                            float (&f)[N]) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) f[e] = p != nullptr && v * N + e < D ? p[v * N + e] : pad;
+  for (int i = 0; i < N / 4; ++i) {
+    float q[4] = {pad, pad, pad, pad};
+    if (p != nullptr) Vec<float>::unpack(load_vec(p, v * (N / 4) + i, D / 4, D), q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[4 * i + e] = q[e];
+  }
 }
 
-// Sums of NS values over the group's G threads, in every thread. red holds
-// 2 x NS x (G / 64) floats; calls alternate `slot`, so one barrier each is
-// enough: a thread that writes a slot again has passed the barrier of the
-// call in between, and with it every read of the slot's last use.
-template <int G, int NS>
-__device__ __forceinline__ void group_sum(float (&s)[NS], float* red, int& slot) {
+// Sum over the wave, in every lane: two quad permutes and two mirrors leave
+// each row of 16 lanes with its sum, four lane reads add the rows. (Shuffles
+// through LDS cost about 100 cycles each of a chain of six.)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), CTRL, 0xF, 0xF, false),
+                          __builtin_amdgcn_mov_dpp(__double2loint(v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float lane_value(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+__device__ __forceinline__ double lane_value(double v, int l) {
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), l),
+                          __builtin_amdgcn_readlane(__double2loint(v), l));
+}
+template <typename S>
+__device__ __forceinline__ S wave_sum(S v) {
+  v += dpp<0xB1>(v);   // quad_perm 1 0 3 2
+  v += dpp<0x4E>(v);   // quad_perm 2 3 0 1
+  v += dpp<0x141>(v);  // row_half_mirror
+  v += dpp<0x140>(v);  // row_mirror
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// A buffer for what a group's waves tell each other. Calls alternate `slot`,
+// so one barrier a call is enough: a wave that writes a slot again has passed
+// the barrier of the call in between, and with it every read of the slot's
+// last use.
+template <int G>
+struct Exchange {
+  double s[2][G / 64];
+  float f[2][2][G / 64];
+};
+
+// mean and 1 / sqrt(variance + eps) of the group's values f (places that hold
+// none are zeros; cnt of the thread's, n_wave of the wave's are values). Each
+// wave takes its own mean and centred sum of squares; the waves' are joined
+// by M2 = sum_w (M2_w + n_w (mean_w - mean)^2). The sums of values are added
+// across threads in fp64, so that a mean near zero keeps its digits.
+template <int G, int NV, int N>
+__device__ __forceinline__ void row_stats(const float (&f)[NV][N], const int (&cnt)[NV],
+                                          float n_wave, int D, float eps, Exchange<G>& ex,
+                                          int& slot, float& mean, float& rstd) {
+  float part[NV];
 #pragma unroll
-  for (int i = 0; i < NS; ++i)
+  for (int i = 0; i < NV; ++i) {
+    float q[N / 2];
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) s[i] += __shfl_xor(s[i], off, 64);
+    for (int e = 0; e < N / 2; ++e) q[e] = f[i][e] + f[i][e + N / 2];
+#pragma unroll
+    for (int h = N / 4; h > 0; h /= 2)
+#pragma unroll
+      for (int e = 0; e < h; ++e) q[e] += q[e + h];
+    part[i] = q[0];
+  }
+  double s = part[0];
+#pragma unroll
+  for (int i = 1; i < NV; ++i) s += part[i];
+  s = wave_sum(s);
+  const float mw = n_wave > 0.f ? static_cast<float>(s / n_wave) : 0.f;
+  float m2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < N; ++e)
+      if (e < cnt[i]) m2 = fmaf(f[i][e] - mw, f[i][e] - mw, m2);
+  m2 = wave_sum(m2);
   if constexpr (G > 64) {
     constexpr int W = G / 64;
-    float* r = red + slot * NS * W;
     if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int i = 0; i < NS; ++i) r[i * W + (threadIdx.x >> 6)] = s[i];
+      ex.s[slot][threadIdx.x >> 6] = s;
+      ex.f[slot][0][threadIdx.x >> 6] = m2;
+      ex.f[slot][1][threadIdx.x >> 6] = n_wave;
     }
     __syncthreads();
+    s = 0.0;
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-      s[i] = 0.f;
+    for (int w = 0; w < W; ++w) s += ex.s[slot][w];
+    mean = static_cast<float>(s / D);
+    m2 = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) s[i] += r[i * W + w];
+    for (int w = 0; w < W; ++w) {
+      const float nw = ex.f[slot][1][w];
+      const float d = nw > 0.f ? static_cast<float>(ex.s[slot][w]) / nw - mean : 0.f;
+      m2 += fmaf(nw * d, d, ex.f[slot][0][w]);
+    }
+    slot ^= 1;
+  } else {
+    mean = mw;
+  }
+  rstd = 1.f / sqrtf(m2 / static_cast<float>(D) + eps);
+}
+
+// Sums of two values over the group's G threads, in every thread.
+template <int G>
+__device__ __forceinline__ void group_sum(float (&s)[2], Exchange<G>& ex, int& slot) {
+  s[0] = wave_sum(s[0]);
+  s[1] = wave_sum(s[1]);
+  if constexpr (G > 64) {
+    constexpr int W = G / 64;
+    if ((threadIdx.x & 63) == 0) {
+      ex.f[slot][0][threadIdx.x >> 6] = s[0];
+      ex.f[slot][1][threadIdx.x >> 6] = s[1];
+    }
+    __syncthreads();
+    s[0] = s[1] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      s[0] += ex.f[slot][0][w];
+      s[1] += ex.f[slot][1][w];
     }
     slot ^= 1;
   }
@@ -133,51 +239,42 @@ __global__ __launch_bounds__(wg_of(G)) void norm_fwd_kernel(
     float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
     int64_t rows, int D) {
   constexpr int N = Vec<T>::N, WG = wg_of(G), R = WG / G;
-  __shared__ float red[2 * (G / 64)];
+  __shared__ Exchange<G> ex;
   int slot = 0;
   const int t = threadIdx.x % G, nfull = D / N;
-  float gm[NV][N], bt[NV][N];
+  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
+  // The next row is in flight while one is computed (G = 1024: the registers
+  // that 16 waves leave a thread do not hold it).
+  constexpr bool kAhead = G < 1024;
+  u32x4 next[NV];
+  auto fetch = [&](int64_t q) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) next[i] = load_vec(x + q * D, t + i * G, nfull, D);
+  };
+  if (kAhead && r < rows) fetch(r);
+  float gm[NV][N], bt[NV][N], n_wave = 0.f;
+  int cnt[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     load_param<N>(gamma, t + i * G, D, 1.f, gm[i]);
     load_param<N>(beta, t + i * G, D, 0.f, bt[i]);
+    cnt[i] = min(max(D - (t + i * G) * N, 0), N);
+    n_wave += static_cast<float>(cnt[i]);
   }
-  const float fd = static_cast<float>(D);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * R;
-  int64_t r = static_cast<int64_t>(blockIdx.x) * R + threadIdx.x / G;
-  u32x4 next[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    next[i] = r < rows ? load_vec(x + r * D, t + i * G, nfull, D) : u32x4{0, 0, 0, 0};
+  n_wave = wave_sum(n_wave);
   for (; r < rows; r += step) {
     float f[NV][N];
+    if (!kAhead) fetch(r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) Vec<T>::unpack(next[i], f[i]);
-    if (r + step < rows) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) next[i] = load_vec(x + (r + step) * D, t + i * G, nfull, D);
-    }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e) s[0] += f[i][e];
-    group_sum<G, 1>(s, red, slot);
-    const float mean = s[0] / fd;  // (a constant row's mean is exact where its sum is)
-    s[0] = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        f[i][e] -= mean;
-        if ((t + i * G) * N + e < D) s[0] = fmaf(f[i][e], f[i][e], s[0]);
-      }
-    group_sum<G, 1>(s, red, slot);
-    const float rstd = 1.f / sqrtf(s[0] / fd + eps);
+    if (kAhead && r + step < rows) fetch(r + step);
+    float mean, rstd;
+    row_stats<G, NV, N>(f, cnt, n_wave, D, eps, ex, slot, mean, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[i][e] = fmaf(f[i][e] * rstd, gm[i][e], bt[i][e]);
+      for (int e = 0; e < N; ++e) f[i][e] = fmaf((f[i][e] - mean) * rstd, gm[i][e], bt[i][e]);
       store_vec(y + r * D, t + i * G, nfull, D, f[i]);
     }
     if (t == 0) {
@@ -195,28 +292,28 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(
     float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
     int64_t rows, int D) {
   constexpr int N = Vec<T>::N, G = 1024;
-  __shared__ float red[2 * (G / 64)];
+  __shared__ Exchange<G> ex;
   int slot = 0;
   const int t = threadIdx.x, nfull = D / N, nvec = (D + N - 1) / N;
   const float fd = static_cast<float>(D);
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* xr = x + r * D;
-    float f[N], s[1] = {0.f};
+    float f[N], s[2] = {0.f, 0.f};
     for (int v = t; v < nvec; v += G) {
       Vec<T>::unpack(load_vec(xr, v, nfull, D), f);
 #pragma unroll
       for (int e = 0; e < N; ++e) s[0] += f[e];
     }
-    group_sum<G, 1>(s, red, slot);
+    group_sum<G>(s, ex, slot);
     const float mean = s[0] / fd;  // (a constant row's mean is exact where its sum is)
-    s[0] = 0.f;
+    s[0] = s[1] = 0.f;
     for (int v = t; v < nvec; v += G) {
       Vec<T>::unpack(load_vec(xr, v, nfull, D), f);
 #pragma unroll
       for (int e = 0; e < N; ++e)
         if (v * N + e < D) s[0] = fmaf(f[e] - mean, f[e] - mean, s[0]);
     }
-    group_sum<G, 1>(s, red, slot);
+    group_sum<G>(s, ex, slot);
     const float rstd = 1.f / sqrtf(s[0] / fd + eps);
     for (int v = t; v < nvec; v += G) {
       Vec<T>::unpack(load_vec(xr, v, nfull, D), f);
@@ -244,9 +341,9 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
     const T* __restrict__ dres, T* __restrict__ dx, float* __restrict__ part, int64_t rows,
     int D) {
   constexpr int N = Vec<T>::N, WG = wg_of(G), R = WG / G;
-  // Sums of the row's two means; with several groups a workgroup, the column
-  // sums of the others at the end.
-  __shared__ float red[R > 1 && PARAMS ? (R - 1) * 64 * NV * N : 4 * (G / 64)];
+  // red: with several groups a workgroup, the column sums of the others.
+  __shared__ Exchange<G> ex;
+  __shared__ float red[R > 1 && PARAMS ? (R - 1) * 64 * NV * N : 1];
   int slot = 0;
   const int t = threadIdx.x % G, grp = threadIdx.x / G, nfull = D / N;
   float gm[NV][N], dg[NV][N], db[NV][N];
@@ -270,9 +367,11 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
     nm = mean_in[q];
     nr = rstd_in[q];
   };
-  if (r < rows) fetch(r);
+  constexpr bool kAhead = G < 1024;  // as in the forward
+  if (kAhead && r < rows) fetch(r);
   for (; r < rows; r += step) {
     float h[NV][N], d[NV][N], s[2] = {0.f, 0.f};
+    if (!kAhead) fetch(r);
     const float mean = nm, rstd = nr;
     u32x4 res[NV];
 #pragma unroll
@@ -281,7 +380,7 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
       Vec<T>::unpack(nd[i], d[i]);
       res[i] = dres != nullptr ? load_vec(dres + r * D, t + i * G, nfull, D) : u32x4{0, 0, 0, 0};
     }
-    if (r + step < rows) fetch(r + step);
+    if (kAhead && r + step < rows) fetch(r + step);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -297,7 +396,7 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
         s[0] += d[i][e];
         s[1] = fmaf(d[i][e], h[i][e], s[1]);
       }
-    group_sum<G, 2>(s, red, slot);
+    group_sum<G>(s, ex, slot);
     const float c0 = s[0] / fd, c1 = s[1] / fd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -349,7 +448,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
     const T* __restrict__ dres, T* __restrict__ dx, int64_t rows, int D) {
   constexpr int N = Vec<T>::N, G = 1024;
-  __shared__ float red[4 * (G / 64)];
+  __shared__ Exchange<G> ex;
   int slot = 0;
   const int t = threadIdx.x, nfull = D / N, nvec = (D + N - 1) / N;
   const float fd = static_cast<float>(D);
@@ -366,7 +465,7 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(
         s[1] = fmaf(d[e] * gm[e], (h[e] - mean) * rstd, s[1]);
       }
     }
-    group_sum<G, 2>(s, red, slot);
+    group_sum<G>(s, ex, slot);
     const float c0 = s[0] / fd, c1 = s[1] / fd;
     for (int v = t; v < nvec; v += G) {
       float o[N];

@@ -288,7 +288,7 @@ __device__ __forceinline__ void store_block(const Product& p, const Out& o, int 
         const float v = fmaf(o.keep, w[q][s], o.add * (acc[q][s] * p.alpha));
         if (!ok(q, s)) continue;
         if (o.w.bf16)
-          static_cast<uint16_t*>(o.w.data)[off(q, s)] = f32_to_bf16(v);
+          static_cast<__bf16*>(o.w.data)[off(q, s)] = static_cast<__bf16>(v);  // to nearest even
         else
           static_cast<float*>(o.w.data)[off(q, s)] = v;
       }

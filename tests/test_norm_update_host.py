@@ -11,6 +11,7 @@ import torch
 from mixture_experts_layer_fp32_amd import _binding as B
 from oracle import norm_update_oracle as ou
 
+CPU = torch.device("cpu")
 FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: every call below fails its checks
 
 
@@ -166,10 +167,10 @@ def test_binding_refuses_host_tensors_and_shapes(lib):
     with pytest.raises(ValueError):
         B.moe_orthogonalize(x, x, torch.zeros(4, dtype=torch.uint8))
     with pytest.raises(ValueError):
-        B._matrices(torch.zeros(2, 4, 8).transpose(1, 2), "g")  # columns not adjacent
+        B._matrices(CPU, torch.zeros(2, 4, 8).transpose(1, 2), "g")  # columns not adjacent
     with pytest.raises(ValueError):
-        B._matrices(torch.zeros(2, 4, 8, dtype=torch.float16), "g")
+        B._matrices(CPU, torch.zeros(2, 4, 8, dtype=torch.float16), "g")
     with pytest.raises(ValueError):
-        B._matrices(torch.zeros(8), "g")
-    m, shape = B._matrices(torch.zeros(3, 4, 16)[:, :, :8], "g")
-    assert shape == (3, 4, 8) and (m.ld, m.stride) == (16, 64)
+        B._matrices(CPU, torch.zeros(8), "g")
+    m = B._matrices(CPU, torch.zeros(3, 4, 16)[:, :, :8], "g")
+    assert (m.ld, m.stride) == (16, 64)
