@@ -36,6 +36,7 @@
 // 4 KB, a fragment is 16 bytes a lane in LDS order, so there are no bank
 // conflicts and no swizzle.
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_internal.h"
 #include "moe_update.h"
@@ -44,6 +45,8 @@ namespace moe {
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 
@@ -179,34 +182,42 @@ constexpr int vmcnt_imm(int n) { return (n & 15) | (7 << 4) | (15 << 8) | ((n >>
 constexpr int kVm0Lgkm0 = 7 << 4;
 constexpr int kOutOfRange = 0x7FFF0000;  // past every operand tile (below 2^28 bytes)
 
-// 4x4 transpose inside each group of 4 lanes: before, lane l's v[s] is row
-// 4 (l / 32) + s, column l % 32; after, it is row 4 (l / 32) + l % 4, column
-// 4 (l % 32 / 4) + s.
-__device__ __forceinline__ void transpose4(float (&v)[4], int quad) {
-  float n[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float x = __builtin_bit_cast(
-        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v[r ^ 1]), 0xB1, 0xF, 0xF, false));
-    n[r] = ((r ^ quad) & 1) ? x : v[r];
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const float x = __builtin_bit_cast(
-        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, n[r ^ 2]), 0x4E, 0xF, 0xF, false));
-    v[r] = ((r ^ quad) & 2) ? x : n[r];
-  }
+// Four values as fp16 parts, two packed conversions each (to nearest even).
+struct Parts {
+  uint2 hi, lo;
+};
+__device__ __forceinline__ Parts split4(const float (&v)[4]) {
+  const f16x2 h0 = __builtin_convertvector(f32x2{v[0], v[1]}, f16x2);
+  const f16x2 h1 = __builtin_convertvector(f32x2{v[2], v[3]}, f16x2);
+  const f16x2 l0 = __builtin_convertvector(
+      f32x2{v[0] - static_cast<float>(h0[0]), v[1] - static_cast<float>(h0[1])}, f16x2);
+  const f16x2 l1 = __builtin_convertvector(
+      f32x2{v[2] - static_cast<float>(h1[0]), v[3] - static_cast<float>(h1[1])}, f16x2);
+  return {uint2{__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)},
+          uint2{__builtin_bit_cast(uint32_t, l0), __builtin_bit_cast(uint32_t, l1)}};
 }
 
-__device__ __forceinline__ void store_parts(uint16_t* frag, int lane, int j, const float (&v)[4]) {
-  union {
-    uint16_t h[4];
-    uint2 w;
-  } hi, lo;
-#pragma unroll
-  for (int s = 0; s < 4; ++s) split(v[s], hi.h[s], lo.h[s]);
-  *reinterpret_cast<uint2*>(frag + lane * 8 + j) = hi.w;
-  *reinterpret_cast<uint2*>(frag + 512 + lane * 8 + j) = lo.w;
+// 4x4 transpose of 16-bit values inside each group of 4 lanes: before, lane
+// l's value s is row s, column l % 4; after, it is row l % 4, column s.
+__device__ __forceinline__ uint2 transpose4(uint2 w, int quad) {
+  auto dpp = [](uint32_t v, auto ctrl) {
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v),
+                                                          decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  const bool up = (quad & 2) != 0;
+  // Lanes 0, 1 take rows 0, 1 of lanes 2, 3 and give them rows 2, 3.
+  uint32_t keep = up ? w.y : w.x;
+  uint32_t got = dpp(up ? w.x : w.y, std::integral_constant<int, 0x4E>{});
+  // Even lanes take the lower halves of both of the pair, odd lanes the upper.
+  const uint32_t sel = (quad & 1) ? 0x03020706u : 0x05040100u;
+  keep = __builtin_amdgcn_perm(dpp(keep, std::integral_constant<int, 0xB1>{}), keep, sel);
+  got = __builtin_amdgcn_perm(dpp(got, std::integral_constant<int, 0xB1>{}), got, sel);
+  return up ? uint2{got, keep} : uint2{keep, got};
+}
+
+__device__ __forceinline__ void store_parts(uint16_t* frag, int lane, int j, const Parts& v) {
+  *reinterpret_cast<uint2*>(frag + lane * 8 + j) = v.hi;
+  *reinterpret_cast<uint2*>(frag + 512 + lane * 8 + j) = v.lo;
 }
 
 // One product D[i][j] = sum_k a[i][k] b[j][k] of n matrices, a of ra 32-row
@@ -325,13 +336,15 @@ __device__ __forceinline__ void store_block(const Product& p, const Out& o, int 
           if (ib == jb && 8 * (q0 + q) + 4 * half + s == l32) v[s] += p.gamma;
         }
       }
-      store_parts(p.out_t + mat * p.so + frag(q), slot(q), 4 * half, v);
+      Parts w = split4(v);
+      store_parts(p.out_t + mat * p.so + frag(q), slot(q), 4 * half, w);
       if (EPI == kOperand || mirror) {
         // Operand with rows i, its depth j.
-        transpose4(v, lane & 3);
+        w.hi = transpose4(w.hi, lane & 3);
+        w.lo = transpose4(w.lo, lane & 3);
         const int j0 = 4 * (l32 >> 2), row = 8 * (q0 + q) + 4 * half + (lane & 3);
         const int64_t fn = (static_cast<int64_t>(ib) * (2 * rb) + 2 * jb + (j0 >> 4)) * 1024;
-        store_parts(p.out_n + mat * p.so + fn, row + 32 * ((j0 >> 3) & 1), j0 & 7, v);
+        store_parts(p.out_n + mat * p.so + fn, row + 32 * ((j0 >> 3) & 1), j0 & 7, w);
       }
     }
   }
@@ -342,13 +355,22 @@ __device__ __forceinline__ void store_block(const Product& p, const Out& o, int 
 // kOperand: alpha D is stored into out_t and out_n.
 // kOut: to the caller's matrices (rows i, columns j).
 // blockIdx.y: one of two independent products.
-template <int EPI, int WM, int WN, int WR, int WC>
+// PARTS 1: the high parts alone, one matrix instruction a product instead of
+//   three and half the bytes, for the last product of a Muon step on bf16
+//   weights (128 x 768 x 2048: 1410 -> 1130 us). Its fp16 operands (11 bits)
+//   cost O 2.7e-4 (full rank) to 3.3e-3 (rank 8) of its size, simulated; W's
+//   own rounding to 8 bits is far above lr scale times that wherever the step
+//   is smaller than the weight. moe_orthogonalize, whose result is O, keeps
+//   both parts, and so do the products before the last, where such errors
+//   would grow with the later steps.
+template <int EPI, int PARTS, int WM, int WN, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, Product p1,
                                                                    Out o, int n, int ra, int rb,
                                                                    int KS) {
   constexpr int BA = WR * WM, BB = WC * WN;    // 32-row blocks per tile
   constexpr int NW = WR * WC;
-  constexpr int kStage = (BA + BB) * 4096;     // K = 32, both parts
+  constexpr int SS = PARTS == 2 ? 2 : 4;       // slices a step
+  constexpr int kStage = (BA + BB) * 4096;
   constexpr int NC = (BA + BB) * 4 / NW;       // 1 KB copies per wave and step
   static_assert((BA + BB) * 4 % NW == 0 && BA * 4 % NC == 0, "copies are shared out evenly");
   static_assert(EPI != kSym || BA == BB, "symmetric results use square tiles");
@@ -374,13 +396,15 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
   int voff[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
-    voff[i] = ((piece0 + i) >> 2) * row_bytes + ((piece0 + i) & 3) * 1024 + lane * 16;
+    voff[i] = ((piece0 + i) >> 2) * row_bytes + ((piece0 + i) & 3) * (2048 / PARTS) + lane * 16;
   const unsigned lds_w = (unsigned)(uintptr_t)(lds_u8*)smem + wave * NC * 1024;
-  const int nk = KS / 2;
-  // A copy past the last step is still issued, out of range (it writes zeros
-  // into a finished slot), so the K loop has no branch around it.
+  const int nk = (KS + SS - 1) / SS;
+  // A copy past the last slice is still issued, out of range (it writes
+  // zeros), so the K loop has no branch around it.
   auto copy = [&](int i, int kt) {
-    dma16(rsrc, kt < nk ? voff[i] : kOutOfRange, kt * 4096, lds_w + (kt & 1) * kStage + i * 1024);
+    const int slice = kt * SS + (PARTS == 2 ? 0 : (piece0 + i) & 3);
+    dma16(rsrc, slice < KS ? voff[i] : kOutOfRange, kt * (SS * 2048),
+          lds_w + (kt & 1) * kStage + i * 1024);
   };
 
   f32x16 acc[WM][WN];
@@ -391,16 +415,17 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // Fragments of one slice: WM of a, then WN of b, [hi, lo] each.
-  constexpr int NF = 2 * (WM + WN), NM = 3 * WM * WN;
+  // Fragments of half a step: WM of a, then WN of b, two each: [hi, lo] of
+  // one slice, or hi of two slices.
+  constexpr int NF = 2 * (WM + WN), NM = (PARTS == 2 ? 3 : 2) * WM * WN;
   f16x8 fr[2][NF];
   auto read = [&](int f, int kt, int ks) {
     const int blk = f / 2 < WM ? wr * WM + f / 2 : BA + wc * WN + f / 2 - WM;
     fr[ks][f] = *reinterpret_cast<const f16x8*>(smem + (kt & 1) * kStage + blk * 4096 + ks * 2048 +
                                                 (f & 1) * 1024 + lane * 16);
   };
-  // Products of slice ks in the order lo hi, hi lo, hi hi; `side(x)` for x in
-  // [0, n) is spread between them.
+  // Products of half a step, of a slice in the order lo hi, hi lo, hi hi;
+  // `side(x)` for x in [0, n) is spread between them.
   auto multiply = [&](int ks, int n, auto side) {
 #pragma unroll
     for (int x = 0; x < NM; ++x) {
@@ -408,9 +433,10 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 #pragma unroll
       for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
       __builtin_amdgcn_sched_barrier(0);
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + (q == 0)],
-                                                         fr[ks][2 * (WM + j) + (q == 1)],
-                                                         acc[i][j], 0, 0, 0);
+      const int qa = PARTS == 2 ? q == 0 : q, qb = PARTS == 2 ? q == 1 : q;
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + qa],
+                                                         fr[ks][2 * (WM + j) + qb], acc[i][j], 0,
+                                                         0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -628,12 +654,14 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       float v[4];
 #pragma unroll
       for (int s = 0; s < 4; ++s) v[s] = acc[4 * q + s] * alpha;
-      store_parts(op + place(q), 0, 0, v);
+      Parts w = split4(v);
+      store_parts(op + place(q), 0, 0, w);
       if (ib != jb) {
-        transpose4(v, lane & 3);
+        w.hi = transpose4(w.hi, lane & 3);
+        w.lo = transpose4(w.lo, lane & 3);
         const int j0 = 4 * (l32 >> 2), row = 8 * q + 4 * half + (lane & 3);
         store_parts(op + ((ib * KS + 2 * jb + (j0 >> 4)) * 2) * 512, row + 32 * ((j0 >> 3) & 1),
-                    j0 & 7, v);
+                    j0 & 7, w);
       }
     }
   };
@@ -731,7 +759,7 @@ int64_t tile_count(int B, int n, int ra, int rb) {
 // 5/4 of the 128-tiles' area (sides just past a multiple of 256). Small tiles
 // too where 128-tiles would compute twice their area (256 x 64 x 256: 134 us,
 // 157 with 128-tiles).
-template <int EPI>
+template <int EPI, int PARTS = 2>
 hipError_t launch_product(const Product& p0, const Product* p1, const Out& o, int n, int ra,
                           int rb, int KS, hipStream_t s) {
   auto grid = [&](int B) {
@@ -744,9 +772,9 @@ hipError_t launch_product(const Product& p0, const Product* p1, const Out& o, in
   if (t128 <= kSmallTiles || t64 <= 2 * t128)
     orth_product_small_kernel<EPI><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else if (t128 <= kMidTiles || 16 * t256 > 5 * t128)
-    orth_product_kernel<EPI, 2, 2, 2, 2><<<grid(4), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
+    orth_product_kernel<EPI, PARTS, 2, 2, 2, 2><<<grid(4), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
-    orth_product_kernel<EPI, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
+    orth_product_kernel<EPI, PARTS, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   return hipGetLastError();
 }
 
@@ -850,7 +878,11 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
       // A <- U P, the next P.
       Product u = sym_args(A, pl, kScaleA, kScaleP, U, kScaleA, 1.f);
       Product qq = sym_args(pl, q, kScaleP, kScaleP, q2, kScaleP, 1.f);
-      e = launch_product<kSym>(u, i > 1 ? &qq : nullptr, none, n, rm, rm, 2 * rm, s);
+      // Both in one launch while that is one round of workgroups (4096 x 4096,
+      // 136 + 136 tiles of 256: 540 us together, 488 one after the other).
+      const bool pair = tile_count<kSym>(8, n, rm, rm) <= 128;
+      e = launch_product<kSym>(u, i > 1 && pair ? &qq : nullptr, none, n, rm, rm, 2 * rm, s);
+      if (e == hipSuccess && i > 1 && !pair) e = sym(qq);
       if (e != hipSuccess) return e;
       if (i > 1) std::swap(q, q2);
       if ((e = sym(sym_args(U, pl, kScaleA, kScaleP, A, kScaleA, 1.f))) != hipSuccess) return e;
@@ -873,7 +905,10 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
         std::swap(x.a, x.b);
         std::swap(x.sa, x.sb);
       }
-      e = launch_product<kOut>(x, nullptr, out, n, tall ? rk : rm, tall ? rm : rk, 2 * rm, s);
+      const int ra = tall ? rk : rm, rb = tall ? rm : rk;
+      e = wm.bf16 && mom != nullptr
+              ? launch_product<kOut, 1>(x, nullptr, out, n, ra, rb, 2 * rm, s)
+              : launch_product<kOut>(x, nullptr, out, n, ra, rb, 2 * rm, s);
     }
     if (e != hipSuccess) return e;
   }
