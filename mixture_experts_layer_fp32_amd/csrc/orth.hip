@@ -47,13 +47,14 @@ namespace {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 4096.f, kScaleA = 4096.f, kScaleP = 1024.f;
 constexpr int kXcds = 8;
-constexpr int kSmallTiles = 128, kMidTiles = 512;
+constexpr int kSmallTiles = 128, kMidTiles = 512, kMidTilesShort = 640;
 
 struct Mats {  // moe_matrices on the device side
   void* data;
@@ -66,26 +67,65 @@ __device__ __forceinline__ float load_el(const Mats& m, int64_t off) {
                 : static_cast<const float*>(m.data)[off];
 }
 
+// V adjacent values (4: aligned to their size).
+template <int V>
+__device__ __forceinline__ void load_v(const Mats& m, int64_t off, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = load_el(m, off);
+  } else if (m.bf16) {
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(m.data) + off);
+    f[0] = __uint_as_float(r.x << 16);
+    f[1] = __uint_as_float(r.x & 0xffff0000u);
+    f[2] = __uint_as_float(r.y << 16);
+    f[3] = __uint_as_float(r.y & 0xffff0000u);
+  } else {
+    const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(m.data) + off);
+    f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w;
+  }
+}
+
 // ---- norm: partial sums of squares; the momentum -----------------------------
 // Partial sums in fp64 (no overflow or underflow of squares). With mom.data
-// the momentum is updated and the norm is that of U.
+// the momentum is updated and the norm is that of U. Bound by memory.
+template <int V>
 __global__ __launch_bounds__(256) void orth_norm_kernel(Mats g, Mats mom, float mu, int nesterov,
-                                                        int rows, int cols,
-                                                        int64_t chunk, double* __restrict__ part) {
+                                                        int rows, int cols, int64_t chunk,
+                                                        double* __restrict__ part) {
   const int b = blockIdx.y;
-  const int64_t e0 = blockIdx.x * chunk;
-  const int64_t e1 = min(e0 + chunk, static_cast<int64_t>(rows) * cols);
+  const int64_t e1 = min((blockIdx.x + 1) * chunk, static_cast<int64_t>(rows) * cols);
+  int64_t e = blockIdx.x * chunk + threadIdx.x * V;  // chunk is a multiple of 4
+  // Row and column of e, carried along.
+  int64_t r = e / cols;
+  int c = static_cast<int>(e - r * cols);
+  const int step_r = 256 * V / cols, step_c = 256 * V % cols;
   double s = 0.0;
-  for (int64_t e = e0 + threadIdx.x; e < e1; e += 256) {
-    const int64_t r = e / cols, c = e - r * cols;
-    float u = load_el(g, b * g.stride + r * g.ld + c);
+#pragma unroll 4
+  for (; e < e1; e += 256 * V) {
+    float u[V];
+    load_v<V>(g, b * g.stride + r * g.ld + c, u);
     if (mom.data != nullptr) {
-      float* mp = static_cast<float*>(mom.data) + b * mom.stride + r * mom.ld + c;
-      const float m = fmaf(mu, *mp, u);
-      *mp = m;
-      u = nesterov ? fmaf(mu, m, u) : m;
+      const int64_t at = b * mom.stride + r * mom.ld + c;
+      float m[V];
+      load_v<V>(mom, at, m);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        m[i] = fmaf(mu, m[i], u[i]);
+        u[i] = nesterov ? fmaf(mu, m[i], u[i]) : m[i];
+      }
+      float* mp = static_cast<float*>(mom.data) + at;
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(mp) = make_float4(m[0], m[1], m[2], m[3]);
+      else
+        *mp = m[0];
     }
-    s += static_cast<double>(u) * u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) s += static_cast<double>(u[i]) * u[i];
+    r += step_r;
+    c += step_c;
+    if (c >= cols) {
+      c -= cols;
+      ++r;
+    }
   }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
@@ -105,15 +145,34 @@ __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) {
 }
 
 // ---- split: U / norm into fragments, both ways round -------------------------
-// One 64 x 64 tile of U a workgroup, through LDS.
+// One 64 x 64 tile of U a workgroup, through LDS. Bound by memory.
+template <int V>
 __global__ __launch_bounds__(256) void orth_split_kernel(
     Mats g, Mats mom, float mu, int nesterov, int rows, int cols, float eps,
     const double* __restrict__ part, int nparts, uint16_t* __restrict__ u_planes,
     uint16_t* __restrict__ ut_planes, int64_t plane_stride, int tiles_c) {
   __shared__ float tile[64][65];
   __shared__ double red[4];
-  const int b = blockIdx.y, tid = threadIdx.x;
+  const int b = gridDim.y - 1 - blockIdx.y, tid = threadIdx.x;
   const int r0 = (blockIdx.x / tiles_c) * 64, c0 = (blockIdx.x % tiles_c) * 64;
+  // The tile's values are on their way while the norm is summed.
+  constexpr int NL = 64 * 64 / (256 * V);
+  float u[NL][V];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int x = (tid + 256 * i) * V, r = r0 + (x >> 6), c = c0 + (x & 63);
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[i][k] = 0.f;
+    if (r < rows && c < cols) {
+      load_v<V>(g, b * g.stride + r * g.ld + c, u[i]);
+      if (mom.data != nullptr) {
+        float m[V];
+        load_v<V>(mom, b * mom.stride + r * mom.ld + c, m);
+#pragma unroll
+        for (int k = 0; k < V; ++k) u[i][k] = nesterov ? fmaf(mu, m[k], u[i][k]) : m[k];
+      }
+    }
+  }
   double s = 0.0;
   for (int i = tid; i < nparts; i += 256) s += part[static_cast<int64_t>(b) * nparts + i];
 #pragma unroll
@@ -122,18 +181,11 @@ __global__ __launch_bounds__(256) void orth_split_kernel(
   __syncthreads();
   const double inv =
       static_cast<double>(kScaleX) / (sqrt(red[0] + red[1] + red[2] + red[3]) + eps);
-  for (int i = tid; i < 64 * 64; i += 256) {
-    const int r = r0 + (i >> 6), c = c0 + (i & 63);
-    float u = 0.f;
-    if (r < rows && c < cols) {
-      u = load_el(g, b * g.stride + r * g.ld + c);
-      if (mom.data != nullptr) {
-        const float m = static_cast<const float*>(mom.data)[b * mom.stride + r * mom.ld + c];
-        u = nesterov ? fmaf(mu, m, u) : m;
-      }
-      u = static_cast<float>(u * inv);
-    }
-    tile[i >> 6][i & 63] = u;
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int x = (tid + 256 * i) * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) tile[x >> 6][(x & 63) + k] = static_cast<float>(u[i][k] * inv);
   }
   __syncthreads();
   // 8 fragments of each orientation (2 row blocks x 4 slices), 64 lanes each.
@@ -197,8 +249,25 @@ __device__ __forceinline__ Parts split4(const float (&v)[4]) {
           uint2{__builtin_bit_cast(uint32_t, l0), __builtin_bit_cast(uint32_t, l1)}};
 }
 
-// 4x4 transpose of 16-bit values inside each group of 4 lanes: before, lane
-// l's value s is row s, column l % 4; after, it is row l % 4, column s.
+// 4x4 transpose inside each group of 4 lanes: before, lane l's v[s] is row s,
+// column l % 4; after, it is row l % 4, column s.
+__device__ __forceinline__ void transpose4(float (&v)[4], int quad) {
+  float n[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float x = __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v[r ^ 1]), 0xB1, 0xF, 0xF, false));
+    n[r] = ((r ^ quad) & 1) ? x : v[r];
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const float x = __builtin_bit_cast(
+        float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, n[r ^ 2]), 0x4E, 0xF, 0xF, false));
+    v[r] = ((r ^ quad) & 2) ? x : n[r];
+  }
+}
+
+// The same for four 16-bit values.
 __device__ __forceinline__ uint2 transpose4(uint2 w, int quad) {
   auto dpp = [](uint32_t v, auto ctrl) {
     return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v),
@@ -230,12 +299,14 @@ struct Product {
   int64_t so;
   const uint16_t* aux;  // kSym: symmetric operand added with factor beta
   float alpha, beta, gamma;
+  int flip;  // each XCD's tiles last to first
 };
 struct Out {  // kOut: matrix row i, column j
   Mats w;
   int rows, cols;
   float keep, add;  // w <- keep w + add O (muon), or w <- add O
   int muon;
+  int vec4;  // groups of four columns are aligned to their size
 };
 
 enum Epilogue { kSym = 0, kOperand = 1, kOut = 2 };
@@ -248,11 +319,12 @@ struct Tile {
   int mat, a0, b0;
 };
 template <int EPI, int BA, int BB>
-__device__ __forceinline__ bool find_tile(int n, int ra, int rb, Tile& t) {
+__device__ __forceinline__ bool find_tile(int n, int ra, int rb, int flip, Tile& t) {
   const int ta = (ra + BA - 1) / BA, tb = (rb + BB - 1) / BB;
   const int per_mat = EPI == kSym ? ta * (ta + 1) / 2 : ta * tb;
   const int total = per_mat * n, per = (total + kXcds - 1) / kXcds;
-  const int u = (static_cast<int>(blockIdx.x) % kXcds) * per + static_cast<int>(blockIdx.x) / kXcds;
+  const int slot = static_cast<int>(blockIdx.x) / kXcds;
+  const int u = (static_cast<int>(blockIdx.x) % kXcds) * per + (flip ? per - 1 - slot : slot);
   if (u >= total) return false;
   t.mat = u / per_mat;
   const int lt = u - t.mat * per_mat;
@@ -280,11 +352,52 @@ __device__ __forceinline__ void store_block(const Product& p, const Out& o, int 
                                             const float (&acc)[NQ][4], int lane) {
   const int half = lane >> 5, l32 = lane & 31;
   if constexpr (EPI == kOut) {
-    // Lanes run along the caller's columns: runs of 64 (bf16) or 128 bytes.
+    const bool whole = (ib + 1) * 32 <= o.rows && (jb + 1) * 32 <= o.cols;
+    if (whole && o.vec4) {
+      // Four lanes exchange their values: a lane gets four columns of one row.
+      const int64_t at = mat * o.w.stride +
+                         static_cast<int64_t>(ib * 32 + 8 * q0 + 4 * half + (lane & 3)) * o.w.ld +
+                         jb * 32 + 4 * (l32 >> 2);
+      float w[NQ][4];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int64_t e = at + 8 * q * o.w.ld;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) w[q][s] = 0.f;
+        if (o.muon && o.w.bf16) {
+          const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(o.w.data) + e);
+          w[q][0] = __uint_as_float(r.x << 16);
+          w[q][1] = __uint_as_float(r.x & 0xffff0000u);
+          w[q][2] = __uint_as_float(r.y << 16);
+          w[q][3] = __uint_as_float(r.y & 0xffff0000u);
+        } else if (o.muon) {
+          const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(o.w.data) + e);
+          w[q][0] = r.x; w[q][1] = r.y; w[q][2] = r.z; w[q][3] = r.w;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        const int64_t e = at + 8 * q * o.w.ld;
+        float v[4] = {acc[q][0], acc[q][1], acc[q][2], acc[q][3]};
+        transpose4(v, lane & 3);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] = fmaf(o.keep, w[q][s], o.add * (v[s] * p.alpha));
+        if (o.w.bf16) {
+          const bf16x2 b0 = __builtin_convertvector(f32x2{v[0], v[1]}, bf16x2);
+          const bf16x2 b1 = __builtin_convertvector(f32x2{v[2], v[3]}, bf16x2);
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(o.w.data) + e) =
+              uint2{__builtin_bit_cast(uint32_t, b0), __builtin_bit_cast(uint32_t, b1)};
+        } else {
+          *reinterpret_cast<float4*>(static_cast<float*>(o.w.data) + e) =
+              make_float4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      return;
+    }
+    // Lanes run along the caller's columns.
     const int r0 = ib * 32 + 8 * q0 + 4 * half, c = jb * 32 + l32;
     const int64_t at = mat * o.w.stride + r0 * o.w.ld + c;
-    const bool whole = (ib + 1) * 32 <= o.rows && (jb + 1) * 32 <= o.cols;
-    auto ok = [&](int q, int s) { return whole || (r0 + 8 * q + s < o.rows && c < o.cols); };
+    auto ok = [&](int q, int s) { return r0 + 8 * q + s < o.rows && c < o.cols; };
     auto off = [&](int q, int s) { return at + (8 * q + s) * o.w.ld; };
     float w[NQ][4];
 #pragma unroll
@@ -378,7 +491,7 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 
   const Product& p = blockIdx.y == 0 ? p0 : p1;
   Tile t;
-  if (!find_tile<EPI, BA, BB>(n, ra, rb, t)) return;
+  if (!find_tile<EPI, BA, BB>(n, ra, rb, p.flip, t)) return;
   const int mat = t.mat, a0 = t.a0, b0 = t.b0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -495,7 +608,7 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
   __shared__ __attribute__((aligned(16))) float part[8][4][4][64][4];  // wave, block, q, lane
   const Product& p = blockIdx.y == 0 ? p0 : p1;
   Tile t;
-  if (!find_tile<EPI, 2, 2>(n, ra, rb, t)) return;
+  if (!find_tile<EPI, 2, 2>(n, ra, rb, p.flip, t)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // Row blocks past the last read the last one again (they are not stored).
@@ -711,16 +824,15 @@ struct Space {
   int64_t part;   // partial sums per matrix
   size_t bytes;
 };
-int norm_parts(int n, int64_t values) {
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(1024, 4096 / std::max(n, 1)));
-  return static_cast<int>(std::min<int64_t>(most, (values + 4095) / 4096));
+int norm_parts(int64_t values) {
+  return static_cast<int>(std::min<int64_t>(1024, (values + 8191) / 8192));
 }
 Space space(int n, int rows, int cols) {
   Space s;
   const int64_t m = ceil32(std::min(rows, cols)), k = ceil32(std::max(rows, cols));
   s.x = m * 2 * k * 1024;
   s.mm = m * 2 * m * 1024;
-  s.part = norm_parts(n, static_cast<int64_t>(rows) * cols);
+  s.part = norm_parts(static_cast<int64_t>(rows) * cols);
   s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.part * 8);
   return s;
 }
@@ -744,6 +856,12 @@ Segments segment_rule(bool bf16_out, bool muon, int m) {
   return muon || m >= 1024 ? Segments{2, 2} : Segments{1, 1};
 }
 
+// Groups of four columns are aligned to their size.
+int aligned4(const moe_matrices& m) {
+  const uintptr_t size = m.dtype == MOE_BF16 ? 8 : 16;
+  return reinterpret_cast<uintptr_t>(m.data) % size == 0 && m.ld % 4 == 0 && m.stride % 4 == 0;
+}
+
 template <int EPI>
 int64_t tile_count(int B, int n, int ra, int rb) {
   const int64_t ta = (ra + B - 1) / B, tb = (rb + B - 1) / B;
@@ -755,23 +873,27 @@ int64_t tile_count(int B, int n, int ra, int rb) {
 // 2 x 1024^2 (72 tiles of 128) 384 / 455 / - us; 2048^2 (136) 1052 / 913 / -;
 // 16 x 1024 x 2048 (576) 2410 / 2090 / 2047; 4096 x 14336 (528) 9998 / 8003 /
 // 7640. So: the small tiles up to half a 128-tile a CU, 128-tiles while one
-// round holds them all, then 256-tiles unless they would compute more than
+// round holds them all (and a little past it at depths up to 1024: 576 tiles
+// 73 us, 82 as 160 of 256), then 256-tiles unless they would compute more than
 // 5/4 of the 128-tiles' area (sides just past a multiple of 256). Small tiles
 // too where 128-tiles would compute twice their area (256 x 64 x 256: 134 us,
 // 157 with 128-tiles).
 template <int EPI, int PARTS = 2>
-hipError_t launch_product(const Product& p0, const Product* p1, const Out& o, int n, int ra,
-                          int rb, int KS, hipStream_t s) {
+hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, int rb, int KS,
+                          int& flip, hipStream_t s) {
   auto grid = [&](int B) {
     const int64_t t = (tile_count<EPI>(B, n, ra, rb) + kXcds - 1) / kXcds * kXcds;
     return dim3(static_cast<unsigned>(t), p1 ? 2 : 1);
   };
+  p0.flip = flip;
+  flip ^= 1;
+  if (p1) p1->flip = p0.flip;
   const Product& q = p1 ? *p1 : p0;
   const int64_t t64 = tile_count<EPI>(2, n, ra, rb), t128 = tile_count<EPI>(4, n, ra, rb);
   const int64_t t256 = tile_count<EPI>(8, n, ra, rb);
   if (t128 <= kSmallTiles || t64 <= 2 * t128)
     orth_product_small_kernel<EPI><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
-  else if (t128 <= kMidTiles || 16 * t256 > 5 * t128)
+  else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) || 16 * t256 > 5 * t128)
     orth_product_kernel<EPI, PARTS, 2, 2, 2, 2><<<grid(4), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
     orth_product_kernel<EPI, PARTS, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
@@ -824,25 +946,35 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
   const Mats mm = mom ? Mats{mom->data, mom->ld, mom->stride, 0} : Mats{nullptr, 0, 0, 0};
   const int nparts = static_cast<int>(sp.part);
   const int64_t values = static_cast<int64_t>(rows) * cols;
-  const int64_t chunk = (values + nparts - 1) / nparts;
-  orth_norm_kernel<<<dim3(nparts, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols,
-                                                   chunk, part);
+  const int64_t chunk = ((values + nparts - 1) / nparts + 3) / 4 * 4;
+  const bool vec4 = cols % 4 == 0 && aligned4(g) && (mom == nullptr || aligned4(*mom));
   const int tr = (rows + 63) / 64, tc = (cols + 63) / 64;
-  orth_split_kernel<<<dim3(tr * tc, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, d.eps,
-                                                     part, nparts, tall ? XT : X, tall ? X : XT,
-                                                     sp.x, tc);
+  auto run = [&](auto norm, auto split) {
+    norm<<<dim3(nparts, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, chunk, part);
+    split<<<dim3(tr * tc, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, d.eps, part,
+                                           nparts, tall ? XT : X, tall ? X : XT, sp.x, tc);
+  };
+  if (vec4)
+    run(orth_norm_kernel<4>, orth_split_kernel<4>);
+  else
+    run(orth_norm_kernel<1>, orth_split_kernel<1>);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
   const Out none{};
   const Out out{wm, rows, cols, mom ? 1.f - d.lr * d.weight_decay : 0.f,
-                mom ? -d.lr * d.scale : 1.f, mom != nullptr};
+                mom ? -d.lr * d.scale : 1.f, mom != nullptr, aligned4(w)};
+  // Every other product takes its tiles in the opposite order: what the last
+  // one wrote at its end is still in the 256 MB cache.
+  int flip = 0;
   // Symmetric m x m product: out = so (a b / (sa sb) + beta aux + gamma I).
   auto sym_args = [&](const uint16_t* a, const uint16_t* b, float sa, float sb, uint16_t* out,
                       float so, float alpha) {
     return Product{a, b, sp.mm, sp.mm, out, out, sp.mm, nullptr, alpha * so / (sa * sb), 0.f, 0.f};
   };
-  auto sym = [&](const Product& p) { return launch_product<kSym>(p, nullptr, none, n, rm, rm, 2 * rm, s); };
+  auto sym = [&](const Product& p) {
+    return launch_product<kSym>(p, nullptr, none, n, rm, rm, 2 * rm, flip, s);
+  };
   auto poly = [&](uint16_t* out) {  // P = aI + bA + cA^2
     Product p = sym_args(A, A, kScaleA, kScaleA, out, kScaleP, kC);
     p.aux = A;
@@ -856,7 +988,8 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     const int L = std::min(left, first ? seg.first : seg.later);
     left -= L;
     Product gram{X, X, sp.x, sp.x, A, A, sp.mm, nullptr, kScaleA / (kScaleX * kScaleX), 0.f, 0.f};
-    if ((e = launch_product<kSym>(gram, nullptr, none, n, rm, rm, 2 * rk, s)) != hipSuccess) return e;
+    e = launch_product<kSym>(gram, nullptr, none, n, rm, rm, 2 * rk, flip, s);
+    if (e != hipSuccess) return e;
     if (rm <= 4) {  // the rest of the segment in one launch
       Product x{XT, A, sp.x, sp.mm, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
       if (left > 0) {
@@ -881,7 +1014,7 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
       // Both in one launch while that is one round of workgroups (4096 x 4096,
       // 136 + 136 tiles of 256: 540 us together, 488 one after the other).
       const bool pair = tile_count<kSym>(8, n, rm, rm) <= 128;
-      e = launch_product<kSym>(u, i > 1 && pair ? &qq : nullptr, none, n, rm, rm, 2 * rm, s);
+      e = launch_product<kSym>(u, i > 1 && pair ? &qq : nullptr, none, n, rm, rm, 2 * rm, flip, s);
       if (e == hipSuccess && i > 1 && !pair) e = sym(qq);
       if (e != hipSuccess) return e;
       if (i > 1) std::swap(q, q2);
@@ -897,7 +1030,7 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     // caller's matrix has its rows at i and its columns at j.
     Product x{XT, q, sp.x, sp.mm, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
     if (left > 0) {
-      e = launch_product<kOperand>(x, nullptr, none, n, rk, rm, 2 * rm, s);
+      e = launch_product<kOperand>(x, nullptr, none, n, rk, rm, 2 * rm, flip, s);
       std::swap(XT, XT2);
     } else {
       x.alpha = 1.f / (kScaleP * kScaleX);
@@ -907,8 +1040,8 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
       }
       const int ra = tall ? rk : rm, rb = tall ? rm : rk;
       e = wm.bf16 && mom != nullptr
-              ? launch_product<kOut, 1>(x, nullptr, out, n, ra, rb, 2 * rm, s)
-              : launch_product<kOut>(x, nullptr, out, n, ra, rb, 2 * rm, s);
+              ? launch_product<kOut, 1>(x, nullptr, out, n, ra, rb, 2 * rm, flip, s)
+              : launch_product<kOut>(x, nullptr, out, n, ra, rb, 2 * rm, flip, s);
     }
     if (e != hipSuccess) return e;
   }
