@@ -345,11 +345,13 @@ __device__ __forceinline__ bool find_tile(int n, int ra, int rb, int flip, Tile&
 
 // Register groups q0 .. q0 + NQ - 1 of one 32 x 32 block (ib, jb): acc[q][s]
 // of lane l is row 8 (q0 + q) + 4 (l / 32) + s of the a block and row l % 32
-// of the b block. mirror: kSym, a tile off the diagonal.
+// of the b block. kSym: blocks above the diagonal are left to their mirror
+// images.
 template <int EPI, int NQ>
 __device__ __forceinline__ void store_block(const Product& p, const Out& o, int mat, int ra,
-                                            int rb, int ib, int jb, bool mirror, int q0,
+                                            int rb, int ib, int jb, int q0,
                                             const float (&acc)[NQ][4], int lane) {
+  if (EPI == kSym && ib < jb) return;
   const int half = lane >> 5, l32 = lane & 31;
   if constexpr (EPI == kOut) {
     const bool whole = (ib + 1) * 32 <= o.rows && (jb + 1) * 32 <= o.cols;
@@ -451,7 +453,7 @@ __device__ __forceinline__ void store_block(const Product& p, const Out& o, int 
       }
       Parts w = split4(v);
       store_parts(p.out_t + mat * p.so + frag(q), slot(q), 4 * half, w);
-      if (EPI == kOperand || mirror) {
+      if (EPI == kOperand || ib != jb) {
         // Operand with rows i, its depth j.
         w.hi = transpose4(w.hi, lane & 3);
         w.lo = transpose4(w.lo, lane & 3);
@@ -528,57 +530,76 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
-  // Fragments of half a step: WM of a, then WN of b, two each: [hi, lo] of
-  // one slice, or hi of two slices.
-  constexpr int NF = 2 * (WM + WN), NM = (PARTS == 2 ? 3 : 2) * WM * WN;
-  f16x8 fr[2][NF];
-  auto read = [&](int f, int kt, int ks) {
-    const int blk = f / 2 < WM ? wr * WM + f / 2 : BA + wc * WN + f / 2 - WM;
-    fr[ks][f] = *reinterpret_cast<const f16x8*>(smem + (kt & 1) * kStage + blk * 4096 + ks * 2048 +
-                                                (f & 1) * 1024 + lane * 16);
-  };
-  // Products of half a step, of a slice in the order lo hi, hi lo, hi hi;
-  // `side(x)` for x in [0, n) is spread between them.
-  auto multiply = [&](int ks, int n, auto side) {
+  // The K loop over the wave's first NJ block columns.
+  auto run = [&](auto nj_c) {
+    constexpr int NJ = decltype(nj_c)::value;
+    // Fragments of half a step: WM of a, then NJ of b, two each: [hi, lo] of
+    // one slice, or hi of two slices.
+    constexpr int NF = NJ > 0 ? 2 * (WM + NJ) : 0, NM = (PARTS == 2 ? 3 : 2) * WM * NJ;
+    f16x8 fr[2][NF > 0 ? NF : 1];
+    auto read = [&](int f, int kt, int ks) {
+      const int blk = f / 2 < WM ? wr * WM + f / 2 : BA + wc * WN + f / 2 - WM;
+      fr[ks][f] = *reinterpret_cast<const f16x8*>(smem + (kt & 1) * kStage + blk * 4096 +
+                                                  ks * 2048 + (f & 1) * 1024 + lane * 16);
+    };
+    // Products of half a step, of a slice in the order lo hi, hi lo, hi hi;
+    // `side(x)` for x in [0, n) is spread between them.
+    auto multiply = [&](int ks, int n, auto side) {
+      if constexpr (NM == 0) {
 #pragma unroll
-    for (int x = 0; x < NM; ++x) {
-      const int q = x / (WM * WN), i = x / WN % WM, j = x % WN;
+        for (int y = 0; y < n; ++y) side(y);
+      }
 #pragma unroll
-      for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
-      __builtin_amdgcn_sched_barrier(0);
-      const int qa = PARTS == 2 ? q == 0 : q, qb = PARTS == 2 ? q == 1 : q;
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + qa],
-                                                         fr[ks][2 * (WM + j) + qb], acc[i][j], 0,
-                                                         0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
+      for (int x = 0; x < NM; ++x) {
+        const int q = x / (WM * NJ), i = x / NJ % WM, j = x % NJ;
 #pragma unroll
-  for (int i = 0; i < NC; ++i) copy(i, 0);
+        for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
+        __builtin_amdgcn_sched_barrier(0);
+        const int qa = PARTS == 2 ? q == 0 : q, qb = PARTS == 2 ? q == 1 : q;
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + qa],
+                                                           fr[ks][2 * (WM + j) + qb], acc[i][j],
+                                                           0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
 #pragma unroll
-  for (int i = 0; i < NC; ++i) copy(i, 1);
-  __builtin_amdgcn_s_waitcnt(vmcnt_imm(NC));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");  // no LDS read moves above the barrier
+    for (int i = 0; i < NC; ++i) copy(i, 0);
 #pragma unroll
-  for (int f = 0; f < NF; ++f) read(f, 0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    // First slice, with the reads of the second in between.
-    multiply(0, NF, [&](int f) { read(f, kt, 1); });
-    // This wave's reads of the step's slot are done and its copies of the
-    // next step have landed; after the barrier every wave's. The slot takes
-    // step kt + 2, a whole step before it is needed, while the second slice
-    // is multiplied and the next step's first slice is read.
-    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+    for (int i = 0; i < NC; ++i) copy(i, 1);
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(NC));
     __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    multiply(1, NF + NC, [&](int y) {
-      if (y < NF)
-        read(y, kt + 1, 0);
-      else
-        copy(y - NF, kt + 2);
-    });
-  }
+    asm volatile("" ::: "memory");  // no LDS read moves above the barrier
+#pragma unroll
+    for (int f = 0; f < NF; ++f) read(f, 0, 0);
+    for (int kt = 0; kt < nk; ++kt) {
+      // First slice, with the reads of the second in between.
+      multiply(0, NF, [&](int f) { read(f, kt, 1); });
+      // This wave's reads of the step's slot are done and its copies of the
+      // next step have landed; after the barrier every wave's. The slot takes
+      // step kt + 2, a whole step before it is needed, while the second slice
+      // is multiplied and the next step's first slice is read.
+      __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      multiply(1, NF + NC, [&](int y) {
+        if (y < NF)
+          read(y, kt + 1, 0);
+        else
+          copy(y - NF, kt + 2);
+      });
+    }
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);  // no copy is left when the wave ends
+  };
+  // Symmetric results, tiles on the diagonal: a wave whose blocks all lie above
+  // it only copies, one whose second half does leaves that out. The card's
+  // clock is bound by its power here, so work left out is time.
+  const int above = EPI == kSym && a0 == b0 ? wr * WM + WM - 1 : BB;  // last row block
+  if (EPI == kSym && wc * WN > above)
+    run(std::integral_constant<int, 0>{});
+  else if (EPI == kSym && WN == 4 && wc * WN + WN / 2 > above)
+    run(std::integral_constant<int, EPI == kSym && WN == 4 ? WN / 2 : WN>{});
+  else
+    run(std::integral_constant<int, WN>{});
 
 #pragma unroll
   for (int i = 0; i < WM; ++i) {
@@ -591,7 +612,7 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
       float v[4][4];
 #pragma unroll
       for (int r = 0; r < 16; ++r) v[r / 4][r % 4] = acc[i][j][r];
-      store_block<EPI, 4>(p, o, mat, ra, rb, ib, jb, a0 != b0, 0, v, lane);
+      store_block<EPI, 4>(p, o, mat, ra, rb, ib, jb, 0, v, lane);
     }
   }
 }
@@ -681,7 +702,7 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
 #pragma unroll
       for (int w = 0; w < 8; ++w) v[q][s] += part[w][b][q0 + q][lane][s];
     }
-  store_block<EPI, 2>(p, o, t.mat, ra, rb, ib, jb, t.a0 != t.b0, q0, v, lane);
+  store_block<EPI, 2>(p, o, t.mat, ra, rb, ib, jb, q0, v, lane);
 }
 
 // ---- short sides up to 128: a segment after its Gram product in one launch ------
@@ -811,7 +832,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
 #pragma unroll
     for (int r = 0; r < 16; ++r) v[r / 4][r % 4] = acc[r];
     store_block<EPI, 4>(p, o, mat, SWAP ? MB : rk, SWAP ? rk : MB, SWAP ? qb : xb, SWAP ? xb : qb,
-                        false, 0, v, lane);
+                        0, v, lane);
   }
 }
 
