@@ -497,7 +497,11 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
   const int mat = t.mat, a0 = t.a0, b0 = t.b0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wr = wave / WC, wc = wave % WC;
+  // Eight waves: waves w and w + 4 share a SIMD; their regions are paired so
+  // that on diagonal tiles, where regions 0 and 5 are half and 1 and 3 not
+  // computed, no SIMD has more than one and a half.
+  const int region = NW == 8 ? (0x31507642 >> (4 * wave)) & 7 : wave;
+  const int wr = region / WC, wc = region % WC;
 
   // ---- copies: a step is 4 (BA + BB) pieces of 1 KB, four a row block; each
   // wave copies NC of them, all of one operand ----
