@@ -497,10 +497,11 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
   const int mat = t.mat, a0 = t.a0, b0 = t.b0;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Eight waves: waves w and w + 4 share a SIMD; their regions are paired so
-  // that on diagonal tiles, where regions 0 and 5 are half and 1 and 3 not
+  // Waves w and w + 4 share a SIMD; their regions are paired so that on
+  // diagonal tiles of 256, where regions 0 and 5 are half and 1 and 3 not
   // computed, no SIMD has more than one and a half.
-  const int region = NW == 8 ? (0x31507642 >> (4 * wave)) & 7 : wave;
+  static_assert(NW == 8, "eight regions");
+  const int region = (0x31507642 >> (4 * wave)) & 7;
   const int wr = region / WC, wc = region % WC;
 
   // ---- copies: a step is 4 (BA + BB) pieces of 1 KB, four a row block; each
@@ -552,18 +553,19 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
       if constexpr (NM == 0) {
 #pragma unroll
         for (int y = 0; y < n; ++y) side(y);
-      }
+      } else {
 #pragma unroll
-      for (int x = 0; x < NM; ++x) {
-        const int q = x / (WM * NJ), i = x / NJ % WM, j = x % NJ;
+        for (int x = 0; x < NM; ++x) {
+          const int q = x / (WM * NJ), i = x / NJ % WM, j = x % NJ;
 #pragma unroll
-        for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
-        __builtin_amdgcn_sched_barrier(0);
-        const int qa = PARTS == 2 ? q == 0 : q, qb = PARTS == 2 ? q == 1 : q;
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + qa],
-                                                           fr[ks][2 * (WM + j) + qb], acc[i][j],
-                                                           0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
+          for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
+          __builtin_amdgcn_sched_barrier(0);
+          const int qa = PARTS == 2 ? q == 0 : q, qb = PARTS == 2 ? q == 1 : q;
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + qa],
+                                                             fr[ks][2 * (WM + j) + qb], acc[i][j],
+                                                             0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     };
 #pragma unroll
@@ -894,7 +896,8 @@ int64_t tile_count(int B, int n, int ra, int rb) {
 }
 
 // Tile shapes: 64 x 64 with the depth split over the waves, 128 x 128 (two
-// workgroups a CU), 256 x 256 (one). Measured, whole calls (small / 128 / 256):
+// workgroups a CU; eight waves each: 16 x 500 x 1500 395 us, with four 405),
+// 256 x 256 (one). Measured, whole calls (small / 128 / 256):
 // 2 x 1024^2 (72 tiles of 128) 384 / 455 / - us; 2048^2 (136) 1052 / 913 / -;
 // 16 x 1024 x 2048 (576) 2410 / 2090 / 2047; 4096 x 14336 (528) 9998 / 8003 /
 // 7640. So: the small tiles up to half a 128-tile a CU, 128-tiles while one
@@ -919,7 +922,7 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
   if (t128 <= kSmallTiles || t64 <= 2 * t128)
     orth_product_small_kernel<EPI><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) || 16 * t256 > 5 * t128)
-    orth_product_kernel<EPI, PARTS, 2, 2, 2, 2><<<grid(4), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
+    orth_product_kernel<EPI, PARTS, 2, 1, 2, 4><<<grid(4), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
     orth_product_kernel<EPI, PARTS, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   return hipGetLastError();
