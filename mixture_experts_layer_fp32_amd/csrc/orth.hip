@@ -629,22 +629,13 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 // buffers of two slices), so there is no barrier until the waves' sums meet
 // in LDS, and the time is that of a few loads. Also the more exact sum: eight
 // parts instead of one chain.
-template <int EPI>
-__global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Product p1, Out o,
-                                                                 int n, int ra, int rb, int KS) {
-  __shared__ __attribute__((aligned(16))) float part[8][4][4][64][4];  // wave, block, q, lane
-  const Product& p = blockIdx.y == 0 ? p0 : p1;
-  Tile t;
-  if (!find_tile<EPI, 2, 2>(n, ra, rb, p.flip, t)) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // Row blocks past the last read the last one again (they are not stored).
-  const uint16_t* src[4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    src[i] = p.a + t.mat * p.sa + static_cast<int64_t>(min(t.a0 + i, ra - 1)) * KS * 1024 + lane * 8;
-    src[2 + i] = p.b + t.mat * p.sb + static_cast<int64_t>(min(t.b0 + i, rb - 1)) * KS * 1024 + lane * 8;
-  }
+
+// Slices [ks0, ks1) of the tile whose operand blocks (two of a, two of b; this
+// lane's values) begin at src. v: register groups 2 (wave % 2) and the next of
+// block wave / 2, summed over the waves.
+typedef float SmallSums[8][4][4][64][4];  // wave, block, register group, lane
+__device__ __forceinline__ void small_tile(const uint16_t* const (&src)[4], int ks0, int ks1,
+                                           int wave, int lane, SmallSums& part, float (&v)[2][4]) {
   f32x16 acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -656,19 +647,19 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
   auto load = [&](int buf, int ks) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (ks + 8 * u < KS) {
+      if (ks + 8 * u < ks1) {
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
-            fr[buf][u][b][q] =
-                *reinterpret_cast<const f16x8*>(src[b] + static_cast<int64_t>(ks + 8 * u) * 1024 + q * 512);
+            fr[buf][u][b][q] = *reinterpret_cast<const f16x8*>(
+                src[b] + static_cast<int64_t>(ks + 8 * u) * 1024 + q * 512);
       }
   };
   auto multiply = [&](int buf, int ks) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (ks + 8 * u < KS) {
+      if (ks + 8 * u < ks1) {
 #pragma unroll
         for (int q = 0; q < 3; ++q)
 #pragma unroll
@@ -679,9 +670,9 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
                   fr[buf][u][i][q == 0], fr[buf][u][2 + j][q == 1], acc[i][j], 0, 0, 0);
       }
   };
-  load(0, wave);
-  load(1, wave + 16);
-  for (int ks = wave; ks < KS; ks += 32) {
+  load(0, ks0 + wave);
+  load(1, ks0 + wave + 16);
+  for (int ks = ks0 + wave; ks < ks1; ks += 32) {
     multiply(0, ks);
     load(0, ks + 32);
     multiply(1, ks + 16);
@@ -695,11 +686,7 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
           make_float4(acc[b / 2][b % 2][4 * q], acc[b / 2][b % 2][4 * q + 1],
                       acc[b / 2][b % 2][4 * q + 2], acc[b / 2][b % 2][4 * q + 3]);
   __syncthreads();
-  // Wave w sums and stores half of block w / 2.
   const int b = wave / 2, q0 = 2 * (wave & 1);
-  const int ib = t.a0 + b / 2, jb = t.b0 + b % 2;
-  if (ib >= ra || jb >= rb) return;
-  float v[2][4];
 #pragma unroll
   for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -708,11 +695,61 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
 #pragma unroll
       for (int w = 0; w < 8; ++w) v[q][s] += part[w][b][q0 + q][lane][s];
     }
-  store_block<EPI, 2>(p, o, t.mat, ra, rb, ib, jb, q0, v, lane);
 }
 
-// ---- short sides up to 128: a segment after its Gram product in one launch ------
-// Every workgroup holds A and P of its matrix in LDS (MB 32-row blocks, at
+template <int EPI>
+__global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Product p1, Out o,
+                                                                 int n, int ra, int rb, int KS) {
+  __shared__ __attribute__((aligned(16))) SmallSums part;
+  const Product& p = blockIdx.y == 0 ? p0 : p1;
+  Tile t;
+  if (!find_tile<EPI, 2, 2>(n, ra, rb, p.flip, t)) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // Row blocks past the last read the last one again (they are not stored).
+  const uint16_t* src[4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    src[i] = p.a + t.mat * p.sa + static_cast<int64_t>(min(t.a0 + i, ra - 1)) * KS * 1024 + lane * 8;
+    src[2 + i] = p.b + t.mat * p.sb + static_cast<int64_t>(min(t.b0 + i, rb - 1)) * KS * 1024 + lane * 8;
+  }
+  float v[2][4];
+  small_tile(src, 0, KS, wave, lane, part, v);
+  const int ib = t.a0 + wave / 4, jb = t.b0 + wave / 2 % 2;
+  if (ib >= ra || jb >= rb) return;
+  store_block<EPI, 2>(p, o, t.mat, ra, rb, ib, jb, 2 * (wave & 1), v, lane);
+}
+
+// ---- short sides up to 128 -------------------------------------------------------
+// X X^T of matrices with at most four row blocks: one or three 64 x 64 tiles,
+// the depth split over the workgroups too. Sums in fp32, for the next kernel:
+// gram[matrix][split][tile][wave][2][lane][4].
+constexpr int kGramTile = 4096;  // floats
+__global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restrict__ x, int64_t sx,
+                                                        int rm, int KS, int tiles, int splits,
+                                                        float* __restrict__ gram) {
+  __shared__ __attribute__((aligned(16))) SmallSums part;
+  const int sp = blockIdx.x / tiles, tile = blockIdx.x % tiles, mat = blockIdx.y;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int a0 = tile == 0 ? 0 : 2, b0 = tile == 2 ? 2 : 0;  // (0, 0), (2, 0), (2, 2)
+  const uint16_t* src[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int rb = min((i < 2 ? a0 : b0) + (i & 1), rm - 1);
+    src[i] = x + mat * sx + static_cast<int64_t>(rb) * KS * 1024 + lane * 8;
+  }
+  float v[2][4];
+  small_tile(src, KS * sp / splits, KS * (sp + 1) / splits, wave, lane, part, v);
+  float* out = gram + ((static_cast<int64_t>(mat) * splits + sp) * tiles + tile) * kGramTile +
+               wave * 512 + lane * 4;
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+    *reinterpret_cast<float4*>(out + q * 256) = make_float4(v[q][0], v[q][1], v[q][2], v[q][3]);
+}
+
+// The rest of a segment in one launch. Every workgroup adds up the Gram
+// product's parts, holds A and P of its matrix in LDS (MB 32-row blocks, at
 // most 64 KB each), takes the segment's steps (1 or 2) there, and multiplies
 // its share of X: group g of XB 32-row blocks of X^T, g = blockIdx.x,
 // blockIdx.x + gridDim.x, ... The steps are repeated by every workgroup of a
@@ -721,13 +758,15 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
 // diagonal (10 of 16 waves for MB = 4, at most 3 on a SIMD).
 // SWAP: the result's rows are those of Q (kOut of a wide matrix).
 template <int MB, int EPI, bool SWAP>
-__global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk) {
+__global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk,
+                                                          const float* __restrict__ gram,
+                                                          int splits) {
   constexpr int KS = 2 * MB, MP = MB == 3 ? 4 : MB, XB = 16 / MP;
   constexpr int kOp = MB * KS * 1024;  // values of an operand
   __shared__ __attribute__((aligned(16))) uint16_t bufs[2][kOp];
   uint16_t *ba = bufs[0], *bp = bufs[1];
-  const int mat = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int mat = blockIdx.y, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   auto frag = [&](const uint16_t* op, int rb, int ks, int part) {
     return *reinterpret_cast<const f16x8*>(op + ((rb * KS + ks) * 2 + part) * 512 + lane * 8);
@@ -753,10 +792,6 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       for (int q = 0; q < 2; ++q)
         x[ks][q] = *reinterpret_cast<const f16x8*>(src + (ks * 2 + q) * 512);
   };
-  for (int i = tid; i < kOp / 8; i += 1024)
-    reinterpret_cast<uint4*>(ba)[i] = reinterpret_cast<const uint4*>(p.b + mat * p.sb)[i];
-  __syncthreads();
-
   // Block (ib, jb), jb <= ib, of the m x m results: wave 0 (0, 0), 1 (1, 0),
   // 2 (1, 1), 3 (2, 0), ...
   const int ib = wave >= 6 ? 3 : wave >= 3 ? 2 : wave >= 1 ? 1 : 0, jb = wave - ib * (ib + 1) / 2;
@@ -805,6 +840,28 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       }
     }
   };
+  {  // A, from register group 2 h + q of block b in wave 2 b + h of its tile
+    constexpr int TILES = MB > 2 ? 3 : 1;
+    const int tile = ib / 2 * (ib / 2 + 1) / 2 + jb / 2, b = 2 * (ib & 1) + (jb & 1);
+    const float* g = gram + (static_cast<int64_t>(mat) * splits * TILES + tile) * kGramTile +
+                     b * 1024 + lane * 4;
+    zero();
+    if (mine) {
+#pragma unroll 4
+      for (int sp = 0; sp < splits; ++sp, g += TILES * kGramTile) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 f = *reinterpret_cast<const float4*>(g + q * 256);
+          acc[4 * q] += f.x;
+          acc[4 * q + 1] += f.y;
+          acc[4 * q + 2] += f.z;
+          acc[4 * q + 3] += f.w;
+        }
+      }
+    }
+    store(ba, kScaleA / (kScaleX * kScaleX));
+    __syncthreads();
+  }
   // P = f(A, A^2); with two steps then U = A P and A_2 = U P, each over its
   // first factor, P_2 over A_2, and Q = P_2 P over P. One copy of the code:
   // it runs once a launch, so its size is time (fetching instructions).
@@ -845,9 +902,12 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
 int ceil32(int v) { return (v + 31) / 32; }
 
 // Workspace, in values (16 bits) per matrix: X and two X^T (or the other way
-// round for tall matrices), five m x m operands; then the norm's partials.
+// round for tall matrices); five m x m operands, or, for short sides up to
+// 128, the Gram product's parts; then the norm's partials.
 struct Space {
   int64_t x, mm;  // values of one X operand, of one m x m operand
+  int tiles, splits;  // short sides up to 128: Gram tiles, depth splits
+  int64_t gram;   // floats
   int64_t part;   // partial sums per matrix
   size_t bytes;
 };
@@ -855,12 +915,21 @@ int norm_parts(int64_t values) {
   return static_cast<int>(std::min<int64_t>(1024, (values + 8191) / 8192));
 }
 Space space(int n, int rows, int cols) {
-  Space s;
+  Space s{};
   const int64_t m = ceil32(std::min(rows, cols)), k = ceil32(std::max(rows, cols));
   s.x = m * 2 * k * 1024;
-  s.mm = m * 2 * m * 1024;
+  if (m <= 4) {
+    // A workgroup a CU, at least 16 slices each (two a wave).
+    s.tiles = m > 2 ? 3 : 1;
+    const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, 2 * k / 16));
+    s.splits = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(most, 256 / (static_cast<int64_t>(std::max(n, 1)) * s.tiles))));
+    s.gram = static_cast<int64_t>(s.tiles) * s.splits * kGramTile;
+  } else {
+    s.mm = m * 2 * m * 1024;
+  }
   s.part = norm_parts(static_cast<int64_t>(rows) * cols);
-  s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.part * 8);
+  s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.gram * 4 + s.part * 8);
   return s;
 }
 
@@ -928,17 +997,19 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
   return hipGetLastError();
 }
 
-// p.a: X^T, p.b: A (after the Gram product).
+// p.a: X^T; after orth_gram_kernel.
 template <int EPI, bool SWAP>
 hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm, int rk,
-                        hipStream_t s) {
+                        const float* gram, int splits, hipStream_t s) {
   const int xb = rm == 1 ? 16 : rm == 2 ? 8 : 4;
   const dim3 grid(std::min((rk + xb - 1) / xb, std::max(1, 256 / n)), n);
   switch (rm) {
-    case 1: orth_steps_kernel<1, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
-    case 2: orth_steps_kernel<2, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
-    case 3: orth_steps_kernel<3, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
-    default: orth_steps_kernel<4, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk); break;
+    case 1:
+      orth_steps_kernel<1, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits);
+      break;
+    case 2: orth_steps_kernel<2, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits); break;
+    case 3: orth_steps_kernel<3, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits); break;
+    default: orth_steps_kernel<4, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits); break;
   }
   return hipGetLastError();
 }
@@ -967,6 +1038,7 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
   uint16_t *X = take(sp.x), *XT = take(sp.x), *XT2 = take(sp.x);
   uint16_t *A = take(sp.mm), *U = take(sp.mm), *P = take(sp.mm), *Q = take(sp.mm),
            *Q2 = take(sp.mm);
+  float* gram = reinterpret_cast<float*>(take(2 * sp.gram));
   double* part = reinterpret_cast<double*>(base);
 
   const Mats gm{g.data, g.ld, g.stride, g.dtype == MOE_BF16};
@@ -1015,22 +1087,24 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
   for (bool first = true; left > 0; first = false) {
     const int L = std::min(left, first ? seg.first : seg.later);
     left -= L;
-    Product gram{X, X, sp.x, sp.x, A, A, sp.mm, nullptr, kScaleA / (kScaleX * kScaleX), 0.f, 0.f};
-    e = launch_product<kSym>(gram, nullptr, none, n, rm, rm, 2 * rk, flip, s);
-    if (e != hipSuccess) return e;
-    if (rm <= 4) {  // the rest of the segment in one launch
-      Product x{XT, A, sp.x, sp.mm, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
+    if (rm <= 4) {
+      orth_gram_kernel<<<dim3(sp.tiles * sp.splits, n), 512, 0, s>>>(X, sp.x, rm, 2 * rk, sp.tiles,
+                                                                     sp.splits, gram);
+      Product x{XT, nullptr, sp.x, 0, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
       if (left > 0) {
-        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, s);
+        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, gram, sp.splits, s);
         std::swap(XT, XT2);
       } else {
         x.alpha = 1.f / (kScaleP * kScaleX);
-        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, s)
-                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, s);
+        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, gram, sp.splits, s)
+                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, gram, sp.splits, s);
       }
       if (e != hipSuccess) return e;
       continue;
     }
+    Product gram_p{X, X, sp.x, sp.x, A, A, sp.mm, nullptr, kScaleA / (kScaleX * kScaleX), 0.f, 0.f};
+    e = launch_product<kSym>(gram_p, nullptr, none, n, rm, rm, 2 * rk, flip, s);
+    if (e != hipSuccess) return e;
     uint16_t *q = Q, *q2 = Q2;
     if ((e = poly(q)) != hipSuccess) return e;
     const uint16_t* pl = q;  // the last P
