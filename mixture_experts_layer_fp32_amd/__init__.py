@@ -27,4 +27,6 @@ from ._binding import (  # noqa: F401
     moe_orthogonalize, moe_orthogonalize_workspace_size, moe_muon_update, moe_matrices,
     moe_muon_desc,
 )
-from .layer import EPRankShareForward, LayerForward, LayerForwardMXFP8, LayerTrain  # noqa: F401
+from .layer import (  # noqa: F401
+    EPRankShareForward, ExpertMuon, LayerForward, LayerForwardMXFP8, LayerTrain,
+)

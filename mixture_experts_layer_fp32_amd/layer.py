@@ -17,7 +17,16 @@ and shared experts from ``moe_expert_ffn_train``), and its backward through
 ``moe_layer_backward`` (include/moe_backward.h): the input gradient and the
 router, expert and shared-expert weight gradients. Without ``save_gu`` the
 backward recomputes G | U: the same gradients, bit for bit, for
-T top_k 2I 4 bytes less memory held between the two passes.
+T top_k 2I 4 bytes less memory held between the two passes. With ``norm=True``
+it is the pre-norm block out = x + layer(layer_norm(x)): the forward
+normalises first (``moe_layer_norm``, include/moe_norm.h) and the residual stays
+x; the backward runs the layer's pieces, then ``moe_layer_norm_backward``, which
+joins the residual's gradient in.
+
+``ExpertMuon`` steps the expert matrices of a ``LayerTrain`` from its gradients
+(``moe_muon_update``, include/moe_update.h): gate, up and down matrices of every
+expert, and of the shared one, each orthogonalised on its own; it owns the fp32
+momentum and the workspace.
 
 ``EPRankShareForward`` runs the share of one expert-parallel rank out of
 ``ep_size`` logical ranks on this GPU, as a sequence of C calls (page "Expert
@@ -101,7 +110,10 @@ class LayerForward:
 
 class LayerTrain:
     def __init__(self, desc: B.moe_desc, w_router, w_gate_up, w_down, logit_bias=None,
-                 shared_gate_up=None, shared_down=None, device="cuda", save_gu=None):
+                 shared_gate_up=None, shared_down=None, device="cuda", save_gu=None,
+                 norm=False, norm_gamma=None, norm_beta=None, norm_eps=1e-5):
+        """norm: a layer norm in front of the layer; norm_gamma, norm_beta [D]
+        fp32 or None (ones, zeros), their gradients in dnorm_gamma, dnorm_beta."""
         self.d = desc
         T, D, E, k, I, Is = desc.T, desc.D, desc.E, desc.top_k, desc.I, desc.I_shared
         M = T * k
@@ -140,13 +152,41 @@ class LayerTrain:
         self.dw_down = torch.empty(E, I, D, dtype=f32, device=device)
         self.dw_shared_gate_up = torch.empty(D, 2 * Is, dtype=f32, device=device) if Is else None
         self.dw_shared_down = torch.empty(Is, D, dtype=f32, device=device) if Is else None
-        self.ws_bwd = B.workspace(B.moe_backward_workspace_size(desc), device)
         self.x = None
+        self.norm = norm
+        if not norm:
+            if norm_gamma is not None or norm_beta is not None:
+                raise ValueError("norm_gamma, norm_beta: only with norm=True")
+            self.ws_bwd = B.workspace(B.moe_backward_workspace_size(desc), device)
+            return
+        self.norm_gamma, self.norm_beta, self.norm_eps = norm_gamma, norm_beta, norm_eps
+        self.h = torch.empty(T, D, dtype=bf, device=device)
+        self.mean = torch.empty(T, dtype=f32, device=device)
+        self.rstd = torch.empty(T, dtype=f32, device=device)
+        # what the layer's backward leaves between its pieces
+        self.dh = torch.empty(T, D, dtype=bf, device=device)
+        self.dy_perm = torch.empty(M, D, dtype=bf, device=device)
+        self.dx_perm = torch.empty(M, D, dtype=f32, device=device)
+        self.dx_shared = torch.empty(T, D, dtype=f32, device=device) if Is else None
+        self.dlogit = torch.empty(T, k, dtype=f32, device=device)
+        self.dl_perm = torch.empty(max(M, 1), dtype=f32, device=device)
+        self.dnorm_gamma = torch.empty(D, dtype=f32, device=device)
+        self.dnorm_beta = torch.empty(D, dtype=f32, device=device)
+        ffn = B.moe_ffn_backward_workspace_size(desc, I, M)
+        if Is:
+            ffn = max(ffn, B.moe_ffn_backward_workspace_size(desc, Is, T))
+        self.ws_bwd = B.workspace(max(
+            ffn, B.moe_router_backward_workspace_size(desc, M),
+            B.moe_layer_norm_backward_workspace_size(T, D)), device)
 
     def forward(self, x, stream=None):
         d, w = self.d, self.w
         E, I, M = d.E, d.I, d.T * d.top_k
-        self.x = x
+        self.x = res = x
+        if self.norm:
+            B.moe_layer_norm(x, self.norm_gamma, self.norm_beta, self.norm_eps, self.h, self.mean,
+                             self.rstd, stream)
+            x = self.h
         B.moe_route(d, x, w["w_router"], w["logit_bias"], None, None, self.topk_idx, self.topk_w,
                     ws=self.ws_route, stream=stream)
         B.moe_permute(d, x, self.topk_idx, 0, E, M, self.counts, self.offsets, self.split,
@@ -165,11 +205,37 @@ class LayerTrain:
             else:
                 B.moe_expert_ffn(d, 1, d.I_shared, d.T, x, None, w["shared_gate_up"],
                                  w["shared_down"], self.shared_out, self.ws_sh, stream)
-        B.moe_unpermute_combine(d, self.y_perm, self.pos, self.topk_w, x, self.shared_out, 0, d.T,
-                                self.out, stream)
+        B.moe_unpermute_combine(d, self.y_perm, self.pos, self.topk_w, res, self.shared_out, 0,
+                                d.T, self.out, stream)
         return self.out
 
+    def _backward_norm(self, dout, stream):
+        d, w, ws = self.d, self.w, self.ws_bwd
+        E, I, M = d.E, d.I, d.T * d.top_k
+        B.moe_combine_backward(d, dout, self.y_perm, self.pos, self.topk_w, self.dy_perm, None,
+                               self.dlogit, self.dl_perm, stream)
+        B.moe_expert_ffn_backward(d, E, I, M, self.x_perm, self.offsets, w["w_gate_up"],
+                                  w["w_down"], self.dy_perm, self.dx_perm, self.dw_gate_up,
+                                  self.dw_down, ws, stream, gu_saved=self.gu)
+        if self.dx_shared is not None:
+            gate_up, down, dgate_up, ddown = (
+                t[None] for t in (w["shared_gate_up"], w["shared_down"], self.dw_shared_gate_up,
+                                  self.dw_shared_down))
+            B.moe_expert_ffn_backward(d, 1, d.I_shared, d.T, self.h, None, gate_up, down, dout,
+                                      self.dx_shared, dgate_up, ddown, ws, stream,
+                                      gu_saved=self.gu_sh)
+        B.moe_router_backward(d, M, self.x_perm, self.offsets, self.dl_perm, self.dw_router, ws,
+                              stream)
+        # The residual's gradient joins behind the norm, not here.
+        B.moe_input_backward(d, self.dx_perm, self.pos, self.topk_idx, self.dlogit, w["w_router"],
+                             self.dx_shared, None, self.dh, stream)
+        B.moe_layer_norm_backward(self.x, self.dh, self.norm_gamma, self.mean, self.rstd, dout,
+                                  self.dx, self.dnorm_gamma, self.dnorm_beta, ws, stream)
+        return self.dx
+
     def backward(self, dout, stream=None):
+        if self.norm:
+            return self._backward_norm(dout, stream)
         w = self.w
         B.moe_layer_backward(self.d, self.x, w["w_router"], w["w_gate_up"], w["w_down"],
                              w["shared_gate_up"], w["shared_down"], self.topk_idx, self.topk_w,
@@ -178,6 +244,38 @@ class LayerTrain:
                              self.dw_shared_gate_up, self.dw_shared_down, self.ws_bwd, stream,
                              gu_saved=self.gu, gu_shared_saved=self.gu_sh)
         return self.dx
+
+
+class ExpertMuon:
+    """Muon for the expert matrices of a LayerTrain (and its shared expert's):
+    step(lr) updates layer.w in place from layer.dw_*. Each [D, I] gate, [D, I]
+    up and [I, D] down matrix is orthogonalised on its own and scaled by
+    0.2 sqrt(longer side). The router weight and the norm's parameters are
+    the caller's (they are not updated here)."""
+
+    def __init__(self, layer: LayerTrain, mu=0.95, nesterov=True, weight_decay=0.0, steps=5,
+                 eps=1e-7):
+        self.kw = dict(mu=mu, nesterov=nesterov, weight_decay=weight_decay, steps=steps, eps=eps)
+        self.momentum = {}
+        self.batches = []
+        need = 256
+        for w_name, g_name, halves in (("w_gate_up", "dw_gate_up", 2), ("w_down", "dw_down", 1),
+                                       ("shared_gate_up", "dw_shared_gate_up", 2),
+                                       ("shared_down", "dw_shared_down", 1)):
+            w, g = layer.w[w_name], getattr(layer, g_name)
+            if g is None:
+                continue
+            m = self.momentum[w_name] = torch.zeros_like(g)
+            for wv, gv, mv in zip(*(t.chunk(halves, dim=-1) for t in (w, g, m))):
+                n = wv.shape[0] if wv.dim() == 3 else 1
+                rows, cols = wv.shape[-2:]
+                need = max(need, B.moe_orthogonalize_workspace_size(n, rows, cols, steps))
+                self.batches.append((gv, mv, wv, 0.2 * max(rows, cols) ** 0.5))
+        self.ws = B.workspace(need, layer.dx.device)
+
+    def step(self, lr, stream=None):
+        for g, m, w, scale in self.batches:
+            B.moe_muon_update(g, m, w, self.ws, lr=lr, scale=scale, stream=stream, **self.kw)
 
 
 class EPRankShareForward:
