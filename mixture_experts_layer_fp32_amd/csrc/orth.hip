@@ -966,15 +966,15 @@ int64_t tile_count(int B, int n, int ra, int rb) {
 
 // Tile shapes: 64 x 64 with the depth split over the waves, 128 x 128 (two
 // workgroups a CU; eight waves each: 16 x 500 x 1500 395 us, with four 405),
-// 256 x 256 (one). Measured, whole calls (small / 128 / 256):
-// 2 x 1024^2 (72 tiles of 128) 384 / 455 / - us; 2048^2 (136) 1052 / 913 / -;
-// 16 x 1024 x 2048 (576) 2410 / 2090 / 2047; 4096 x 14336 (528) 9998 / 8003 /
-// 7640. So: the small tiles up to half a 128-tile a CU, 128-tiles while one
-// round holds them all (and a little past it at depths up to 1024: 576 tiles
-// 73 us, 82 as 160 of 256), then 256-tiles unless they would compute more than
-// 5/4 of the 128-tiles' area (sides just past a multiple of 256). Small tiles
-// too where 128-tiles would compute twice their area (256 x 64 x 256: 134 us,
-// 157 with 128-tiles).
+// 256 x 256 (one). Measured, whole calls (small / 128 / 256): 2 x 1024^2 (72
+// tiles of 128) 384 / 455 / - us; 2048^2 (136) 1052 / 913 / -; 4096 x 14336
+// (528) 9998 / 8003 / 7640; 32 x 1024^2 (1152) - / 2552 / 2660; 256 x 64 x 256
+// (256, a quarter of each used) 134 / 157 / -. So: small tiles up to half a
+// 128-tile a CU and where 128-tiles would compute twice their area; 128-tiles
+// while one round holds them (and up to 640 at depths up to 1024: 16 x 1024^2,
+// 576, 73 us, 82 as 160 of 256); then whichever takes less by its rounds, one
+// of 256-tiles counting as 1.9 of 128-tiles up to that depth, as 1.7 beyond
+// (4096 x 14336, X <- Q X: 4 rounds 1.21 ms, 7 rounds 1.28).
 template <int EPI, int PARTS = 2>
 hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, int rb, int KS,
                           int& flip, hipStream_t s) {
@@ -990,7 +990,8 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
   const int64_t t256 = tile_count<EPI>(8, n, ra, rb);
   if (t128 <= kSmallTiles || t64 <= 2 * t128)
     orth_product_small_kernel<EPI><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
-  else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) || 16 * t256 > 5 * t128)
+  else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) ||
+           (KS <= 64 ? 19 : 17) * ((t256 + 255) / 256) > 10 * ((t128 + 511) / 512))
     orth_product_kernel<EPI, PARTS, 2, 1, 2, 4><<<grid(4), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
     orth_product_kernel<EPI, PARTS, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
