@@ -75,6 +75,24 @@ def test_orthogonalize(n, rows, cols, g_dtype, out_dtype):
         assert _excess(out[i], ou.orthogonalize(_np(g[i])), HALF[out_dtype]) <= TOL, i
 
 
+# Batches whose products take 128 x 128 tiles (300 and more of them) and
+# 256 x 256 ones (252 of sides that end inside a tile), wide, tall and square;
+# the first, a middle and the last matrix are compared, and that no other row
+# is left unwritten.
+MANY = [(50, 301, 333), (50, 333, 301), (42, 750, 801), (42, 801, 750), (42, 768, 768)]
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("n,rows,cols", MANY)
+def test_many_matrices(n, rows, cols, out_dtype):
+    print(f"[orth] n={n} {rows}x{cols} {out_dtype}", flush=True)
+    g = torch.randn(n, rows, cols, device="cuda", generator=torch.Generator("cuda").manual_seed(n))
+    out = _orth(g, out_dtype)
+    assert torch.isfinite(out).all() and float(out.abs().max()) < 1.3
+    for i in (0, n // 2, n - 1):
+        assert _excess(_np(out[i]), ou.orthogonalize(_np(g[i])), HALF[out_dtype]) <= TOL, i
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7])
 @pytest.mark.parametrize("rows,cols", [(96, 160), (200, 70)])
 def test_steps(rows, cols, steps):
@@ -167,6 +185,27 @@ def test_muon_update(n, rows, cols, g_dtype, w_dtype, nesterov):
                             - 4 * U * np.abs(wi), 0.0)
         # fp32 roundings of lr, scale and decay: 4 units of the update too
         assert np.linalg.norm(excess) <= 0.02 * 1.5 * (TOL + 4 * U * np.sqrt(min(rows, cols)))
+
+
+@pytest.mark.parametrize("n,rows,cols", MANY)
+def test_muon_many_matrices(n, rows, cols):
+    """bf16 weights: the last product's operands are rounded to fp16, an error of
+    at most 2^-11 of |Q| |X| per entry: |Q|_2 <= 11.9, |X|_F <= 1.21 sqrt(m)."""
+    print(f"[muon] n={n} {rows}x{cols}", flush=True)
+    gen = torch.Generator("cuda").manual_seed(n)
+    g, m, w = (torch.randn(n, rows, cols, device="cuda", generator=gen) * s
+               for s in (1e-2, 1e-2, 0.05))
+    w = w.to(BF16)
+    keep = [0, n // 2, n - 1]
+    old = [(_np(g[i]), _np(m[i]), _np(w[i])) for i in keep]
+    kw = dict(lr=0.02, mu=0.9, weight_decay=0.1, scale=1.5)
+    moe.moe_muon_update(g, m, w, _ws(n, rows, cols), **kw)
+    torch.cuda.synchronize()
+    tol = 0.02 * 1.5 * (TOL + 11.9 * 1.21 * np.sqrt(min(rows, cols)) * 2.0 ** -11)
+    for i, (gi, mi, wi) in zip(keep, old):
+        rm, rw = ou.muon_update(gi, mi, wi, **kw)
+        assert np.all(np.abs(_np(m[i]) - rm) <= 3 * U * (np.abs(gi) + np.abs(mi)))
+        assert _excess(_np(w[i]), rw, HALF[BF16] + U) <= tol
 
 
 def test_muon_views_and_no_gradient():
