@@ -911,8 +911,10 @@ struct Space {
   int64_t part;   // partial sums per matrix
   size_t bytes;
 };
-int norm_parts(int64_t values) {
-  return static_cast<int>(std::min<int64_t>(1024, (values + 8191) / 8192));
+int norm_parts(int n, int64_t values) {
+  // Few values: short chunks, whose time is that of a few loads.
+  const int64_t chunk = n * values > (int64_t(1) << 23) ? 8192 : 2048;
+  return static_cast<int>(std::min<int64_t>(1024, (values + chunk - 1) / chunk));
 }
 Space space(int n, int rows, int cols) {
   Space s{};
@@ -928,7 +930,7 @@ Space space(int n, int rows, int cols) {
   } else {
     s.mm = m * 2 * m * 1024;
   }
-  s.part = norm_parts(static_cast<int64_t>(rows) * cols);
+  s.part = norm_parts(n, static_cast<int64_t>(rows) * cols);
   s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.gram * 4 + s.part * 8);
   return s;
 }
