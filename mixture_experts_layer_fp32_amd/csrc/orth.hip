@@ -628,14 +628,18 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 // slice by slice; each wave reads its fragments straight into registers (two
 // buffers of two slices), so there is no barrier until the waves' sums meet
 // in LDS, and the time is that of a few loads. Also the more exact sum: eight
-// parts instead of one chain.
+// parts instead of one chain. With more tiles than CUs four waves a workgroup,
+// two workgroups a CU (6 x 700^2 339 -> 322 us, 64 x 160^2 166 -> 142).
 
 // Slices [ks0, ks1) of the tile whose operand blocks (two of a, two of b; this
-// lane's values) begin at src. v: register groups 2 (wave % 2) and the next of
-// block wave / 2, summed over the waves.
-typedef float SmallSums[8][4][4][64][4];  // wave, block, register group, lane
+// lane's values) begin at src, shared out over NW waves (8 or 4). v: the
+// wave's 16 / NW register groups of block 4 wave / NW, summed over the waves.
+template <int NW>
+using SmallSums = float[NW][4][4][64][4];  // wave, block, register group, lane
+template <int NW>
 __device__ __forceinline__ void small_tile(const uint16_t* const (&src)[4], int ks0, int ks1,
-                                           int wave, int lane, SmallSums& part, float (&v)[2][4]) {
+                                           int wave, int lane, SmallSums<NW>& part,
+                                           float (&v)[16 / NW][4]) {
   f32x16 acc[2][2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -647,19 +651,19 @@ __device__ __forceinline__ void small_tile(const uint16_t* const (&src)[4], int 
   auto load = [&](int buf, int ks) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (ks + 8 * u < ks1) {
+      if (ks + NW * u < ks1) {
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             fr[buf][u][b][q] = *reinterpret_cast<const f16x8*>(
-                src[b] + static_cast<int64_t>(ks + 8 * u) * 1024 + q * 512);
+                src[b] + static_cast<int64_t>(ks + NW * u) * 1024 + q * 512);
       }
   };
   auto multiply = [&](int buf, int ks) {
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      if (ks + 8 * u < ks1) {
+      if (ks + NW * u < ks1) {
 #pragma unroll
         for (int q = 0; q < 3; ++q)
 #pragma unroll
@@ -671,12 +675,12 @@ __device__ __forceinline__ void small_tile(const uint16_t* const (&src)[4], int 
       }
   };
   load(0, ks0 + wave);
-  load(1, ks0 + wave + 16);
-  for (int ks = ks0 + wave; ks < ks1; ks += 32) {
+  load(1, ks0 + wave + 2 * NW);
+  for (int ks = ks0 + wave; ks < ks1; ks += 4 * NW) {
     multiply(0, ks);
-    load(0, ks + 32);
-    multiply(1, ks + 16);
-    load(1, ks + 48);
+    load(0, ks + 4 * NW);
+    multiply(1, ks + 2 * NW);
+    load(1, ks + 6 * NW);
   }
 #pragma unroll
   for (int b = 0; b < 4; ++b)
@@ -686,21 +690,21 @@ __device__ __forceinline__ void small_tile(const uint16_t* const (&src)[4], int 
           make_float4(acc[b / 2][b % 2][4 * q], acc[b / 2][b % 2][4 * q + 1],
                       acc[b / 2][b % 2][4 * q + 2], acc[b / 2][b % 2][4 * q + 3]);
   __syncthreads();
-  const int b = wave / 2, q0 = 2 * (wave & 1);
+  const int b = 4 * wave / NW, q0 = 16 / NW * wave % 4;
 #pragma unroll
-  for (int q = 0; q < 2; ++q)
+  for (int q = 0; q < 16 / NW; ++q)
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       v[q][s] = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) v[q][s] += part[w][b][q0 + q][lane][s];
+      for (int w = 0; w < NW; ++w) v[q][s] += part[w][b][q0 + q][lane][s];
     }
 }
 
-template <int EPI>
-__global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Product p1, Out o,
+template <int EPI, int NW>
+__global__ __launch_bounds__(64 * NW) void orth_product_small_kernel(Product p0, Product p1, Out o,
                                                                  int n, int ra, int rb, int KS) {
-  __shared__ __attribute__((aligned(16))) SmallSums part;
+  __shared__ __attribute__((aligned(16))) SmallSums<NW> part;
   const Product& p = blockIdx.y == 0 ? p0 : p1;
   Tile t;
   if (!find_tile<EPI, 2, 2>(n, ra, rb, p.flip, t)) return;
@@ -713,11 +717,11 @@ __global__ __launch_bounds__(512) void orth_product_small_kernel(Product p0, Pro
     src[i] = p.a + t.mat * p.sa + static_cast<int64_t>(min(t.a0 + i, ra - 1)) * KS * 1024 + lane * 8;
     src[2 + i] = p.b + t.mat * p.sb + static_cast<int64_t>(min(t.b0 + i, rb - 1)) * KS * 1024 + lane * 8;
   }
-  float v[2][4];
-  small_tile(src, 0, KS, wave, lane, part, v);
-  const int ib = t.a0 + wave / 4, jb = t.b0 + wave / 2 % 2;
+  float v[16 / NW][4];
+  small_tile<NW>(src, 0, KS, wave, lane, part, v);
+  const int b = 4 * wave / NW, ib = t.a0 + b / 2, jb = t.b0 + b % 2;
   if (ib >= ra || jb >= rb) return;
-  store_block<EPI, 2>(p, o, t.mat, ra, rb, ib, jb, 2 * (wave & 1), v, lane);
+  store_block<EPI, 16 / NW>(p, o, t.mat, ra, rb, ib, jb, 16 / NW * wave % 4, v, lane);
 }
 
 // ---- short sides up to 128 -------------------------------------------------------
@@ -728,7 +732,7 @@ constexpr int kGramTile = 4096;  // floats
 __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restrict__ x, int64_t sx,
                                                         int rm, int KS, int tiles, int splits,
                                                         float* __restrict__ gram) {
-  __shared__ __attribute__((aligned(16))) SmallSums part;
+  __shared__ __attribute__((aligned(16))) SmallSums<8> part;
   const int sp = blockIdx.x / tiles, tile = blockIdx.x % tiles, mat = blockIdx.y;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -740,7 +744,7 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
     src[i] = x + mat * sx + static_cast<int64_t>(rb) * KS * 1024 + lane * 8;
   }
   float v[2][4];
-  small_tile(src, KS * sp / splits, KS * (sp + 1) / splits, wave, lane, part, v);
+  small_tile<8>(src, KS * sp / splits, KS * (sp + 1) / splits, wave, lane, part, v);
   float* out = gram + ((static_cast<int64_t>(mat) * splits + sp) * tiles + tile) * kGramTile +
                wave * 512 + lane * 4;
 #pragma unroll
@@ -990,9 +994,12 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
   const Product& q = p1 ? *p1 : p0;
   const int64_t t64 = tile_count<EPI>(2, n, ra, rb), t128 = tile_count<EPI>(4, n, ra, rb);
   const int64_t t256 = tile_count<EPI>(8, n, ra, rb);
-  if (t128 <= kSmallTiles || t64 <= 2 * t128)
-    orth_product_small_kernel<EPI><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
-  else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) ||
+  if (t128 <= kSmallTiles || t64 <= 2 * t128) {
+    if (t64 * (p1 ? 2 : 1) <= 256)
+      orth_product_small_kernel<EPI, 8><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
+    else
+      orth_product_small_kernel<EPI, 4><<<grid(2), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
+  } else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) ||
            (KS <= 64 ? 19 : 17) * ((t256 + 255) / 256) > 10 * ((t128 + 511) / 512))
     orth_product_kernel<EPI, PARTS, 2, 1, 2, 4><<<grid(4), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
