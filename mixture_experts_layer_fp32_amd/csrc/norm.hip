@@ -502,27 +502,29 @@ __global__ __launch_bounds__(256) void norm_param_kernel(const T* __restrict__ x
   part[(static_cast<int64_t>(gridDim.y) + blockIdx.y) * D + c] = db;
 }
 
-// dgamma (blockIdx.y 0) and dbeta (1): the P partial rows added in row order
-// per wave, then the waves in order. P == 0 writes zeros.
-constexpr int kFinishWaves = 16;
-__global__ __launch_bounds__(64 * kFinishWaves) void norm_finish_kernel(
+// dgamma (blockIdx.y 0) and dbeta (1): 32 columns a workgroup, the P partial
+// rows shared out over 32 half waves, each adding its own in row order, then
+// the half waves in order. P == 0 writes zeros.
+constexpr int kFinishCols = 32, kFinishRows = 32;
+__global__ __launch_bounds__(kFinishCols * kFinishRows) void norm_finish_kernel(
     const float* __restrict__ part, int P, int D, float* __restrict__ dgamma,
     float* __restrict__ dbeta) {
-  __shared__ float red[kFinishWaves][64];
+  __shared__ float red[kFinishRows][kFinishCols];
   float* out = blockIdx.y == 0 ? dgamma : dbeta;
   if (out == nullptr) return;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), w = threadIdx.x >> 6;
+  const int t = threadIdx.x % kFinishCols, w = threadIdx.x / kFinishCols;
+  const int c = blockIdx.x * kFinishCols + t;
   const float* p = part + static_cast<int64_t>(blockIdx.y) * P * D;
   float s = 0.f;
   if (c < D) {
 #pragma unroll 8
-    for (int q = w; q < P; q += kFinishWaves) s += p[static_cast<int64_t>(q) * D + c];
+    for (int q = w; q < P; q += kFinishRows) s += p[static_cast<int64_t>(q) * D + c];
   }
-  red[w][threadIdx.x & 63] = s;
+  red[w][t] = s;
   __syncthreads();
   if (w == 0 && c < D) {
 #pragma unroll
-    for (int q = 1; q < kFinishWaves; ++q) s += red[q][threadIdx.x];
+    for (int q = 1; q < kFinishRows; ++q) s += red[q][t];
     out[c] = s;
   }
 }
@@ -644,7 +646,8 @@ hipError_t launch_norm_bwd(bool bf16, int64_t rows, int D, const void* x, const 
     if (e != hipSuccess) return e;
   }
   if (!params) return hipSuccess;
-  norm_finish_kernel<<<dim3((D + 63) / 64, 2), 64 * kFinishWaves, 0, s>>>(
+  norm_finish_kernel<<<dim3((D + kFinishCols - 1) / kFinishCols, 2), kFinishCols * kFinishRows, 0,
+                       s>>>(
       part, static_cast<int>(bwd_parts(rows, D)), D, dgamma, dbeta);
   return hipGetLastError();
 }
