@@ -47,7 +47,8 @@ typedef struct {
  * norm is summed in fp64. Errors are those of fp32 arithmetic.
  *
  *  n      matrices (>= 0; 0: nothing is done), at most 65535
- *  rows, cols   1 .. MOE_MAX_WIDTH; the smaller one at most 32768
+ *  rows, cols   1 .. MOE_MAX_WIDTH; the smaller one at most 32768;
+ *         n ceil(rows / 64) ceil(cols / 64) below 2^23
  *  g      dtype MOE_F32 or MOE_BF16
  *  steps  1 .. MOE_MAX_ORTH_STEPS
  *  eps    >= 0, finite (0 makes a zero matrix NaN)

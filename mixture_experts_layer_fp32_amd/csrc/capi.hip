@@ -1076,7 +1076,7 @@ moe_status check_orth_sizes(int32_t n, int32_t rows, int32_t cols, int32_t steps
   if (n < 0 || rows < 1 || cols < 1 || steps < 1 || steps > MOE_MAX_ORTH_STEPS)
     return MOE_ERR_INVALID_ARG;
   if (n > 65535 || rows > MOE_MAX_WIDTH || cols > MOE_MAX_WIDTH || std::min(rows, cols) > 32768 ||
-      moe::orth_tiles(n, rows, cols) >= (int64_t(1) << 30))
+      moe::orth_tiles(n, rows, cols) >= (int64_t(1) << 23))  // 512 threads each in a launch
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

@@ -233,7 +233,8 @@ hipError_t launch_norm_bwd(bool bf16, int64_t rows, int D, const void* x, const 
 
 // Newton-Schulz orthogonalisation (orth.hip) of g into w, or, with a momentum,
 // a Muon step on w. ws: orth_ws_bytes() bytes. orth_tiles bounds the
-// workgroups of any launch (the caller keeps it below 2^30).
+// workgroups of any launch (the caller keeps it below 2^23, so that a launch
+// has fewer than 2^32 threads).
 size_t orth_ws_bytes(int n, int rows, int cols);
 int64_t orth_tiles(int n, int rows, int cols);
 hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const moe_matrices* mom,

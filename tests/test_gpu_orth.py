@@ -48,7 +48,8 @@ def _ws(n, rows, cols, steps=5):
 def _orth(g, out_dtype=F32, steps=5, eps=1e-7):
     n, rows, cols = g.shape
     out = torch.full(g.shape, 7.0, dtype=out_dtype, device="cuda")
-    moe.moe_orthogonalize(g, out, _ws(n, rows, cols, steps), steps=steps, eps=eps)
+    # a workspace full of NaN: nothing in it is read before it is written
+    moe.moe_orthogonalize(g, out, _ws(n, rows, cols, steps).fill_(0xFF), steps=steps, eps=eps)
     torch.cuda.synchronize()
     return out
 

@@ -195,6 +195,22 @@ def test_training_step_graph_replays_match_eager():
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_tokens(dtype):
+    """A step of a rank that got no tokens: zero gradients, weights decayed."""
+    w = wl.Workload("none", T=0, D=64, E=4, k=2, I=64, dtype=dtype, I_shared=64)
+    lay, dv, dout, _, _ = _block(w)
+    assert lay.forward(dv["x"]).shape == (0, 64)
+    lay.backward(dout)
+    names = ("dw_router", "dw_gate_up", "dw_down", "dw_shared_gate_up", "dw_shared_down",
+             "dnorm_gamma", "dnorm_beta")
+    assert not any(getattr(lay, k).any() for k in names)
+    old = lay.w["w_down"].float().clone()
+    moe.ExpertMuon(lay, weight_decay=0.5).step(0.5)
+    torch.cuda.synchronize()
+    assert torch.equal(lay.w["w_down"], (old * 0.75).to(w.torch_dtype))
+
+
 def test_norm_arguments():
     d = moe.make_desc(T=4, D=64, E=2, top_k=1, I=64)
     t = torch.zeros(2, 64, 64, device="cuda")

@@ -119,6 +119,7 @@ def test_orthogonalize_refusals(lib):
     assert call(n=65536) == B.MOE_ERR_UNSUPPORTED
     assert call(rows=B.MOE_MAX_WIDTH + 1) == B.MOE_ERR_UNSUPPORTED
     assert call(rows=32769, cols=32769) == B.MOE_ERR_UNSUPPORTED
+    assert call(n=2048, rows=4096, cols=4096) == B.MOE_ERR_UNSUPPORTED  # 2^23 tiles of 64 x 64
     for bad, code in ((_mats(data=None), B.MOE_ERR_INVALID_ARG),
                       (_mats(ld=15), B.MOE_ERR_INVALID_ARG),
                       (_mats(stride=15), B.MOE_ERR_INVALID_ARG),
