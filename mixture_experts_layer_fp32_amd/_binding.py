@@ -851,26 +851,29 @@ def moe_expert_ffn_ptrs(d: moe_desc, n_experts, inter, cap_rows, x_perm, offsets
 _ACT_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
 
-def _device_of(t, name: str) -> torch.device:
+def _device_of(t, name: str) -> int:
+    """The index of the GPU that t is on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a GPU tensor")
-    return t.device
+    return t.get_device()
 
 
-def _ptr_on(dev: torch.device, t, name: str, dtype: torch.dtype, shape=None):
-    """_ptr for a call that runs on dev: the same refusals, and tensors of
-    other devices. (These calls are short next to their launches: what is
-    checked is checked in the fewest steps.)"""
+def _ptr_on(dev: int, t, name: str, dtype: torch.dtype, shape=None):
+    """_ptr for a call that runs on GPU dev: the same refusals, and tensors of
+    other devices. (These calls are short: what is checked is checked in the
+    fewest steps, and named when something is wrong.)"""
     if t is None:
         return None
-    if not (isinstance(t, torch.Tensor) and t.device == dev and t.dtype == dtype
-            and t.is_contiguous() and (shape is None or t.shape == shape)):
-        if isinstance(t, torch.Tensor) and t.is_cuda and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, other tensors on {dev}")
-        return _ptr(t, name, dtype, shape)  # raises, naming what is wrong
-    return t.data_ptr()
+    try:
+        if (t.get_device() == dev and t.dtype is dtype and t.is_contiguous()
+                and (shape is None or t.shape == shape)):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _ptr(t, name, dtype, shape)
+    raise ValueError(f"{name}: on {t.device}, other tensors on cuda:{dev}")
 
 
 def _act_code(t: torch.Tensor, name: str) -> int:
@@ -886,22 +889,19 @@ def _rows(t, name: str):
     return t.shape
 
 
-def _launch(name: str, dev: torch.device, args, stream):
-    """Call entry point `name` with dev current, on `stream` (None: torch's
+def _launch(name: str, dev: int, args, stream):
+    """Call entry point `name` with GPU dev current, on `stream` (None: torch's
     current stream of dev)."""
-    fn = getattr(load_library(), name)
-    if dev.index == torch._C._cuda_getDevice():
-        status = fn(*args, _raw_stream(dev.index) if stream is None else _stream(stream))
+    fn = getattr(_lib or load_library(), name)
+    if dev == torch._C._cuda_getDevice():
+        # torch.cuda.current_stream().cuda_stream without the Stream object
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None
+                    else _stream(stream))
     else:
         with torch.cuda.device(dev):
             status = fn(*args, _stream(stream))
     if status != MOE_OK:
         _check(name, status)
-
-
-def _raw_stream(index: int) -> int:
-    # torch.cuda.current_stream(index).cuda_stream without the Stream object.
-    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def moe_layer_norm(x, gamma, beta, eps, y, mean=None, rstd=None, stream=None):
@@ -952,12 +952,12 @@ def moe_layer_norm_backward(x, dy, gamma, mean, rstd, dres, dx, dgamma, dbeta, w
 # adjacent in memory; rows and matrices may be spaced (views of the gate or up
 # columns of a gate_up tensor).
 # ---------------------------------------------------------------------------
-def _matrices(dev: torch.device, t, name: str, shape=None):
-    """moe_matrices of a tensor of matrices on dev."""
+def _matrices(dev: int, t, name: str, shape=None):
+    """moe_matrices of a tensor of matrices on GPU dev."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
         raise ValueError(f"{name}: expected [n, rows, cols] or [rows, cols]")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, other tensors on {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, other tensors on cuda:{dev}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     rows, cols = t.shape[-2:]

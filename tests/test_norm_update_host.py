@@ -11,7 +11,7 @@ import torch
 from mixture_experts_layer_fp32_amd import _binding as B
 from oracle import norm_update_oracle as ou
 
-CPU = torch.device("cpu")
+CPU = torch.zeros(1).get_device()
 FAKE = ctypes.c_void_p(0x1000)  # never dereferenced: every call below fails its checks
 
 
