@@ -332,14 +332,15 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(
 }
 
 // ---- backward: the row in registers ----------------------------------------
-// PARAMS: this workgroup's sums of dy h and dy over its rows go to
-// part[2][gridDim.x][D].
+// PARAMS: this workgroup's sums of dy h and dy over its rows go to row
+// blockIdx.x of part_g and part_b [gridDim.x][D] (NULL: not wanted); a single
+// workgroup writes dgamma and dbeta themselves.
 template <typename T, int G, int NV, bool PARAMS>
 __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
     const T* __restrict__ x, const T* __restrict__ dy, const float* __restrict__ gamma,
     const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
-    const T* __restrict__ dres, T* __restrict__ dx, float* __restrict__ part, int64_t rows,
-    int D) {
+    const T* __restrict__ dres, T* __restrict__ dx, float* __restrict__ part_g,
+    float* __restrict__ part_b, int64_t rows, int D) {
   constexpr int N = Vec<T>::N, WG = wg_of(G), R = WG / G;
   // red: with several groups a workgroup, the column sums of the others.
   __shared__ Exchange<G> ex;
@@ -409,8 +410,9 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
   }
   if constexpr (PARAMS) {
     // dgamma then dbeta: the other groups' sums through LDS to group 0.
-    float* out = part + static_cast<int64_t>(blockIdx.x) * D;
     auto flush = [&](float(&a)[NV][N], float* o) {
+      if (o == nullptr) return;
+      o += static_cast<int64_t>(blockIdx.x) * D;
       if constexpr (R > 1) {
         __syncthreads();
         if (grp > 0) {
@@ -436,8 +438,8 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
           if (c < D) o[c] = a[i][e];
         }
     };
-    flush(dg, out);
-    flush(db, out + static_cast<int64_t>(gridDim.x) * D);
+    flush(dg, part_g);
+    flush(db, part_b);
   }
 }
 
@@ -487,7 +489,8 @@ __global__ __launch_bounds__(256) void norm_param_kernel(const T* __restrict__ x
                                                          const T* __restrict__ dy,
                                                          const float* __restrict__ mean_in,
                                                          const float* __restrict__ rstd_in,
-                                                         float* __restrict__ part, int64_t rows,
+                                                         float* __restrict__ part_g,
+                                                         float* __restrict__ part_b, int64_t rows,
                                                          int D, int64_t chunk) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= D) return;
@@ -498,8 +501,8 @@ __global__ __launch_bounds__(256) void norm_param_kernel(const T* __restrict__ x
     dg = fmaf(d, (load_act(x + r * D + c) - mean_in[r]) * rstd_in[r], dg);
     db += d;
   }
-  part[static_cast<int64_t>(blockIdx.y) * D + c] = dg;
-  part[(static_cast<int64_t>(gridDim.y) + blockIdx.y) * D + c] = db;
+  if (part_g != nullptr) part_g[static_cast<int64_t>(blockIdx.y) * D + c] = dg;
+  if (part_b != nullptr) part_b[static_cast<int64_t>(blockIdx.y) * D + c] = db;
 }
 
 // dgamma (blockIdx.y 0) and dbeta (1): 32 columns a workgroup, the P partial
@@ -580,42 +583,42 @@ hipError_t fwd_t(int64_t rows, int D, const void* x, const float* gamma, const f
 
 template <typename T, int G>
 void bwd_g(const void* x, const void* dy, const float* gamma, const float* mean,
-           const float* rstd, const void* dres, void* dx, float* part, int64_t rows, int D,
-           hipStream_t s) {
+           const float* rstd, const void* dres, void* dx, float* part_g, float* part_b,
+           int64_t rows, int D, hipStream_t s) {
   constexpr int NV = kRegVals / Vec<T>::N;
   const int grid = static_cast<int>(bwd_parts(rows, D));
   const T *xt = static_cast<const T*>(x), *dyt = static_cast<const T*>(dy),
           *rt = static_cast<const T*>(dres);
   T* dxt = static_cast<T*>(dx);
-  if (part != nullptr)
+  if (part_g != nullptr || part_b != nullptr)
     norm_bwd_kernel<T, G, NV, true>
-        <<<grid, wg_of(G), 0, s>>>(xt, dyt, gamma, mean, rstd, rt, dxt, part, rows, D);
+        <<<grid, wg_of(G), 0, s>>>(xt, dyt, gamma, mean, rstd, rt, dxt, part_g, part_b, rows, D);
   else
-    norm_bwd_kernel<T, G, NV, false>
-        <<<grid, wg_of(G), 0, s>>>(xt, dyt, gamma, mean, rstd, rt, dxt, nullptr, rows, D);
+    norm_bwd_kernel<T, G, NV, false><<<grid, wg_of(G), 0, s>>>(xt, dyt, gamma, mean, rstd, rt, dxt,
+                                                               nullptr, nullptr, rows, D);
 }
 
 template <typename T>
 void bwd_t(int64_t rows, int D, const void* x, const void* dy, const float* gamma,
-           const float* mean, const float* rstd, const void* dres, void* dx, float* part,
-           hipStream_t s) {
+           const float* mean, const float* rstd, const void* dres, void* dx, float* part_g,
+           float* part_b, hipStream_t s) {
   if (D > kMaxRegWidth) {
     const T *xt = static_cast<const T*>(x), *dyt = static_cast<const T*>(dy);
     norm_bwd_wide_kernel<T><<<static_cast<int>(std::min<int64_t>(rows, 2 * kCus)), 1024, 0, s>>>(
         xt, dyt, gamma, mean, rstd, static_cast<const T*>(dres), static_cast<T*>(dx), rows, D);
-    if (part != nullptr) {
+    if (part_g != nullptr || part_b != nullptr) {
       const int64_t P = bwd_parts(rows, D);
       norm_param_kernel<T><<<dim3((D + 255) / 256, static_cast<unsigned>(P)), 256, 0, s>>>(
-          xt, dyt, mean, rstd, part, rows, D, (rows + P - 1) / P);
+          xt, dyt, mean, rstd, part_g, part_b, rows, D, (rows + P - 1) / P);
     }
     return;
   }
   switch (group_of(D)) {
-    case 64: bwd_g<T, 64>(x, dy, gamma, mean, rstd, dres, dx, part, rows, D, s); break;
-    case 128: bwd_g<T, 128>(x, dy, gamma, mean, rstd, dres, dx, part, rows, D, s); break;
-    case 256: bwd_g<T, 256>(x, dy, gamma, mean, rstd, dres, dx, part, rows, D, s); break;
-    case 512: bwd_g<T, 512>(x, dy, gamma, mean, rstd, dres, dx, part, rows, D, s); break;
-    default: bwd_g<T, 1024>(x, dy, gamma, mean, rstd, dres, dx, part, rows, D, s); break;
+    case 64: bwd_g<T, 64>(x, dy, gamma, mean, rstd, dres, dx, part_g, part_b, rows, D, s); break;
+    case 128: bwd_g<T, 128>(x, dy, gamma, mean, rstd, dres, dx, part_g, part_b, rows, D, s); break;
+    case 256: bwd_g<T, 256>(x, dy, gamma, mean, rstd, dres, dx, part_g, part_b, rows, D, s); break;
+    case 512: bwd_g<T, 512>(x, dy, gamma, mean, rstd, dres, dx, part_g, part_b, rows, D, s); break;
+    default: bwd_g<T, 1024>(x, dy, gamma, mean, rstd, dres, dx, part_g, part_b, rows, D, s); break;
   }
 }
 
@@ -637,18 +640,22 @@ hipError_t launch_norm_bwd(bool bf16, int64_t rows, int D, const void* x, const 
                            const void* dres, void* dx, float* dgamma, float* dbeta, float* part,
                            hipStream_t s) {
   const bool params = dgamma != nullptr || dbeta != nullptr;
+  const int64_t P = bwd_parts(rows, D);
   if (rows > 0) {
+    // One part: the sums are the gradients themselves.
+    float* pg = P == 1 ? dgamma : params ? part : nullptr;
+    float* pb = P == 1 ? dbeta : params ? part + P * D : nullptr;
     if (bf16)
-      bwd_t<uint16_t>(rows, D, x, dy, gamma, mean, rstd, dres, dx, params ? part : nullptr, s);
+      bwd_t<uint16_t>(rows, D, x, dy, gamma, mean, rstd, dres, dx, pg, pb, s);
     else
-      bwd_t<float>(rows, D, x, dy, gamma, mean, rstd, dres, dx, params ? part : nullptr, s);
+      bwd_t<float>(rows, D, x, dy, gamma, mean, rstd, dres, dx, pg, pb, s);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || P == 1) return e;
   }
   if (!params) return hipSuccess;
   norm_finish_kernel<<<dim3((D + kFinishCols - 1) / kFinishCols, 2), kFinishCols * kFinishRows, 0,
                        s>>>(
-      part, static_cast<int>(bwd_parts(rows, D)), D, dgamma, dbeta);
+      part, static_cast<int>(P), D, dgamma, dbeta);
   return hipGetLastError();
 }
 
