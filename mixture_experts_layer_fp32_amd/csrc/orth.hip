@@ -755,19 +755,28 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
 // The rest of a segment in one launch. Every workgroup adds up the Gram
 // product's parts, holds A and P of its matrix in LDS (MB 32-row blocks, at
 // most 64 KB each), takes the segment's steps (1 or 2) there, and multiplies
-// its share of X: group g of XB 32-row blocks of X^T, g = blockIdx.x,
-// blockIdx.x + gridDim.x, ... The steps are repeated by every workgroup of a
-// matrix: they take a few microseconds, a launch each would take more. A wave
-// has one 32 x 32 block: of the m x m products those on and below the
-// diagonal (10 of 16 waves for MB = 4, at most 3 on a SIMD).
+// its share of X. The steps are repeated by every workgroup of a matrix: they
+// take a few microseconds, a launch each would take more. A wave has one 32 x
+// 32 block: of the m x m products those on and below the diagonal (10 of 16
+// waves for MB = 4, at most 3 on a SIMD).
+// STAGED: one group of xbw blocks of X^T a workgroup, copied into LDS during the
+//   steps; while the card has a CU for each (8 x 128 x 512 91 -> 81 us).
+//   Otherwise groups of XB blocks, g = blockIdx.x, blockIdx.x + gridDim.x, ...
+//   (200 x 128 x 512 203 us, 220 as the other way's loop).
 // SWAP: the result's rows are those of Q (kOut of a wide matrix).
-template <int MB, int EPI, bool SWAP>
+// MB = 4, one step, groups of four: 11.5 us, of it the launch 2.5, the Gram
+// parts 1.0, the step 2.7, X 5.3.
+constexpr int steps_xb(int mb) { return mb == 1 ? 16 : mb == 2 ? 8 : 4; }
+constexpr int steps_staged(int mb) { return mb == 4 ? 2 : 4; }  // 32 KB or less
+template <int MB, int EPI, bool SWAP, bool STAGED>
 __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk,
-                                                          const float* __restrict__ gram,
+                                                          int xbw, const float* __restrict__ gram,
                                                           int splits) {
-  constexpr int KS = 2 * MB, MP = MB == 3 ? 4 : MB, XB = 16 / MP;
+  constexpr int KS = 2 * MB, MP = MB == 3 ? 4 : MB, XB = steps_xb(MB);
   constexpr int kOp = MB * KS * 1024;  // values of an operand
-  __shared__ __attribute__((aligned(16))) uint16_t bufs[2][kOp];
+  __shared__ __attribute__((aligned(1024))) uint16_t bufs[2][kOp];
+  __shared__ __attribute__((aligned(1024))) uint16_t
+      xs[STAGED ? steps_staged(MB) * KS * 1024 : 8];
   uint16_t *ba = bufs[0], *bp = bufs[1];
   const int mat = blockIdx.y, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -863,6 +872,15 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
         }
       }
     }
+    if constexpr (STAGED) {  // X^T on its way into LDS, 1 KB a copy
+      const int x0 = blockIdx.x * xbw, nb = min(xbw, rk - x0);
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(p.a + mat * p.sa + static_cast<int64_t>(x0) * (KS * 1024)), 0, nb * KS * 2048,
+          0x00020000);
+      const unsigned lds_x = (unsigned)(uintptr_t)(lds_u8*)xs;
+      for (int c = wave; c < nb * KS * 2; c += 16)
+        dma16(rsrc, lane * 16, c * 1024, lds_x + c * 1024);
+    }
     store(ba, kScaleA / (kScaleX * kScaleX));
     __syncthreads();
   }
@@ -879,21 +897,27 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
     __syncthreads();
   }
 
-  const int qb = wave % MP;
-  int xb = blockIdx.x * XB + wave / MP;
-  if (qb >= MB) return;
+  if constexpr (STAGED) {
+    __builtin_amdgcn_s_waitcnt(kVm0Lgkm0);  // this wave's copies; after the barrier all
+    __syncthreads();
+  }
+  const int qb = wave % MP, per = STAGED ? xbw : XB;
+  int xb = blockIdx.x * per + wave / MP;
+  if (qb >= MB || wave / MP >= per) return;
 #pragma unroll 1
-  for (; xb < rk; xb += gridDim.x * XB) {
-    load_x(xb);
+  for (; xb < rk; xb += STAGED ? rk : gridDim.x * XB) {
+    if constexpr (!STAGED) load_x(xb);
     zero();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       __builtin_amdgcn_sched_barrier(0);  // not all of Q's fragments at once
       const f16x8 qh = frag(bp, qb, ks, 0), ql = frag(bp, qb, ks, 1);
+      const f16x8 xh = STAGED ? frag(xs, wave / MP, ks, 0) : x[ks][0];
+      const f16x8 xl = STAGED ? frag(xs, wave / MP, ks, 1) : x[ks][1];
       if constexpr (SWAP)
-        mma(qh, ql, x[ks][0], x[ks][1]);
+        mma(qh, ql, xh, xl);
       else
-        mma(x[ks][0], x[ks][1], qh, ql);
+        mma(xh, xl, qh, ql);
     }
     float v[4][4];
 #pragma unroll
@@ -1011,15 +1035,27 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
 template <int EPI, bool SWAP>
 hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm, int rk,
                         const float* gram, int splits, hipStream_t s) {
-  const int xb = rm == 1 ? 16 : rm == 2 ? 8 : 4;
-  const dim3 grid(std::min((rk + xb - 1) / xb, std::max(1, 256 / n)), n);
+  auto run = [&](auto mb) {
+    constexpr int MB = decltype(mb)::value;
+    // As few blocks of X^T a workgroup as leave a CU for each.
+    int xbw = 1;
+    auto groups_of = [&](int per) { return (rk + per - 1) / per; };
+    auto fits = [&](int per) { return static_cast<int64_t>(groups_of(per)) * n <= 256; };
+    while (xbw < steps_staged(MB) && !fits(xbw)) xbw *= 2;
+    if (fits(xbw)) {
+      orth_steps_kernel<MB, EPI, SWAP, true>
+          <<<dim3(groups_of(xbw), n), 1024, 0, s>>>(p, o, steps, rk, xbw, gram, splits);
+    } else {
+      const dim3 grid(std::min(groups_of(steps_xb(MB)), std::max(1, 256 / n)), n);
+      orth_steps_kernel<MB, EPI, SWAP, false>
+          <<<grid, 1024, 0, s>>>(p, o, steps, rk, 0, gram, splits);
+    }
+  };
   switch (rm) {
-    case 1:
-      orth_steps_kernel<1, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits);
-      break;
-    case 2: orth_steps_kernel<2, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits); break;
-    case 3: orth_steps_kernel<3, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits); break;
-    default: orth_steps_kernel<4, EPI, SWAP><<<grid, 1024, 0, s>>>(p, o, steps, rk, gram, splits); break;
+    case 1: run(std::integral_constant<int, 1>{}); break;
+    case 2: run(std::integral_constant<int, 2>{}); break;
+    case 3: run(std::integral_constant<int, 3>{}); break;
+    default: run(std::integral_constant<int, 4>{}); break;
   }
   return hipGetLastError();
 }
