@@ -759,19 +759,32 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
 // take a few microseconds, a launch each would take more. A wave has one 32 x
 // 32 block: of the m x m products those on and below the diagonal (10 of 16
 // waves for MB = 4, at most 3 on a SIMD).
-// STAGED: one group of xbw blocks of X^T a workgroup, copied into LDS during the
+// kStaged: one group of xbw blocks of X^T a workgroup, copied into LDS during the
 //   steps; while the card has a CU for each (8 x 128 x 512 91 -> 81 us).
 //   Otherwise groups of XB blocks, g = blockIdx.x, blockIdx.x + gridDim.x, ...
 //   (200 x 128 x 512 203 us, 220 as the other way's loop).
+// kGram: staged, and the workgroup's blocks of the new X, still in LDS, give
+//   its part of the next segment's Gram product: no launch for it, no X in
+//   memory (8 x 128 x 512 81 -> 75 us, 32 x 128 x 256 94 -> 77). As many blocks
+//   a workgroup as LDS holds, since every workgroup adds up all parts of its
+//   matrix (8 x 128 x 512 as 8 parts 75 us, as 16 84), and up to gram_parts()
+//   parts: about 0.3 MB to read. While a CU for each workgroup is there, or one
+//   workgroup is all of a matrix (512 x 64 x 64 80 -> 67 us; 60 x 128 x 512, 480
+//   workgroups, 133 -> 190: the steps are repeated in each).
 // SWAP: the result's rows are those of Q (kOut of a wide matrix).
 // MB = 4, one step, groups of four: 11.5 us, of it the launch 2.5, the Gram
 // parts 1.0, the step 2.7, X 5.3.
 constexpr int steps_xb(int mb) { return mb == 1 ? 16 : mb == 2 ? 8 : 4; }
 constexpr int steps_staged(int mb) { return mb == 4 ? 2 : 4; }  // 32 KB or less
-template <int MB, int EPI, bool SWAP, bool STAGED>
+constexpr int gram_parts(int mb) { return mb == 1 ? 32 : mb == 2 ? 16 : 8; }
+enum XGroups { kLoop = 0, kStaged = 1, kGram = 2 };
+template <int MB, int EPI, bool SWAP, int MODE>
 __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk,
                                                           int xbw, const float* __restrict__ gram,
-                                                          int splits) {
+                                                          int splits,
+                                                          float* __restrict__ next_gram) {
+  constexpr bool STAGED = MODE != kLoop;
+  static_assert(MODE != kGram || (EPI == kOperand && !SWAP), "the next segment's operand");
   constexpr int KS = 2 * MB, MP = MB == 3 ? 4 : MB, XB = steps_xb(MB);
   constexpr int kOp = MB * KS * 1024;  // values of an operand
   __shared__ __attribute__((aligned(1024))) uint16_t bufs[2][kOp];
@@ -853,11 +866,16 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       }
     }
   };
-  {  // A, from register group 2 h + q of block b in wave 2 b + h of its tile
-    constexpr int TILES = MB > 2 ? 3 : 1;
+  // This wave's block in part sp of `of` parts of matrix mat's Gram product.
+  constexpr int TILES = MB > 2 ? 3 : 1;
+  auto gram_at = [&](int sp, int of) {
     const int tile = ib / 2 * (ib / 2 + 1) / 2 + jb / 2, b = 2 * (ib & 1) + (jb & 1);
-    const float* g = gram + (static_cast<int64_t>(mat) * splits * TILES + tile) * kGramTile +
-                     b * 1024 + lane * 4;
+    return ((static_cast<int64_t>(mat) * of + sp) * TILES + tile) * kGramTile + b * 1024 +
+           lane * 4;
+  };
+  const int nb = STAGED ? min(xbw, rk - static_cast<int>(blockIdx.x) * xbw) : 0;
+  {  // A, from register group 2 h + q of block b in wave 2 b + h of its tile
+    const float* g = gram + gram_at(0, splits);
     zero();
     if (mine) {
 #pragma unroll 4
@@ -873,7 +891,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       }
     }
     if constexpr (STAGED) {  // X^T on its way into LDS, 1 KB a copy
-      const int x0 = blockIdx.x * xbw, nb = min(xbw, rk - x0);
+      const int x0 = blockIdx.x * xbw;
       const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(p.a + mat * p.sa + static_cast<int64_t>(x0) * (KS * 1024)), 0, nb * KS * 2048,
           0x00020000);
@@ -903,10 +921,9 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
   }
   const int qb = wave % MP, per = STAGED ? xbw : XB;
   int xb = blockIdx.x * per + wave / MP;
-  if (qb >= MB || wave / MP >= per) return;
-#pragma unroll 1
-  for (; xb < rk; xb += STAGED ? rk : gridDim.x * XB) {
-    if constexpr (!STAGED) load_x(xb);
+  const bool busy = qb < MB && wave / MP < per && xb < rk;
+  if (MODE != kGram && !busy) return;
+  auto times_q = [&]() {  // acc <- the block of X^T times Q
     zero();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
@@ -919,11 +936,53 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       else
         mma(xh, xl, qh, ql);
     }
-    float v[4][4];
+  };
+  if constexpr (MODE != kGram) {
+#pragma unroll 1
+    for (; xb < rk; xb += STAGED ? rk : gridDim.x * XB) {
+      if constexpr (!STAGED) load_x(xb);
+      times_q();
+      float v[4][4];
 #pragma unroll
-    for (int r = 0; r < 16; ++r) v[r / 4][r % 4] = acc[r];
-    store_block<EPI, 4>(p, o, mat, SWAP ? MB : rk, SWAP ? rk : MB, SWAP ? qb : xb, SWAP ? xb : qb,
-                        0, v, lane);
+      for (int r = 0; r < 16; ++r) v[r / 4][r % 4] = acc[r];
+      store_block<EPI, 4>(p, o, mat, SWAP ? MB : rk, SWAP ? rk : MB, SWAP ? qb : xb,
+                          SWAP ? xb : qb, 0, v, lane);
+    }
+  } else {
+    if (busy) times_q();
+    __syncthreads();  // xs has been read: now the blocks of X, depth 32 xbw
+    auto xfrag = [&](int rb, int ks, int part) { return ((rb * 2 * xbw + ks) * 2 + part) * 512; };
+    if (busy) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+#pragma unroll
+        for (int s = 0; s < 4; ++s) v[s] = acc[4 * q + s] * p.alpha;
+        Parts w = split4(v);
+        store_parts(xs + xfrag(qb, 2 * (wave / MP) + (q >> 1), 0), l32 + 32 * (q & 1), 4 * half, w);
+        w.hi = transpose4(w.hi, lane & 3);
+        w.lo = transpose4(w.lo, lane & 3);
+        const int j0 = 4 * (l32 >> 2), row = 8 * q + 4 * half + (lane & 3);
+        store_parts(p.out_n + mat * p.so +
+                        (static_cast<int64_t>(xb) * KS + 2 * qb + (j0 >> 4)) * 1024,
+                    row + 32 * ((j0 >> 3) & 1), j0 & 7, w);
+      }
+    }
+    __syncthreads();
+    if (!mine) return;
+    zero();
+#pragma unroll 2
+    for (int ks = 0; ks < 2 * nb; ++ks) {
+      auto at = [&](int rb, int part) {
+        return *reinterpret_cast<const f16x8*>(xs + xfrag(rb, ks, part) + lane * 8);
+      };
+      mma(at(ib, 0), at(ib, 1), at(jb, 0), at(jb, 1));
+    }
+    float* g = next_gram + gram_at(blockIdx.x, gridDim.x);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4*>(g + q * 256) =
+          make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
   }
 }
 
@@ -935,7 +994,8 @@ int ceil32(int v) { return (v + 31) / 32; }
 struct Space {
   int64_t x, mm;  // values of one X operand, of one m x m operand
   int tiles, splits;  // short sides up to 128: Gram tiles, depth splits
-  int64_t gram;   // floats
+  int gram_xbw;   // blocks of X^T a workgroup that gives the next Gram parts too, or 0
+  int64_t gram;   // floats of the Gram parts; with gram_xbw there are two such
   int64_t part;   // partial sums per matrix
   size_t bytes;
 };
@@ -954,12 +1014,15 @@ Space space(int n, int rows, int cols) {
     const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, 2 * k / 16));
     s.splits = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(most, 256 / (static_cast<int64_t>(std::max(n, 1)) * s.tiles))));
-    s.gram = static_cast<int64_t>(s.tiles) * s.splits * kGramTile;
+    const int mb = static_cast<int>(m), xbw = steps_staged(mb);
+    const int64_t next = (k + xbw - 1) / xbw;
+    if (next <= gram_parts(mb) && (next == 1 || next * n <= 256)) s.gram_xbw = xbw;
+    s.gram = s.tiles * std::max<int64_t>(s.splits, s.gram_xbw ? next : 0) * kGramTile;
   } else {
     s.mm = m * 2 * m * 1024;
   }
   s.part = norm_parts(n, static_cast<int64_t>(rows) * cols);
-  s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.gram * 4 + s.part * 8);
+  s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.gram * (s.gram_xbw ? 8 : 4) + s.part * 8);
   return s;
 }
 
@@ -1034,21 +1097,30 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
 // p.a: X^T; after orth_gram_kernel.
 template <int EPI, bool SWAP>
 hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm, int rk,
-                        const float* gram, int splits, hipStream_t s) {
+                        const float* gram, int splits, int gram_xbw, float* next_gram,
+                        hipStream_t s) {
   auto run = [&](auto mb) {
     constexpr int MB = decltype(mb)::value;
+    if constexpr (EPI == kOperand) {
+      if (next_gram != nullptr) {
+        const int groups = (rk + gram_xbw - 1) / gram_xbw;
+        orth_steps_kernel<MB, EPI, SWAP, kGram>
+            <<<dim3(groups, n), 1024, 0, s>>>(p, o, steps, rk, gram_xbw, gram, splits, next_gram);
+        return;
+      }
+    }
     // As few blocks of X^T a workgroup as leave a CU for each.
     int xbw = 1;
     auto groups_of = [&](int per) { return (rk + per - 1) / per; };
     auto fits = [&](int per) { return static_cast<int64_t>(groups_of(per)) * n <= 256; };
     while (xbw < steps_staged(MB) && !fits(xbw)) xbw *= 2;
     if (fits(xbw)) {
-      orth_steps_kernel<MB, EPI, SWAP, true>
-          <<<dim3(groups_of(xbw), n), 1024, 0, s>>>(p, o, steps, rk, xbw, gram, splits);
+      orth_steps_kernel<MB, EPI, SWAP, kStaged>
+          <<<dim3(groups_of(xbw), n), 1024, 0, s>>>(p, o, steps, rk, xbw, gram, splits, nullptr);
     } else {
       const dim3 grid(std::min(groups_of(steps_xb(MB)), std::max(1, 256 / n)), n);
-      orth_steps_kernel<MB, EPI, SWAP, false>
-          <<<grid, 1024, 0, s>>>(p, o, steps, rk, 0, gram, splits);
+      orth_steps_kernel<MB, EPI, SWAP, kLoop>
+          <<<grid, 1024, 0, s>>>(p, o, steps, rk, 0, gram, splits, nullptr);
     }
   };
   switch (rm) {
@@ -1085,6 +1157,7 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
   uint16_t *A = take(sp.mm), *U = take(sp.mm), *P = take(sp.mm), *Q = take(sp.mm),
            *Q2 = take(sp.mm);
   float* gram = reinterpret_cast<float*>(take(2 * sp.gram));
+  float* next_gram = sp.gram_xbw ? reinterpret_cast<float*>(take(2 * sp.gram)) : nullptr;
   double* part = reinterpret_cast<double*>(base);
 
   const Mats gm{g.data, g.ld, g.stride, g.dtype == MOE_BF16};
@@ -1129,21 +1202,29 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     return sym(p);
   };
   const Segments seg = segment_rule(wm.bf16, mom != nullptr, std::min(rows, cols));
-  int left = d.steps;
+  int left = d.steps, splits = 0;  // parts of the Gram product
   for (bool first = true; left > 0; first = false) {
     const int L = std::min(left, first ? seg.first : seg.later);
     left -= L;
     if (rm <= 4) {
-      orth_gram_kernel<<<dim3(sp.tiles * sp.splits, n), 512, 0, s>>>(X, sp.x, rm, 2 * rk, sp.tiles,
-                                                                     sp.splits, gram);
+      if (first || next_gram == nullptr) {
+        orth_gram_kernel<<<dim3(sp.tiles * sp.splits, n), 512, 0, s>>>(X, sp.x, rm, 2 * rk,
+                                                                       sp.tiles, sp.splits, gram);
+        splits = sp.splits;
+      }
       Product x{XT, nullptr, sp.x, 0, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
       if (left > 0) {
-        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, gram, sp.splits, s);
+        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, gram, splits, sp.gram_xbw,
+                                          next_gram, s);
         std::swap(XT, XT2);
+        if (next_gram != nullptr) {
+          std::swap(gram, next_gram);
+          splits = (rk + sp.gram_xbw - 1) / sp.gram_xbw;
+        }
       } else {
         x.alpha = 1.f / (kScaleP * kScaleX);
-        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, gram, sp.splits, s)
-                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, gram, sp.splits, s);
+        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, gram, splits, 0, nullptr, s)
+                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, gram, splits, 0, nullptr, s);
       }
       if (e != hipSuccess) return e;
       continue;

@@ -94,6 +94,25 @@ def test_many_matrices(n, rows, cols, out_dtype):
         assert _excess(_np(out[i]), ou.orthogonalize(_np(g[i])), HALF[out_dtype]) <= TOL, i
 
 
+# Short sides of one to four 32-row blocks: the next step's Gram product from
+# one workgroup of a matrix, from several of which the last has fewer blocks, or
+# from a launch of its own (long sides; many matrices).
+SHORT = [(300, 20, 60), (2, 2000, 30), (1, 17, 5000), (300, 100, 64), (2, 50, 700), (90, 64, 500),
+         (2, 90, 380), (2, 300, 90), (3, 120, 300), (2, 270, 128), (40, 128, 520)]
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("n,rows,cols", SHORT)
+def test_short_sides(n, rows, cols, out_dtype):
+    print(f"[orth] n={n} {rows}x{cols} {out_dtype}", flush=True)
+    g = _randn(n, rows, cols, seed=n + cols).cuda()
+    out = _orth(g, out_dtype)
+    assert torch.isfinite(out).all() and float(out.abs().max()) < 1.3
+    assert torch.equal(out, _orth(g, out_dtype))
+    for i in (0, n // 2, n - 1):
+        assert _excess(_np(out[i]), ou.orthogonalize(_np(g[i])), HALF[out_dtype]) <= TOL, i
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 5, 6, 7])
 @pytest.mark.parametrize("rows,cols", [(96, 160), (200, 70)])
 def test_steps(rows, cols, steps):
