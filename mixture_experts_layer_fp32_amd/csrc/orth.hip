@@ -752,6 +752,133 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
     *reinterpret_cast<float4*>(out + q * 256) = make_float4(v[q][0], v[q][1], v[q][2], v[q][3]);
 }
 
+// Blocks of X^T a workgroup of the steps kernel has at most, by row blocks of X:
+// one a wave and row block; as many as its LDS holds; and most Gram parts.
+constexpr int steps_xb(int mb) { return mb == 1 ? 16 : mb == 2 ? 8 : 4; }
+constexpr int steps_staged(int mb) { return mb == 4 ? 2 : 4; }  // 48 KB or less
+constexpr int gram_parts(int mb) { return mb == 1 ? 32 : mb == 2 ? 16 : 8; }
+
+// Row block of the w-th block on or below the diagonal: (0, 0), (1, 0), (1, 1),
+// (2, 0), ...
+__device__ __forceinline__ int sym_row(int w) { return w >= 6 ? 3 : w >= 3 ? 2 : w >= 1 ? 1 : 0; }
+
+// Block (ib, jb) in part sp of `parts` of a matrix's Gram product, as
+// orth_gram_kernel lays it out (register group 2 h + q of block b in wave 2 b + h
+// of its tile).
+template <int MB>
+__device__ __forceinline__ int64_t gram_at(int mat, int sp, int parts, int ib, int jb, int lane) {
+  const int tile = ib / 2 * (ib / 2 + 1) / 2 + jb / 2, b = 2 * (ib & 1) + (jb & 1);
+  return ((static_cast<int64_t>(mat) * parts + sp) * (MB > 2 ? 3 : 1) + tile) * kGramTile +
+         b * 1024 + lane * 4;
+}
+
+// Block (ib, jb) of the Gram product of xs, an operand of MB row blocks and KS
+// slices in LDS of which the first `slices` count, to g (gram_at).
+template <int MB>
+__device__ __forceinline__ void gram_part(const uint16_t* xs, int KS, int slices, int ib, int jb,
+                                          int lane, float* __restrict__ g) {
+  f32x16 acc;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
+#pragma unroll 2
+  for (int ks = 0; ks < slices; ++ks) {
+    auto at = [&](int rb, int part) {
+      return *reinterpret_cast<const f16x8*>(xs + ((rb * KS + ks) * 2 + part) * 512 + lane * 8);
+    };
+    const f16x8 ah = at(ib, 0), al = at(ib, 1), bh = at(jb, 0), bl = at(jb, 1);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(al, bh, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bl, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah, bh, acc, 0, 0, 0);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    *reinterpret_cast<float4*>(g + q * 256) =
+        make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+}
+
+// orth_split_kernel where the steps kernel gives the later Gram products: one
+// workgroup has XB blocks of X's depth and all of its rows, writes X^T and
+// gives its part of the first Gram product. X itself is not written. A launch
+// less (4 x 64 x 512 42.6 -> 38.8 us, 512 x 64 x 64 68 -> 60; 8 x 128 x 512
+// 75.2 -> 75.9, as many parts to add up as later). Bound by the latency of its
+// loads and of the launch.
+template <int V, int MB, bool TALL>
+__global__ __launch_bounds__(1024) void orth_split_gram_kernel(
+    Mats g, Mats mom, float mu, int nesterov, int rows, int cols, float eps,
+    const double* __restrict__ part, int nparts, uint16_t* __restrict__ xt_planes,
+    int64_t plane_stride, int rk, float* __restrict__ gram) {
+  constexpr int XB = steps_staged(MB), KS = 2 * XB;
+  constexpr int TR = TALL ? 32 * XB : 32 * MB, TC = TALL ? 32 * MB : 32 * XB;  // of U
+  __shared__ float tile[TR][TC + 1];
+  __shared__ __attribute__((aligned(16))) uint16_t xs[MB * KS * 1024];
+  __shared__ double red[16];
+  const int mat = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int x0 = blockIdx.x * XB, nb = min(XB, rk - x0);
+  const int r0 = TALL ? 32 * x0 : 0, c0 = TALL ? 0 : 32 * x0;
+  constexpr int NL = TR * TC / (1024 * V);
+  static_assert(TR * TC % (1024 * V) == 0, "whole rounds");
+  float u[NL][V];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int x = (tid + 1024 * i) * V, r = r0 + x / TC, c = c0 + x % TC;
+#pragma unroll
+    for (int k = 0; k < V; ++k) u[i][k] = 0.f;
+    if (r < rows && c < cols) {
+      load_v<V>(g, mat * g.stride + r * g.ld + c, u[i]);
+      if (mom.data != nullptr) {
+        float m[V];
+        load_v<V>(mom, mat * mom.stride + r * mom.ld + c, m);
+#pragma unroll
+        for (int k = 0; k < V; ++k) u[i][k] = nesterov ? fmaf(mu, m[k], u[i][k]) : m[k];
+      }
+    }
+  }
+  double s = 0.0;
+  for (int i = tid; i < nparts; i += 1024) s += part[static_cast<int64_t>(mat) * nparts + i];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+  if (lane == 0) red[wave] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += red[w];
+  const double inv = static_cast<double>(kScaleX) / (sqrt(s) + eps);
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int x = (tid + 1024 * i) * V;
+#pragma unroll
+    for (int k = 0; k < V; ++k) tile[x / TC][x % TC + k] = static_cast<float>(u[i][k] * inv);
+  }
+  __syncthreads();
+  auto x_at = [&](int i, int k) { return TALL ? tile[k][i] : tile[i][k]; };
+  auto fragment = [&](uint16_t* out, auto value) {
+    union {
+      uint16_t h[8];
+      uint4 v;
+    } hi, lo;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) split(value(8 * (lane >> 5) + j), hi.h[j], lo.h[j]);
+    uint4* p = reinterpret_cast<uint4*>(out + lane * 8);
+    p[0] = hi.v;
+    p[64] = lo.v;
+  };
+  uint16_t* xt = xt_planes + mat * plane_stride + static_cast<int64_t>(x0) * (2 * MB) * 1024;
+  for (int f = wave; f < MB * KS; f += 16) {  // X: row block f / KS
+    const int i = 32 * (f / KS) + (lane & 31), k0 = 16 * (f % KS);
+    fragment(xs + f * 1024, [&](int j) { return x_at(i, k0 + j); });
+  }
+  for (int f = wave; f < nb * 2 * MB; f += 16) {  // X^T: row block f / (2 MB)
+    const int k = 32 * (f / (2 * MB)) + (lane & 31), i0 = 16 * (f % (2 * MB));
+    fragment(xt + f * 1024, [&](int j) { return x_at(i0 + j, k); });
+  }
+  __syncthreads();
+  const int ib = sym_row(wave), jb = wave - ib * (ib + 1) / 2;
+  if (wave < MB * (MB + 1) / 2)
+    gram_part<MB>(xs, KS, 2 * nb, ib, jb, lane,
+                  gram + gram_at<MB>(mat, blockIdx.x, gridDim.x, ib, jb, lane));
+}
+
 // The rest of a segment in one launch. Every workgroup adds up the Gram
 // product's parts, holds A and P of its matrix in LDS (MB 32-row blocks, at
 // most 64 KB each), takes the segment's steps (1 or 2) there, and multiplies
@@ -759,10 +886,10 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
 // take a few microseconds, a launch each would take more. A wave has one 32 x
 // 32 block: of the m x m products those on and below the diagonal (10 of 16
 // waves for MB = 4, at most 3 on a SIMD).
-// kStaged: one group of xbw blocks of X^T a workgroup, copied into LDS during the
-//   steps; while the card has a CU for each (8 x 128 x 512 91 -> 81 us).
-//   Otherwise groups of XB blocks, g = blockIdx.x, blockIdx.x + gridDim.x, ...
-//   (200 x 128 x 512 203 us, 220 as the other way's loop).
+// kLoop: groups of XB blocks of X^T, g = blockIdx.x, blockIdx.x + gridDim.x, ...
+// kStaged: one group of xbw blocks a workgroup, copied into LDS during the steps;
+//   while the card has a CU for each (8 x 128 x 512 91 -> 81 us; 200 x 128 x 512,
+//   as a loop of staged groups, 203 -> 220).
 // kGram: staged, and the workgroup's blocks of the new X, still in LDS, give
 //   its part of the next segment's Gram product: no launch for it, no X in
 //   memory (8 x 128 x 512 81 -> 75 us, 32 x 128 x 256 94 -> 77). As many blocks
@@ -772,11 +899,9 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
 //   workgroup is all of a matrix (512 x 64 x 64 80 -> 67 us; 60 x 128 x 512, 480
 //   workgroups, 133 -> 190: the steps are repeated in each).
 // SWAP: the result's rows are those of Q (kOut of a wide matrix).
-// MB = 4, one step, groups of four: 11.5 us, of it the launch 2.5, the Gram
-// parts 1.0, the step 2.7, X 5.3.
-constexpr int steps_xb(int mb) { return mb == 1 ? 16 : mb == 2 ? 8 : 4; }
-constexpr int steps_staged(int mb) { return mb == 4 ? 2 : 4; }  // 32 KB or less
-constexpr int gram_parts(int mb) { return mb == 1 ? 32 : mb == 2 ? 16 : 8; }
+// MB = 4, one step, kLoop: 11.5 us, of it the launch 2.5, two Gram parts 1.0,
+// the step 2.7, X 5.3; kGram with eight parts 12.7 (and no launch of 5.3 for the
+// Gram product).
 enum XGroups { kLoop = 0, kStaged = 1, kGram = 2 };
 template <int MB, int EPI, bool SWAP, int MODE>
 __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk,
@@ -818,9 +943,8 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       for (int q = 0; q < 2; ++q)
         x[ks][q] = *reinterpret_cast<const f16x8*>(src + (ks * 2 + q) * 512);
   };
-  // Block (ib, jb), jb <= ib, of the m x m results: wave 0 (0, 0), 1 (1, 0),
-  // 2 (1, 1), 3 (2, 0), ...
-  const int ib = wave >= 6 ? 3 : wave >= 3 ? 2 : wave >= 1 ? 1 : 0, jb = wave - ib * (ib + 1) / 2;
+  // Block (ib, jb) of the m x m results.
+  const int ib = sym_row(wave), jb = wave - ib * (ib + 1) / 2;
   const bool mine = wave < MB * (MB + 1) / 2;
   auto product = [&](const uint16_t* a, const uint16_t* b) {
     zero();
@@ -866,16 +990,10 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       }
     }
   };
-  // This wave's block in part sp of `of` parts of matrix mat's Gram product.
   constexpr int TILES = MB > 2 ? 3 : 1;
-  auto gram_at = [&](int sp, int of) {
-    const int tile = ib / 2 * (ib / 2 + 1) / 2 + jb / 2, b = 2 * (ib & 1) + (jb & 1);
-    return ((static_cast<int64_t>(mat) * of + sp) * TILES + tile) * kGramTile + b * 1024 +
-           lane * 4;
-  };
   const int nb = STAGED ? min(xbw, rk - static_cast<int>(blockIdx.x) * xbw) : 0;
   {  // A, from register group 2 h + q of block b in wave 2 b + h of its tile
-    const float* g = gram + gram_at(0, splits);
+    const float* g = gram + gram_at<MB>(mat, 0, splits, ib, jb, lane);
     zero();
     if (mine) {
 #pragma unroll 4
@@ -951,7 +1069,6 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
   } else {
     if (busy) times_q();
     __syncthreads();  // xs has been read: now the blocks of X, depth 32 xbw
-    auto xfrag = [&](int rb, int ks, int part) { return ((rb * 2 * xbw + ks) * 2 + part) * 512; };
     if (busy) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -959,7 +1076,8 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
 #pragma unroll
         for (int s = 0; s < 4; ++s) v[s] = acc[4 * q + s] * p.alpha;
         Parts w = split4(v);
-        store_parts(xs + xfrag(qb, 2 * (wave / MP) + (q >> 1), 0), l32 + 32 * (q & 1), 4 * half, w);
+        store_parts(xs + (qb * 2 * xbw + 2 * (wave / MP) + (q >> 1)) * 1024, l32 + 32 * (q & 1),
+                    4 * half, w);
         w.hi = transpose4(w.hi, lane & 3);
         w.lo = transpose4(w.lo, lane & 3);
         const int j0 = 4 * (l32 >> 2), row = 8 * q + 4 * half + (lane & 3);
@@ -969,20 +1087,9 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       }
     }
     __syncthreads();
-    if (!mine) return;
-    zero();
-#pragma unroll 2
-    for (int ks = 0; ks < 2 * nb; ++ks) {
-      auto at = [&](int rb, int part) {
-        return *reinterpret_cast<const f16x8*>(xs + xfrag(rb, ks, part) + lane * 8);
-      };
-      mma(at(ib, 0), at(ib, 1), at(jb, 0), at(jb, 1));
-    }
-    float* g = next_gram + gram_at(blockIdx.x, gridDim.x);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<float4*>(g + q * 256) =
-          make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+    if (mine)
+      gram_part<MB>(xs, 2 * xbw, 2 * nb, ib, jb, lane,
+                    next_gram + gram_at<MB>(mat, blockIdx.x, gridDim.x, ib, jb, lane));
   }
 }
 
@@ -993,8 +1100,8 @@ int ceil32(int v) { return (v + 31) / 32; }
 // 128, the Gram product's parts; then the norm's partials.
 struct Space {
   int64_t x, mm;  // values of one X operand, of one m x m operand
-  int tiles, splits;  // short sides up to 128: Gram tiles, depth splits
-  int gram_xbw;   // blocks of X^T a workgroup that gives the next Gram parts too, or 0
+  int tiles, splits;  // short sides up to 128: Gram tiles, parts along the depth
+  int gram_xbw;   // blocks of X^T a workgroup that gives the Gram parts too (no X then), or 0
   int64_t gram;   // floats of the Gram parts; with gram_xbw there are two such
   int64_t part;   // partial sums per matrix
   size_t bytes;
@@ -1009,20 +1116,25 @@ Space space(int n, int rows, int cols) {
   const int64_t m = ceil32(std::min(rows, cols)), k = ceil32(std::max(rows, cols));
   s.x = m * 2 * k * 1024;
   if (m <= 4) {
-    // A workgroup a CU, at least 16 slices each (two a wave).
     s.tiles = m > 2 ? 3 : 1;
-    const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, 2 * k / 16));
-    s.splits = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(most, 256 / (static_cast<int64_t>(std::max(n, 1)) * s.tiles))));
     const int mb = static_cast<int>(m), xbw = steps_staged(mb);
-    const int64_t next = (k + xbw - 1) / xbw;
-    if (next <= gram_parts(mb) && (next == 1 || next * n <= 256)) s.gram_xbw = xbw;
-    s.gram = s.tiles * std::max<int64_t>(s.splits, s.gram_xbw ? next : 0) * kGramTile;
+    const int64_t own = (k + xbw - 1) / xbw;
+    if (own <= gram_parts(mb) && (own == 1 || own * n <= 256)) {
+      s.gram_xbw = xbw;
+      s.splits = static_cast<int>(own);
+    } else {
+      // A workgroup a CU, at least 16 slices each (two a wave).
+      const int64_t most = std::min<int64_t>(16, std::max<int64_t>(1, 2 * k / 16));
+      s.splits = static_cast<int>(std::max<int64_t>(
+          1, std::min<int64_t>(most, 256 / (static_cast<int64_t>(std::max(n, 1)) * s.tiles))));
+    }
+    s.gram = static_cast<int64_t>(s.tiles) * s.splits * kGramTile;
   } else {
     s.mm = m * 2 * m * 1024;
   }
   s.part = norm_parts(n, static_cast<int64_t>(rows) * cols);
-  s.bytes = static_cast<size_t>(n) * ((3 * s.x + 5 * s.mm) * 2 + s.gram * (s.gram_xbw ? 8 : 4) + s.part * 8);
+  s.bytes = static_cast<size_t>(n) * (((s.gram_xbw ? 2 : 3) * s.x + 5 * s.mm) * 2 +
+                                      (s.gram_xbw ? 2 : 1) * s.gram * 4 + s.part * 8);
   return s;
 }
 
@@ -1094,12 +1206,24 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
   return hipGetLastError();
 }
 
-// p.a: X^T; after orth_gram_kernel.
+// f with the number of row blocks (1 to 4) as a type.
+template <typename F>
+void with_blocks(int rm, F f) {
+  switch (rm) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    case 3: f(std::integral_constant<int, 3>{}); break;
+    default: f(std::integral_constant<int, 4>{}); break;
+  }
+}
+
+// p.a: X^T; gram: `splits` parts. next_gram (NULL: not wanted): the next
+// segment's parts, of gram_xbw blocks each.
 template <int EPI, bool SWAP>
 hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm, int rk,
                         const float* gram, int splits, int gram_xbw, float* next_gram,
                         hipStream_t s) {
-  auto run = [&](auto mb) {
+  with_blocks(rm, [&](auto mb) {
     constexpr int MB = decltype(mb)::value;
     if constexpr (EPI == kOperand) {
       if (next_gram != nullptr) {
@@ -1122,13 +1246,7 @@ hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm
       orth_steps_kernel<MB, EPI, SWAP, kLoop>
           <<<grid, 1024, 0, s>>>(p, o, steps, rk, 0, gram, splits, nullptr);
     }
-  };
-  switch (rm) {
-    case 1: run(std::integral_constant<int, 1>{}); break;
-    case 2: run(std::integral_constant<int, 2>{}); break;
-    case 3: run(std::integral_constant<int, 3>{}); break;
-    default: run(std::integral_constant<int, 4>{}); break;
-  }
+  });
   return hipGetLastError();
 }
 
@@ -1153,7 +1271,7 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     base += values * 2 * n;
     return q;
   };
-  uint16_t *X = take(sp.x), *XT = take(sp.x), *XT2 = take(sp.x);
+  uint16_t *X = sp.gram_xbw ? nullptr : take(sp.x), *XT = take(sp.x), *XT2 = take(sp.x);
   uint16_t *A = take(sp.mm), *U = take(sp.mm), *P = take(sp.mm), *Q = take(sp.mm),
            *Q2 = take(sp.mm);
   float* gram = reinterpret_cast<float*>(take(2 * sp.gram));
@@ -1173,10 +1291,26 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     split<<<dim3(tr * tc, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, d.eps, part,
                                            nparts, tall ? XT : X, tall ? X : XT, sp.x, tc);
   };
-  if (vec4)
+  auto run_gram = [&](auto vec, auto mb) {
+    constexpr int V = decltype(vec)::value, MB = decltype(mb)::value;
+    orth_norm_kernel<V>
+        <<<dim3(nparts, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, chunk, part);
+    auto split = tall ? orth_split_gram_kernel<V, MB, true> : orth_split_gram_kernel<V, MB, false>;
+    split<<<dim3(sp.splits, n), 1024, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, d.eps, part,
+                                              nparts, XT, sp.x, rk, gram);
+  };
+  if (sp.gram_xbw) {
+    with_blocks(rm, [&](auto mb) {
+      if (vec4)
+        run_gram(std::integral_constant<int, 4>{}, mb);
+      else
+        run_gram(std::integral_constant<int, 1>{}, mb);
+    });
+  } else if (vec4) {
     run(orth_norm_kernel<4>, orth_split_kernel<4>);
-  else
+  } else {
     run(orth_norm_kernel<1>, orth_split_kernel<1>);
+  }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
@@ -1202,29 +1336,24 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     return sym(p);
   };
   const Segments seg = segment_rule(wm.bf16, mom != nullptr, std::min(rows, cols));
-  int left = d.steps, splits = 0;  // parts of the Gram product
+  int left = d.steps;
   for (bool first = true; left > 0; first = false) {
     const int L = std::min(left, first ? seg.first : seg.later);
     left -= L;
     if (rm <= 4) {
-      if (first || next_gram == nullptr) {
+      if (next_gram == nullptr)
         orth_gram_kernel<<<dim3(sp.tiles * sp.splits, n), 512, 0, s>>>(X, sp.x, rm, 2 * rk,
                                                                        sp.tiles, sp.splits, gram);
-        splits = sp.splits;
-      }
       Product x{XT, nullptr, sp.x, 0, X, XT2, sp.x, nullptr, 1.f / kScaleP, 0.f, 0.f};
       if (left > 0) {
-        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, gram, splits, sp.gram_xbw,
+        e = launch_steps<kOperand, false>(x, none, L, n, rm, rk, gram, sp.splits, sp.gram_xbw,
                                           next_gram, s);
         std::swap(XT, XT2);
-        if (next_gram != nullptr) {
-          std::swap(gram, next_gram);
-          splits = (rk + sp.gram_xbw - 1) / sp.gram_xbw;
-        }
+        if (next_gram != nullptr) std::swap(gram, next_gram);
       } else {
         x.alpha = 1.f / (kScaleP * kScaleX);
-        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, gram, splits, 0, nullptr, s)
-                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, gram, splits, 0, nullptr, s);
+        e = tall ? launch_steps<kOut, false>(x, out, L, n, rm, rk, gram, sp.splits, 0, nullptr, s)
+                 : launch_steps<kOut, true>(x, out, L, n, rm, rk, gram, sp.splits, 0, nullptr, s);
       }
       if (e != hipSuccess) return e;
       continue;
