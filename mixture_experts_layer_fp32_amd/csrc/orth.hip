@@ -762,6 +762,31 @@ constexpr int gram_parts(int mb) { return mb == 1 ? 32 : mb == 2 ? 16 : 8; }
 // (2, 0), ...
 __device__ __forceinline__ int sym_row(int w) { return w >= 6 ? 3 : w >= 3 ? 2 : w >= 1 ? 1 : 0; }
 
+// The matrix of this workgroup and which of the matrix's `groups` workgroups it
+// is; false past the last. runs > 0: a grid of one dimension in eight runs, one
+// an XCD (workgroup b runs on XCD b % 8), so that a matrix's workgroups share
+// the L2 that has what all of them read (8 x 128 x 512 75.8 -> 63.6 us, 8 x 32 x
+// 4096 65 -> 48). Otherwise blockIdx is (group, matrix): where a matrix has one
+// workgroup, or its Gram parts come from another kernel's order (50 x 972 x 36
+// 102 us, in runs 106).
+struct Group {
+  int mat, index, groups;
+};
+__device__ __forceinline__ bool find_group(int n, int runs, Group& g) {
+  if (runs == 0) {
+    g = {static_cast<int>(blockIdx.y), static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x)};
+    return true;
+  }
+  const int total = n * runs, per = (total + kXcds - 1) / kXcds;
+  const int u = static_cast<int>(blockIdx.x) % kXcds * per + static_cast<int>(blockIdx.x) / kXcds;
+  g = {u / runs, u % runs, runs};
+  return u < total;
+}
+int runs_of(int groups) { return groups > 1 ? groups : 0; }
+dim3 group_grid(int n, int groups) {
+  return groups > 1 ? dim3((n * groups + kXcds - 1) / kXcds * kXcds) : dim3(1, n);
+}
+
 // Block (ib, jb) in part sp of `parts` of a matrix's Gram product, as
 // orth_gram_kernel lays it out (register group 2 h + q of block b in wave 2 b + h
 // of its tile).
@@ -806,15 +831,17 @@ template <int V, int MB, bool TALL>
 __global__ __launch_bounds__(1024) void orth_split_gram_kernel(
     Mats g, Mats mom, float mu, int nesterov, int rows, int cols, float eps,
     const double* __restrict__ part, int nparts, uint16_t* __restrict__ xt_planes,
-    int64_t plane_stride, int rk, float* __restrict__ gram) {
+    int64_t plane_stride, int rk, int n, int runs, float* __restrict__ gram) {
   constexpr int XB = steps_staged(MB), KS = 2 * XB;
   constexpr int TR = TALL ? 32 * XB : 32 * MB, TC = TALL ? 32 * MB : 32 * XB;  // of U
   __shared__ float tile[TR][TC + 1];
   __shared__ __attribute__((aligned(16))) uint16_t xs[MB * KS * 1024];
   __shared__ double red[16];
-  const int mat = blockIdx.y, tid = threadIdx.x, lane = tid & 63;
+  Group me;
+  if (!find_group(n, runs, me)) return;
+  const int mat = me.mat, tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int x0 = blockIdx.x * XB, nb = min(XB, rk - x0);
+  const int x0 = me.index * XB, nb = min(XB, rk - x0);
   const int r0 = TALL ? 32 * x0 : 0, c0 = TALL ? 0 : 32 * x0;
   constexpr int NL = TR * TC / (1024 * V);
   static_assert(TR * TC % (1024 * V) == 0, "whole rounds");
@@ -876,7 +903,7 @@ __global__ __launch_bounds__(1024) void orth_split_gram_kernel(
   const int ib = sym_row(wave), jb = wave - ib * (ib + 1) / 2;
   if (wave < MB * (MB + 1) / 2)
     gram_part<MB>(xs, KS, 2 * nb, ib, jb, lane,
-                  gram + gram_at<MB>(mat, blockIdx.x, gridDim.x, ib, jb, lane));
+                  gram + gram_at<MB>(mat, me.index, me.groups, ib, jb, lane));
 }
 
 // The rest of a segment in one launch. Every workgroup adds up the Gram
@@ -886,7 +913,7 @@ __global__ __launch_bounds__(1024) void orth_split_gram_kernel(
 // take a few microseconds, a launch each would take more. A wave has one 32 x
 // 32 block: of the m x m products those on and below the diagonal (10 of 16
 // waves for MB = 4, at most 3 on a SIMD).
-// kLoop: groups of XB blocks of X^T, g = blockIdx.x, blockIdx.x + gridDim.x, ...
+// kLoop: groups of XB blocks of X^T, g = index, index + groups, ...
 // kStaged: one group of xbw blocks a workgroup, copied into LDS during the steps;
 //   while the card has a CU for each (8 x 128 x 512 91 -> 81 us; 200 x 128 x 512,
 //   as a loop of staged groups, 203 -> 220).
@@ -905,7 +932,7 @@ __global__ __launch_bounds__(1024) void orth_split_gram_kernel(
 enum XGroups { kLoop = 0, kStaged = 1, kGram = 2 };
 template <int MB, int EPI, bool SWAP, int MODE>
 __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk,
-                                                          int xbw, const float* __restrict__ gram,
+                                                          int xbw, int n, int runs, const float* __restrict__ gram,
                                                           int splits,
                                                           float* __restrict__ next_gram) {
   constexpr bool STAGED = MODE != kLoop;
@@ -916,7 +943,9 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
   __shared__ __attribute__((aligned(1024))) uint16_t
       xs[STAGED ? steps_staged(MB) * KS * 1024 : 8];
   uint16_t *ba = bufs[0], *bp = bufs[1];
-  const int mat = blockIdx.y, lane = threadIdx.x & 63;
+  Group me;
+  if (!find_group(n, runs, me)) return;
+  const int mat = me.mat, lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = lane >> 5, l32 = lane & 31;
   auto frag = [&](const uint16_t* op, int rb, int ks, int part) {
@@ -991,7 +1020,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
     }
   };
   constexpr int TILES = MB > 2 ? 3 : 1;
-  const int nb = STAGED ? min(xbw, rk - static_cast<int>(blockIdx.x) * xbw) : 0;
+  const int nb = STAGED ? min(xbw, rk - me.index * xbw) : 0;
   {  // A, from register group 2 h + q of block b in wave 2 b + h of its tile
     const float* g = gram + gram_at<MB>(mat, 0, splits, ib, jb, lane);
     zero();
@@ -1009,7 +1038,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
       }
     }
     if constexpr (STAGED) {  // X^T on its way into LDS, 1 KB a copy
-      const int x0 = blockIdx.x * xbw;
+      const int x0 = me.index * xbw;
       const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(p.a + mat * p.sa + static_cast<int64_t>(x0) * (KS * 1024)), 0, nb * KS * 2048,
           0x00020000);
@@ -1038,7 +1067,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
     __syncthreads();
   }
   const int qb = wave % MP, per = STAGED ? xbw : XB;
-  int xb = blockIdx.x * per + wave / MP;
+  int xb = me.index * per + wave / MP;
   const bool busy = qb < MB && wave / MP < per && xb < rk;
   if (MODE != kGram && !busy) return;
   auto times_q = [&]() {  // acc <- the block of X^T times Q
@@ -1057,7 +1086,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
   };
   if constexpr (MODE != kGram) {
 #pragma unroll 1
-    for (; xb < rk; xb += STAGED ? rk : gridDim.x * XB) {
+    for (; xb < rk; xb += STAGED ? rk : me.groups * XB) {
       if constexpr (!STAGED) load_x(xb);
       times_q();
       float v[4][4];
@@ -1089,7 +1118,7 @@ __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int 
     __syncthreads();
     if (mine)
       gram_part<MB>(xs, 2 * xbw, 2 * nb, ib, jb, lane,
-                    next_gram + gram_at<MB>(mat, blockIdx.x, gridDim.x, ib, jb, lane));
+                    next_gram + gram_at<MB>(mat, me.index, me.groups, ib, jb, lane));
   }
 }
 
@@ -1229,7 +1258,8 @@ hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm
       if (next_gram != nullptr) {
         const int groups = (rk + gram_xbw - 1) / gram_xbw;
         orth_steps_kernel<MB, EPI, SWAP, kGram>
-            <<<dim3(groups, n), 1024, 0, s>>>(p, o, steps, rk, gram_xbw, gram, splits, next_gram);
+            <<<group_grid(n, groups), 1024, 0, s>>>(p, o, steps, rk, gram_xbw, n,
+                                                    runs_of(groups), gram, splits, next_gram);
         return;
       }
     }
@@ -1240,11 +1270,12 @@ hipError_t launch_steps(const Product& p, const Out& o, int steps, int n, int rm
     while (xbw < steps_staged(MB) && !fits(xbw)) xbw *= 2;
     if (fits(xbw)) {
       orth_steps_kernel<MB, EPI, SWAP, kStaged>
-          <<<dim3(groups_of(xbw), n), 1024, 0, s>>>(p, o, steps, rk, xbw, gram, splits, nullptr);
+          <<<group_grid(n, groups_of(xbw)), 1024, 0, s>>>(
+              p, o, steps, rk, xbw, n, runs_of(groups_of(xbw)), gram, splits, nullptr);
     } else {
-      const dim3 grid(std::min(groups_of(steps_xb(MB)), std::max(1, 256 / n)), n);
+      const int groups = std::min(groups_of(steps_xb(MB)), std::max(1, 256 / n));
       orth_steps_kernel<MB, EPI, SWAP, kLoop>
-          <<<grid, 1024, 0, s>>>(p, o, steps, rk, 0, gram, splits, nullptr);
+          <<<dim3(groups, n), 1024, 0, s>>>(p, o, steps, rk, 0, n, 0, gram, splits, nullptr);
     }
   });
   return hipGetLastError();
@@ -1296,8 +1327,9 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
     orth_norm_kernel<V>
         <<<dim3(nparts, n), 256, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, chunk, part);
     auto split = tall ? orth_split_gram_kernel<V, MB, true> : orth_split_gram_kernel<V, MB, false>;
-    split<<<dim3(sp.splits, n), 1024, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, d.eps, part,
-                                              nparts, XT, sp.x, rk, gram);
+    split<<<group_grid(n, sp.splits), 1024, 0, s>>>(gm, mm, d.mu, d.nesterov, rows, cols, d.eps,
+                                                    part, nparts, XT, sp.x, rk, n, runs_of(sp.splits),
+                                                    gram);
   };
   if (sp.gram_xbw) {
     with_blocks(rm, [&](auto mb) {
