@@ -756,7 +756,7 @@ __global__ __launch_bounds__(512) void orth_gram_kernel(const uint16_t* __restri
 // one a wave and row block; as many as its LDS holds; and most Gram parts.
 constexpr int steps_xb(int mb) { return mb == 1 ? 16 : mb == 2 ? 8 : 4; }
 constexpr int steps_staged(int mb) { return mb == 4 ? 2 : 4; }  // 48 KB or less
-constexpr int gram_parts(int mb) { return mb == 1 ? 32 : mb == 2 ? 16 : 8; }
+constexpr int gram_parts(int mb) { return mb <= 2 ? 32 : 16; }
 
 // Row block of the w-th block on or below the diagonal: (0, 0), (1, 0), (1, 1),
 // (2, 0), ...
@@ -922,7 +922,9 @@ __global__ __launch_bounds__(1024) void orth_split_gram_kernel(
 //   memory (8 x 128 x 512 81 -> 75 us, 32 x 128 x 256 94 -> 77). As many blocks
 //   a workgroup as LDS holds, since every workgroup adds up all parts of its
 //   matrix (8 x 128 x 512 as 8 parts 75 us, as 16 84), and up to gram_parts()
-//   parts: about 0.3 MB to read. While a CU for each workgroup is there, or one
+//   parts (16 parts of 16 x 128 x 1024 115 -> 94 us, of 4 x 128 x 1024 81 -> 83,
+//   32 of 1 x 128 x 2048 72 -> 88; 30 of 4 x 64 x 3840 83 -> 67, 63 of 2 x 32 x
+//   8000 75 -> 83). While a CU for each workgroup is there, or one
 //   workgroup is all of a matrix (512 x 64 x 64 80 -> 67 us; 60 x 128 x 512, 480
 //   workgroups, 133 -> 190: the steps are repeated in each).
 // SWAP: the result's rows are those of Q (kOut of a wide matrix).
