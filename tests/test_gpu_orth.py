@@ -289,3 +289,26 @@ def test_same_bits_on_another_stream_and_in_a_graph():
     out2 = torch.empty_like(out)
     moe.moe_orthogonalize(g, out2, big)
     assert torch.equal(out2, ref[0])
+
+
+@pytest.mark.parametrize("n,rows,cols", [(5, 120, 300), (300, 64, 40)])
+def test_short_sides_in_a_graph_and_two_at_once(n, rows, cols):
+    print(f"[orth] graph n={n} {rows}x{cols}", flush=True)
+    g, g2 = _randn(n, rows, cols, seed=21).cuda(), _randn(n, rows, cols, seed=22).cuda()
+    m0, w0 = _randn(n, rows, cols, seed=23).cuda(), _randn(n, rows, cols, seed=24).cuda()
+    m, w, ws, ws2 = m0.clone(), w0.clone(), _ws(n, rows, cols), _ws(n, rows, cols)
+    moe.moe_muon_update(g, m, w, ws, lr=0.02)
+    ref, ref2 = [m.clone(), w.clone()], _orth(g2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_muon_update(g, m, w, ws, lr=0.02)
+    side, out2 = torch.cuda.Stream(), torch.empty_like(g2)
+    for _ in range(3):
+        m.copy_(m0)
+        w.copy_(w0)
+        out2.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        moe.moe_orthogonalize(g2, out2, ws2, stream=side.cuda_stream)  # beside it
+        torch.cuda.synchronize()
+        assert torch.equal(m, ref[0]) and torch.equal(w, ref[1]) and torch.equal(out2, ref2)
