@@ -470,21 +470,17 @@ __device__ __forceinline__ void store_block(const Product& p, const Out& o, int 
 // kOperand: alpha D is stored into out_t and out_n.
 // kOut: to the caller's matrices (rows i, columns j).
 // blockIdx.y: one of two independent products.
-// PARTS 1: the high parts alone, one matrix instruction a product instead of
-//   three and half the bytes, for the last product of a Muon step on bf16
-//   weights (128 x 768 x 2048: 1410 -> 1130 us). Its fp16 operands (11 bits)
-//   cost O 2.7e-4 (full rank) to 3.3e-3 (rank 8) of its size, simulated; W's
-//   own rounding to 8 bits is far above lr scale times that wherever the step
-//   is smaller than the weight. moe_orthogonalize, whose result is O, keeps
-//   both parts, and so do the products before the last, where such errors
-//   would grow with the later steps.
-template <int EPI, int PARTS, int WM, int WN, int WR, int WC>
+// Every product has both fp16 parts, the last one of a bf16 result too: its high
+// parts alone (11 bits) put O off by 3e-4 at full rank and by 3.3e-3 below it,
+// where Q is near 11.9 I off the gradient's range and all of its diagonal rounds
+// the same way, twice bf16's own rounding.
+template <int EPI, int WM, int WN, int WR, int WC>
 __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, Product p1,
                                                                    Out o, int n, int ra, int rb,
                                                                    int KS) {
   constexpr int BA = WR * WM, BB = WC * WN;    // 32-row blocks per tile
   constexpr int NW = WR * WC;
-  constexpr int SS = PARTS == 2 ? 2 : 4;       // slices a step
+  constexpr int SS = 2;                        // slices a step
   constexpr int kStage = (BA + BB) * 4096;
   constexpr int NC = (BA + BB) * 4 / NW;       // 1 KB copies per wave and step
   static_assert((BA + BB) * 4 % NW == 0 && BA * 4 % NC == 0, "copies are shared out evenly");
@@ -516,14 +512,13 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
   int voff[NC];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
-    voff[i] = ((piece0 + i) >> 2) * row_bytes + ((piece0 + i) & 3) * (2048 / PARTS) + lane * 16;
+    voff[i] = ((piece0 + i) >> 2) * row_bytes + ((piece0 + i) & 3) * 1024 + lane * 16;
   const unsigned lds_w = (unsigned)(uintptr_t)(lds_u8*)smem + wave * NC * 1024;
-  const int nk = (KS + SS - 1) / SS;
+  const int nk = KS / SS;  // KS is even
   // A copy past the last slice is still issued, out of range (it writes
   // zeros), so the K loop has no branch around it.
   auto copy = [&](int i, int kt) {
-    const int slice = kt * SS + (PARTS == 2 ? 0 : (piece0 + i) & 3);
-    dma16(rsrc, slice < KS ? voff[i] : kOutOfRange, kt * (SS * 2048),
+    dma16(rsrc, kt < nk ? voff[i] : kOutOfRange, kt * (SS * 2048),
           lds_w + (kt & 1) * kStage + i * 1024);
   };
 
@@ -538,9 +533,8 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
   // The K loop over the wave's first NJ block columns.
   auto run = [&](auto nj_c) {
     constexpr int NJ = decltype(nj_c)::value;
-    // Fragments of half a step: WM of a, then NJ of b, two each: [hi, lo] of
-    // one slice, or hi of two slices.
-    constexpr int NF = NJ > 0 ? 2 * (WM + NJ) : 0, NM = (PARTS == 2 ? 3 : 2) * WM * NJ;
+    // Fragments of half a step: WM of a, then NJ of b, [hi, lo] of one slice each.
+    constexpr int NF = NJ > 0 ? 2 * (WM + NJ) : 0, NM = 3 * WM * NJ;
     f16x8 fr[2][NF > 0 ? NF : 1];
     auto read = [&](int f, int kt, int ks) {
       const int blk = f / 2 < WM ? wr * WM + f / 2 : BA + wc * WN + f / 2 - WM;
@@ -560,10 +554,8 @@ __global__ __launch_bounds__(64 * WR * WC) void orth_product_kernel(Product p0, 
 #pragma unroll
           for (int y = x * n / NM; y < (x + 1) * n / NM; ++y) side(y);
           __builtin_amdgcn_sched_barrier(0);
-          const int qa = PARTS == 2 ? q == 0 : q, qb = PARTS == 2 ? q == 1 : q;
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[ks][2 * i + qa],
-                                                             fr[ks][2 * (WM + j) + qb], acc[i][j],
-                                                             0, 0, 0);
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              fr[ks][2 * i + (q == 0)], fr[ks][2 * (WM + j) + (q == 1)], acc[i][j], 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -1211,7 +1203,7 @@ int64_t tile_count(int B, int n, int ra, int rb) {
 // 576, 73 us, 82 as 160 of 256); then whichever takes less by its rounds, one
 // of 256-tiles counting as 1.9 of 128-tiles up to that depth, as 1.7 beyond
 // (4096 x 14336, X <- Q X: 4 rounds 1.21 ms, 7 rounds 1.28).
-template <int EPI, int PARTS = 2>
+template <int EPI>
 hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, int rb, int KS,
                           int& flip, hipStream_t s) {
   auto grid = [&](int B) {
@@ -1231,9 +1223,9 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
       orth_product_small_kernel<EPI, 4><<<grid(2), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
   } else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) ||
            (KS <= 64 ? 19 : 17) * ((t256 + 255) / 256) > 10 * ((t128 + 511) / 512))
-    orth_product_kernel<EPI, PARTS, 2, 1, 2, 4><<<grid(4), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
+    orth_product_kernel<EPI, 2, 1, 2, 4><<<grid(4), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
-    orth_product_kernel<EPI, PARTS, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
+    orth_product_kernel<EPI, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   return hipGetLastError();
 }
 
@@ -1431,9 +1423,7 @@ hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const m
         std::swap(x.sa, x.sb);
       }
       const int ra = tall ? rk : rm, rb = tall ? rm : rk;
-      e = wm.bf16 && mom != nullptr
-              ? launch_product<kOut, 1>(x, nullptr, out, n, ra, rb, 2 * rm, flip, s)
-              : launch_product<kOut>(x, nullptr, out, n, ra, rb, 2 * rm, flip, s);
+      e = launch_product<kOut>(x, nullptr, out, n, ra, rb, 2 * rm, flip, s);
     }
     if (e != hipSuccess) return e;
   }
