@@ -149,6 +149,19 @@ struct Exchange {
   float f[2][2][G / 64];
 };
 
+// Sum of a vector's values, by halves.
+template <int N>
+__device__ __forceinline__ float vec_sum(const float (&f)[N]) {
+  float q[N / 2];
+#pragma unroll
+  for (int e = 0; e < N / 2; ++e) q[e] = f[e] + f[e + N / 2];
+#pragma unroll
+  for (int h = N / 4; h > 0; h /= 2)
+#pragma unroll
+    for (int e = 0; e < h; ++e) q[e] += q[e + h];
+  return q[0];
+}
+
 // mean and 1 / sqrt(variance + eps) of the group's values f (places that hold
 // none are zeros; cnt of the thread's, n_wave of the wave's are values). Each
 // wave takes its own mean and centred sum of squares; the waves' are joined
@@ -158,21 +171,9 @@ template <int G, int NV, int N>
 __device__ __forceinline__ void row_stats(const float (&f)[NV][N], const int (&cnt)[NV],
                                           float n_wave, int D, float eps, Exchange<G>& ex,
                                           int& slot, float& mean, float& rstd) {
-  float part[NV];
+  double s = vec_sum<N>(f[0]);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float q[N / 2];
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) q[e] = f[i][e] + f[i][e + N / 2];
-#pragma unroll
-    for (int h = N / 4; h > 0; h /= 2)
-#pragma unroll
-      for (int e = 0; e < h; ++e) q[e] += q[e + h];
-    part[i] = q[0];
-  }
-  double s = part[0];
-#pragma unroll
-  for (int i = 1; i < NV; ++i) s += part[i];
+  for (int i = 1; i < NV; ++i) s += vec_sum<N>(f[i]);
   s = wave_sum(s);
   const float mw = n_wave > 0.f ? static_cast<float>(s / n_wave) : 0.f;
   float m2 = 0.f;
@@ -230,6 +231,19 @@ __device__ __forceinline__ void group_sum(float (&s)[2], Exchange<G>& ex, int& s
   }
 }
 
+// The same of one value in fp64 (G > 64).
+template <int G>
+__device__ __forceinline__ double group_sum(double s, Exchange<G>& ex, int& slot) {
+  s = wave_sum(s);
+  if ((threadIdx.x & 63) == 0) ex.s[slot][threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0.0;
+#pragma unroll
+  for (int w = 0; w < G / 64; ++w) s += ex.s[slot][w];
+  slot ^= 1;
+  return s;
+}
+
 constexpr int wg_of(int G) { return G == 64 ? 256 : G; }
 
 // ---- forward: the row in registers -----------------------------------------
@@ -285,7 +299,10 @@ __global__ __launch_bounds__(wg_of(G)) void norm_fwd_kernel(
 }
 
 // ---- forward: rows wider than the registers hold ---------------------------
-// One workgroup a row; the second and third reads of x come from the caches.
+// One workgroup a row; the second and third reads of x come from the caches. A
+// thread adds up to 256 values: from vector to vector in fp64, as across threads
+// (in fp32 the y of a constant row of 262144 values 1000.1 was 0.6 instead of 0;
+// the pass is bound by memory either way).
 template <typename T>
 __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
@@ -299,14 +316,12 @@ __global__ __launch_bounds__(1024) void norm_fwd_wide_kernel(
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const T* xr = x + r * D;
     float f[N], s[2] = {0.f, 0.f};
+    double sum = 0.0;
     for (int v = t; v < nvec; v += G) {
       Vec<T>::unpack(load_vec(xr, v, nfull, D), f);
-#pragma unroll
-      for (int e = 0; e < N; ++e) s[0] += f[e];
+      sum += vec_sum<N>(f);
     }
-    group_sum<G>(s, ex, slot);
-    const float mean = s[0] / fd;  // (a constant row's mean is exact where its sum is)
-    s[0] = s[1] = 0.f;
+    const float mean = static_cast<float>(group_sum<G>(sum, ex, slot) / D);
     for (int v = t; v < nvec; v += G) {
       Vec<T>::unpack(load_vec(xr, v, nfull, D), f);
 #pragma unroll
