@@ -146,20 +146,17 @@ __device__ __forceinline__ S wave_sum(S v) {
 template <int G>
 struct Exchange {
   double s[2][G / 64];
-  float f[2][2][G / 64];
+  float f[2][3][G / 64];
 };
 
-// Sum of a vector's values, by halves.
+// Sum of a vector's values: of four in fp32, of the fours in fp64 (eight bf16
+// values of 2^125 leave fp32's range; of either type values below 2^126 do not).
 template <int N>
-__device__ __forceinline__ float vec_sum(const float (&f)[N]) {
-  float q[N / 2];
+__device__ __forceinline__ double vec_sum(const float (&f)[N]) {
+  double s = (f[0] + f[2]) + (f[1] + f[3]);
 #pragma unroll
-  for (int e = 0; e < N / 2; ++e) q[e] = f[e] + f[e + N / 2];
-#pragma unroll
-  for (int h = N / 4; h > 0; h /= 2)
-#pragma unroll
-    for (int e = 0; e < h; ++e) q[e] += q[e + h];
-  return q[0];
+  for (int e = 4; e < N; e += 4) s += (f[e] + f[e + 2]) + (f[e + 1] + f[e + 3]);
+  return s;
 }
 
 // mean and 1 / sqrt(variance + eps) of the group's values f (places that hold
@@ -189,6 +186,7 @@ __device__ __forceinline__ void row_stats(const float (&f)[NV][N], const int (&c
       ex.s[slot][threadIdx.x >> 6] = s;
       ex.f[slot][0][threadIdx.x >> 6] = m2;
       ex.f[slot][1][threadIdx.x >> 6] = n_wave;
+      ex.f[slot][2][threadIdx.x >> 6] = mw;
     }
     __syncthreads();
     s = 0.0;
@@ -199,7 +197,7 @@ __device__ __forceinline__ void row_stats(const float (&f)[NV][N], const int (&c
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float nw = ex.f[slot][1][w];
-      const float d = nw > 0.f ? static_cast<float>(ex.s[slot][w]) / nw - mean : 0.f;
+      const float d = nw > 0.f ? ex.f[slot][2][w] - mean : 0.f;
       m2 += fmaf(nw * d, d, ex.f[slot][0][w]);
     }
     slot ^= 1;

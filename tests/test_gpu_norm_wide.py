@@ -69,3 +69,18 @@ def test_rows_far_from_zero(D, dtype):
     assert np.all(np.abs(_np(rstd) - rr) <= rr * ev)
     tol = (em * rr)[:, None] + np.abs(ry) * (ev[:, None] + 3 * U) + HALF[dt] * np.abs(ry)
     assert np.all(np.abs(_np(y) - ry) <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [8, 300, 1031, 2048, 9001, 16391])
+def test_sums_past_the_range(D, dtype):
+    """Values whose mean is in fp32's range and whose sums are not."""
+    print(f"[norm] large D={D} {dtype}", flush=True)
+    values = torch.tensor([2.0 ** 122, -2.0 ** 125]).to(DT[dtype])
+    x = values[:, None].expand(2, D).contiguous().cuda()
+    y, (mean, rstd) = torch.full_like(x, 7.0), torch.empty(2, 2, device="cuda")
+    moe.moe_layer_norm(x, None, None, 1e-5, y, mean, rstd)
+    torch.cuda.synchronize()
+    assert torch.equal(mean.cpu(), values.float()) and not y.any()
+    # eps rounded to fp32, a root and a division: 2 u of 1 / sqrt(eps)
+    assert np.all(np.abs(_np(rstd) * np.sqrt(1e-5) - 1) <= 3 * U)
