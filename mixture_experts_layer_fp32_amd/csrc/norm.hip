@@ -361,9 +361,11 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
   int slot = 0;
   const int t = threadIdx.x % G, grp = threadIdx.x / G, nfull = D / N;
   float gm[NV][N], dg[NV][N], db[NV][N];
+  int cnt[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     load_param<N>(gamma, t + i * G, D, 1.f, gm[i]);
+    cnt[i] = min(max(D - (t + i * G) * N, 0), N);
 #pragma unroll
     for (int e = 0; e < N; ++e) dg[i][e] = db[i][e] = 0.f;
   }
@@ -399,14 +401,16 @@ __global__ __launch_bounds__(wg_of(G)) void norm_bwd_kernel(
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        h[i][e] = (h[i][e] - mean) * rstd;
+        // Places past D hold d = 0, and h = 0: -mean rstd may be infinite where
+        // (x - mean) rstd is not, in rows of nearly equal values above 1e36.
+        // (Up to 3 % at ragged widths; a branch around it, or x = mean there,
+        // cost as much or more.)
+        h[i][e] = e < cnt[i] ? (h[i][e] - mean) * rstd : 0.f;
         if (PARAMS) {
           dg[i][e] = fmaf(d[i][e], h[i][e], dg[i][e]);
           db[i][e] += d[i][e];
         }
         d[i][e] *= gm[i][e];
-        // Places past D hold d = 0 and a finite h unless the row's own
-        // statistics are not finite, and then the whole row is NaN anyway.
         s[0] += d[i][e];
         s[1] = fmaf(d[i][e], h[i][e], s[1]);
       }
@@ -469,11 +473,17 @@ __global__ __launch_bounds__(1024) void norm_bwd_wide_kernel(
   const float fd = static_cast<float>(D);
   for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
     const float mean = mean_in[r], rstd = rstd_in[r];
+    const bool far = isinf(mean * rstd);
     float h[N], d[N], gm[N], s[2] = {0.f, 0.f};
     for (int v = t; v < nvec; v += G) {
       Vec<T>::unpack(load_vec(x + r * D, v, nfull, D), h);
       Vec<T>::unpack(load_vec(dy + r * D, v, nfull, D), d);
       load_param<N>(gamma, v, D, 1.f, gm);
+      if (far && v == nfull) {  // h = 0 past D, as in the registers' kernel
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (v * N + e >= D) h[e] = mean;
+      }
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         s[0] = fmaf(d[e], gm[e], s[0]);

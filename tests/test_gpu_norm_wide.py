@@ -84,3 +84,30 @@ def test_sums_past_the_range(D, dtype):
     assert torch.equal(mean.cpu(), values.float()) and not y.any()
     # eps rounded to fp32, a root and a division: 2 u of 1 / sqrt(eps)
     assert np.all(np.abs(_np(rstd) * np.sqrt(1e-5) - 1) <= 3 * U)
+
+
+@pytest.mark.parametrize("gamma", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [63, 300, 1031, 9001, 16391, 40001])
+def test_backward_of_large_constant_rows(D, dtype, gamma):
+    """mean rstd leaves fp32's range, (x - mean) rstd = 0 does not: the places of
+    the last vector past D add nothing, and dx = rstd (g - mean(g))."""
+    print(f"[norm] backward of constant rows D={D} {dtype} {gamma}", flush=True)
+    dt, gen = DT[dtype], torch.Generator().manual_seed(D)
+    x = torch.tensor([2.0 ** 122, -2.0 ** 125])[:, None].expand(2, D).contiguous().to(dt).cuda()
+    gm = (1 + 0.2 * torch.randn(D, generator=gen)).cuda() if gamma else None
+    dy = torch.randn(2, D, generator=gen).to(dt).cuda()
+    y, dx = torch.empty_like(x), torch.full_like(x, 7.0)
+    mean, rstd = torch.empty(2, 2, device="cuda")
+    dgamma, dbeta = torch.full((2, D), 7.0, device="cuda")
+    moe.moe_layer_norm(x, gm, None, 1e-5, y, mean, rstd)
+    moe.moe_layer_norm_backward(x, dy, gm, mean, rstd, None, dx, dgamma, dbeta,
+                                moe.workspace(moe.moe_layer_norm_backward_workspace_size(2, D)))
+    torch.cuda.synchronize()
+    assert not y.any() and not dgamma.any()
+    g = _np(dy) * (_np(gm) if gamma else 1.0)
+    ref = _np(rstd)[:, None] * (g - g.mean(1, keepdims=True))
+    # dy gamma and the difference round once each, their mean at most 300 times
+    tol = _np(rstd)[:, None] * (3 * U * np.abs(g) + 300 * U * np.abs(g).mean(1, keepdims=True))
+    assert np.all(np.abs(_np(dx) - ref) <= tol + (HALF[dt] + 2 * U) * np.abs(ref))
+    assert np.all(np.abs(_np(dbeta) - _np(dy).sum(0)) <= 2 * U * np.abs(_np(dy)).sum(0))
