@@ -36,9 +36,10 @@ def _gpu_and_library():
     torch.cuda.synchronize()
 
 
-def _tol(rank):
+def _tol(rank, steps=5):
     a, root = 3.4445, np.sqrt(rank)
-    return E * sum(a ** (5 - i) * min(a ** i, 1.21 * root) for i in range(6)) / (0.68 * root)
+    return E * sum(a ** (steps - i) * min(a ** i, 1.21 * root)
+                   for i in range(steps + 1)) / (0.68 * root)
 
 
 def _gradients(n, rows, cols, rank, seed):
@@ -54,9 +55,13 @@ def _ws(n, rows, cols):
     return moe.workspace(moe.moe_orthogonalize_workspace_size(n, rows, cols))
 
 
-def _check(got, ref, rank, what):
+def _exact(g, steps=5):
+    return ou.orthogonalize(g.double().cpu().numpy(), steps)
+
+
+def _check(got, ref, rank, what, steps=5):
     """got [rows, cols] (fp32 or bf16) against the float64 ref."""
-    tol = _tol(rank or min(ref.shape)) * np.linalg.norm(ref)
+    tol = _tol(min(rank or min(ref.shape), *ref.shape), steps) * np.linalg.norm(ref)
     err = np.linalg.norm(got.detach().double().cpu().numpy() - ref)
     if got.dtype == BF16:
         own = np.linalg.norm(torch.from_numpy(ref).to(BF16).double().numpy() - ref)
@@ -81,4 +86,45 @@ def test_muon_on_bf16_weights(n, rows, cols, rank):
     moe.moe_muon_update(g, m, w, _ws(n, rows, cols), lr=1.0, nesterov=False)
     torch.cuda.synchronize()
     for i in (0, n - 1):
-        _check(-w[i], ou.orthogonalize(g[i].double().cpu().numpy()), rank, i)
+        _check(-w[i], _exact(g[i]), rank, i)
+
+
+# The same, and short sides that take a launch of their own for the Gram product
+# (many matrices, a long side).
+@pytest.mark.parametrize("rank", [0, 64, 8, 1])
+@pytest.mark.parametrize("n,rows,cols", SHAPES + [(60, 128, 520), (2, 4200, 30)])
+def test_fp32_and_bf16_results(n, rows, cols, rank):
+    """moe_orthogonalize into both types, and the Muon step on fp32 weights that
+    start at zero: segments of one, two and three steps, on both sides of 128."""
+    print(f"[orth] n={n} {rows}x{cols} rank={rank}", flush=True)
+    g = _gradients(n, rows, cols, rank, seed=rows + rank + 1)
+    f, h, ws = torch.full_like(g, 7.0), torch.full_like(g, 7.0, dtype=BF16), _ws(n, rows, cols)
+    moe.moe_orthogonalize(g, f, ws)
+    moe.moe_orthogonalize(g, h, ws)
+    m, w = torch.zeros_like(g), torch.zeros_like(g)
+    moe.moe_muon_update(g, m, w, ws, lr=1.0, nesterov=False)
+    torch.cuda.synchronize()
+    for i in (0, n - 1):
+        ref = _exact(g[i])
+        for name, got in (("fp32", f[i]), ("bf16", h[i]), ("muon", -w[i])):
+            _check(got, ref, rank, (name, i))
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("rank", [0, 8, 1])
+@pytest.mark.parametrize("n,rows,cols", [(3, 90, 200), (2, 256, 512)])
+def test_more_steps(n, rows, cols, rank, out_dtype):
+    """Eight steps within the bound for eight. Sixteen: outside a low-rank
+    gradient's range rounding has become as large as the result (as the header
+    says), which still has no singular value above 1.21."""
+    print(f"[orth] steps n={n} {rows}x{cols} rank={rank} {out_dtype}", flush=True)
+    g = _gradients(n, rows, cols, rank, seed=rows + rank + 2)
+    out = torch.empty_like(g, dtype=out_dtype)
+    moe.moe_orthogonalize(g, out, _ws(n, rows, cols), steps=8)
+    for i in (0, n - 1):
+        _check(out[i], _exact(g[i], 8), rank, i, steps=8)
+    moe.moe_orthogonalize(g, out, _ws(n, rows, cols), steps=16)
+    for i in (0, n - 1):
+        assert torch.isfinite(out[i]).all()
+        # 1.205 is the iteration's largest value on [0, 1.21]; bf16 rounds
+        assert np.linalg.norm(out[i].double().cpu().numpy(), 2) <= 1.22
