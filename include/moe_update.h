@@ -43,8 +43,16 @@ typedef struct {
  * zero matrix gives zeros; a matrix with a NaN or an infinite value gives NaN
  * throughout; the other matrices do not change.
  * Precision: every product runs on the fp16 matrix cores with each fp32 value
- * held as two fp16 parts (23 significant bits), summed in fp32; the Frobenius
- * norm is summed in fp64. Errors are those of fp32 arithmetic.
+ * held as two fp16 parts (within 2^-22 of it), summed in fp32; the Frobenius
+ * norm is summed in fp64. Measured against 64 bits, as a share of ||out||_F,
+ * for five steps into an fp32 out: 0.6e-6 to 6e-6 where G has full rank, 4e-6 to
+ * 1.5e-4 for ranks from 64 down to 1 (fp32 arithmetic, measured the same way:
+ * 1.3e-6 to 4e-6, and 3e-6 to 2.6e-4). A bf16 out, whose own rounding is 1.7e-3,
+ * takes more of its steps between two products X X^T: up to 1e-5 at full rank.
+ * Steps past five: outside the range of a G of low rank every step multiplies
+ * rounding errors by 3.4445, in this as in any arithmetic. At ranks 1 and 8 the
+ * error is 1e-3 to 4e-3 after 8 steps, 0.1 to 0.6 after 12, and after 16 the
+ * result has directions that G does not have.
  *
  *  n      matrices (>= 0; 0: nothing is done), at most 65535
  *  rows, cols   1 .. MOE_MAX_WIDTH; the smaller one at most 32768;
@@ -87,9 +95,10 @@ typedef struct {
  * moe_muon_update - one Muon step for each matrix, in place:
  *   M <- mu M + G;  U = G + mu M (nesterov) or M;
  *   W <- (1 - lr weight_decay) W - lr scale O,  O = moe_orthogonalize(U).
- * fp32 throughout; W is rounded once to its type (to nearest even: with bf16
- * weights, steps below half a unit in W's last place leave W as it is). A
- * matrix without gradient (G = 0, M = 0) is only decayed.
+ * fp32, with the products of moe_orthogonalize in O, before and in the last one
+ * alike; W is rounded once to its type (to nearest even: with bf16 weights, steps
+ * below half a unit in W's last place leave W as it is). A matrix without
+ * gradient (G = 0, M = 0) is only decayed.
  *
  *  g         dtype MOE_F32 or MOE_BF16 (LayerTrain's gradients are fp32)
  *  momentum  dtype MOE_F32   in and out
