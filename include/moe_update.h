@@ -63,8 +63,10 @@ typedef struct {
  *  out    dtype MOE_F32 or MOE_BF16; may be g itself (same data, ld, stride
  *         and dtype), otherwise it must not overlap g
  *  ws     workspace of at least moe_orthogonalize_workspace_size() bytes
- *         (about 12 n rows cols + 20 n m^2; for m up to 128 at most about
- *         12 n rows cols + the larger of 26 MB and 96 n KB), 256-byte aligned
+ *         (with R, C and M the sizes rows, cols and m rounded up to multiples
+ *         of 32: at most 12 n R C + 20 n M^2 + 8 n KB, for m up to 128 at most
+ *         12 n R C + the larger of 26 MB and 96 n KB; thin matrices take far
+ *         more than their values), 256-byte aligned
  * Errors: INVALID_ARG (sizes, NULL pointers, ld, stride, eps, steps, a
  * misaligned ws), UNSUPPORTED (dtype, sizes past the limits), WORKSPACE.
  */
