@@ -54,7 +54,7 @@ typedef __attribute__((address_space(3))) unsigned char lds_u8;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr float kScaleX = 4096.f, kScaleA = 4096.f, kScaleP = 1024.f;
 constexpr int kXcds = 8;
-constexpr int kSmallTiles = 128, kMidTiles = 512, kMidTilesShort = 640;
+constexpr int kSmallTiles = 128;
 
 struct Mats {  // moe_matrices on the device side
   void* data;
@@ -1198,11 +1198,13 @@ int64_t tile_count(int B, int n, int ra, int rb) {
 // tiles of 128) 384 / 455 / - us; 2048^2 (136) 1052 / 913 / -; 4096 x 14336
 // (528) 9998 / 8003 / 7640; 32 x 1024^2 (1152) - / 2552 / 2660; 256 x 64 x 256
 // (256, a quarter of each used) 134 / 157 / -. So: small tiles up to half a
-// 128-tile a CU and where 128-tiles would compute twice their area; 128-tiles
-// while one round holds them (and up to 640 at depths up to 1024: 16 x 1024^2,
-// 576, 73 us, 82 as 160 of 256); then whichever takes less by its rounds, one
-// of 256-tiles counting as 1.9 of 128-tiles up to that depth, as 1.7 beyond
-// (4096 x 14336, X <- Q X: 4 rounds 1.21 ms, 7 rounds 1.28).
+// 128-tile a CU and where 128-tiles would compute twice their area; of the others
+// whichever take less by their rounds, one of 256-tiles counting as 1.9 of
+// 128-tiles at depths up to 1024, as 1.7 beyond (4096 x 14336, X <- Q X: 4 rounds
+// 1.21 ms, 7 rounds 1.28). Symmetric products of 513 to 640 128-tiles, two rounds
+// against one of 256-tiles, whole calls (128 / 256): 16 x 1024^2 1363 / 1331 us,
+// 28 x 768^2 1150 / 1098, 58 x 512^2 917 / 850, 175 x 256^2 590 / 510, 40 x 640^2
+// 1048 / 1050, 19 x 896^2 1229 / 1253, 29 x 700^2 1031 / 1061.
 template <int EPI>
 hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, int rb, int KS,
                           int& flip, hipStream_t s) {
@@ -1221,8 +1223,7 @@ hipError_t launch_product(Product p0, Product* p1, const Out& o, int n, int ra, 
       orth_product_small_kernel<EPI, 8><<<grid(2), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
     else
       orth_product_small_kernel<EPI, 4><<<grid(2), 256, 0, s>>>(p0, q, o, n, ra, rb, KS);
-  } else if (t128 <= (KS <= 64 ? kMidTilesShort : kMidTiles) ||
-           (KS <= 64 ? 19 : 17) * ((t256 + 255) / 256) > 10 * ((t128 + 511) / 512))
+  } else if ((KS <= 64 ? 19 : 17) * ((t256 + 255) / 256) > 10 * ((t128 + 511) / 512))
     orth_product_kernel<EPI, 2, 1, 2, 4><<<grid(4), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
   else
     orth_product_kernel<EPI, 2, 4, 4, 2><<<grid(8), 512, 0, s>>>(p0, q, o, n, ra, rb, KS);
