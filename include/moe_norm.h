@@ -3,7 +3,9 @@
  * gradient. The MoE layer of moe.h takes its hidden states as they are; in a
  * pre-norm block they are the layer norm of the block's input, and the block's
  * input gradient is the layer's, taken back through the norm, plus the
- * residual branch's.
+ * residual branch's. (LayerTrain has that block; moe_layer_forward adds the
+ * tensor it routes as the residual, which there is the norm's output. Norms
+ * without a mean are not covered.)
  *
  * Conventions as in moe.h: caller-owned DEVICE memory, work enqueued on
  * `stream`, host-side argument checks before any HIP call, moe_status codes.
@@ -26,7 +28,8 @@ extern "C" {
  * moe_layer_norm - for every row of D values
  *   mean = sum(x) / D,  rstd = 1 / sqrt(sum((x - mean)^2) / D + eps),
  *   y = (x - mean) rstd gamma + beta,
- * in fp32 (the variance from centred values), y rounded once to nearest even.
+ * in fp32 (the sum of x in fp64, the variance from centred values), y rounded
+ * once to nearest even.
  *
  *  rows   >= 0 (0: nothing is done)
  *  D      1 .. MOE_MAX_WIDTH

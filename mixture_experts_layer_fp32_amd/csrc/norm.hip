@@ -9,12 +9,17 @@
 // a thread, that hold it in registers, so x (and dy) are read once; gamma and
 // beta, and in the backward the column sums, stay in registers over all rows
 // of the group. Measured (a copy of 1 GiB moves 5.1 TB/s): forward 8192 x 4096
-// bf16 27 us, 4.9 TB/s; backward with the residual 16384 x 2048 bf16 56 us,
-// 4.8 TB/s, 4096 x 7168 fp32 93 us, 5.0 TB/s. What it took: the row's two sums
-// across the lanes in registers and one barrier a row (44 -> 34 us forward),
-// non-temporal stores (34 -> 32; backward 64 -> 57), the hardware's bf16
-// conversion (32 -> 27). Tried and slower: two rows in flight ahead,
-// non-temporal loads of bf16 rows, fewer or one row per workgroup.
+// bf16 25.4 us, 5.3 TB/s (part of x is still cached); backward with the residual
+// 16384 x 2048 bf16 62 us, 4.3 TB/s, 4096 x 7168 fp32 91 us, 5.1 TB/s. What it
+// took: the row's two sums across the lanes in registers and one barrier a row
+// (44 -> 34 us forward), non-temporal stores (34 -> 32; backward 64 -> 57), the
+// hardware's bf16 conversion (32 -> 27), the waves' means joined without a
+// division each (4096 x 7168 fp32 43 -> 38). Tried and slower: two rows in flight
+// ahead, non-temporal loads of bf16 rows, fewer or one row per workgroup. Rows
+// above 8192 values (16 waves, nothing read ahead) and above 16384 (x from the
+// caches a second and third time) are further off: 3000 x 10000 bf16 48 us, 2.5
+// TB/s, 2000 x 20000 bf16 50 us, 3.2, 1000 x 40000 fp32 87 us, 3.7; their
+// backward with the residual 104, 98 and 178 us.
 #include <algorithm>
 
 #include "moe_internal.h"

@@ -920,9 +920,12 @@ __global__ __launch_bounds__(1024) void orth_split_gram_kernel(
 //   workgroup is all of a matrix (512 x 64 x 64 80 -> 67 us; 60 x 128 x 512, 480
 //   workgroups, 133 -> 190: the steps are repeated in each).
 // SWAP: the result's rows are those of Q (kOut of a wide matrix).
-// MB = 4, one step, kLoop: 11.5 us, of it the launch 2.5, two Gram parts 1.0,
-// the step 2.7, X 5.3; kGram with eight parts 12.7 (and no launch of 5.3 for the
-// Gram product).
+// Where a launch's time goes (copies without each part in turn), MB = 4, kGram,
+// one step, eight Gram parts (8 x 128 x 512): 11.4 us, of it the launch 3.2,
+// copying X^T 0.2, the Gram parts 2.1, the step's product 2.8, Q X with its stores
+// 2.0, the next Gram part 1.2. Two steps, four parts (8 x 256 x 128): 18.7 us, of
+// it 3.2, 0.1, 0.9, the five products 12.0, 1.7 and 0.8. Each part is a chain of a
+// few dependent loads or products; none is bound by a rate.
 enum XGroups { kLoop = 0, kStaged = 1, kGram = 2 };
 template <int MB, int EPI, bool SWAP, int MODE>
 __global__ __launch_bounds__(1024) void orth_steps_kernel(Product p, Out o, int steps, int rk,
