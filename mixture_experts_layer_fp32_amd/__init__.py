@@ -2,7 +2,8 @@
 
 The computation runs in hand-written HIP kernels inside libmoe.so, reached
 through its C ABI (include/moe.h, include/moe_mxfp8.h, include/moe_backward.h,
-include/moe_variants.h, include/moe_norm.h, include/moe_update.h). This package
+include/moe_variants.h, include/moe_norm.h, include/moe_update.h,
+include/moe_fp8.h, include/moe_ckpt.h, include/moe_balance.h). This package
 is the thin Python binding
 (same function names as the C entry points) plus owners of device buffers.
 Importing it does not load the library; the first call does, and it raises
@@ -26,6 +27,12 @@ from ._binding import (  # noqa: F401
     moe_layer_norm, moe_layer_norm_backward, moe_layer_norm_backward_workspace_size,
     moe_orthogonalize, moe_orthogonalize_workspace_size, moe_muon_update, moe_matrices,
     moe_muon_desc,
+    moe_fp8_quantize_rows, moe_fp8_pack_weights, pack_expert_weights_fp8, moe_expert_gate_up_fp8,
+    moe_expert_down_fp8, moe_expert_ffn_fp8, moe_ffn_fp8_workspace_size,
+    moe_ckpt_save_rows, moe_ckpt_restore_rows, moe_expert_gate_up_train_ckpt,
+    moe_expert_ffn_train_ckpt, moe_expert_gate_up_backward_ckpt, moe_expert_ffn_backward_ckpt,
+    moe_balance_loss, moe_balance_loss_workspace_size, moe_balance_loss_backward,
+    moe_router_backward_dense, moe_router_backward_dense_workspace_size,
 )
 from .layer import (  # noqa: F401
     EPRankShareForward, ExpertMuon, LayerForward, LayerForwardMXFP8, LayerTrain,

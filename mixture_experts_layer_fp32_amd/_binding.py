@@ -1,6 +1,7 @@
 """ctypes binding of libmoe (include/moe.h, include/moe_mxfp8.h,
 include/moe_backward.h, include/moe_variants.h, include/moe_norm.h,
-include/moe_update.h): one Python function per C entry
+include/moe_update.h, include/moe_fp8.h, include/moe_ckpt.h,
+include/moe_balance.h): one Python function per C entry
 point, with the same name. Arguments are torch tensors (device memory) or
 None; the binding checks their device, dtype, shape and contiguity, passes
 their addresses and torch's current HIP stream, and raises MoeError on a
@@ -55,6 +56,16 @@ EXPORTS = (
     "moe_layer_norm", "moe_layer_norm_backward", "moe_layer_norm_backward_workspace_size",
     # optimiser step of the expert matrices
     "moe_orthogonalize", "moe_orthogonalize_workspace_size", "moe_muon_update",
+    # FP8 with block scales
+    "moe_fp8_quantize_rows", "moe_fp8_pack_weights", "moe_expert_gate_up_fp8",
+    "moe_expert_down_fp8", "moe_expert_ffn_fp8", "moe_ffn_fp8_workspace_size",
+    # activation checkpoints in 8 bits
+    "moe_ckpt_save_rows", "moe_ckpt_restore_rows", "moe_expert_gate_up_train_ckpt",
+    "moe_expert_ffn_train_ckpt", "moe_expert_gate_up_backward_ckpt",
+    "moe_expert_ffn_backward_ckpt",
+    # balance loss and the dense router backward
+    "moe_balance_loss", "moe_balance_loss_workspace_size", "moe_balance_loss_backward",
+    "moe_router_backward_dense", "moe_router_backward_dense_workspace_size",
 )
 
 
@@ -177,6 +188,38 @@ _SIGS = {
     "moe_muon_update": (ctypes.c_int32, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                                          ctypes.POINTER(moe_muon_desc), _M, _M, _M, _P,
                                          ctypes.c_size_t, _P]),
+    "moe_fp8_quantize_rows": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                               _P, _P, _P, _P]),
+    "moe_fp8_pack_weights": (ctypes.c_int32, [ctypes.c_int32] * 4 + [_P] * 4),
+    "moe_expert_gate_up_fp8": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32,
+                                                ctypes.c_int64] + [_P] * 7),
+    "moe_expert_down_fp8": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32,
+                                             ctypes.c_int64] + [_P] * 7),
+    "moe_expert_ffn_fp8": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32, ctypes.c_int64]
+                           + [_P] * 9 + [ctypes.c_size_t, _P]),
+    "moe_ffn_fp8_workspace_size": (ctypes.c_size_t, [_D, ctypes.c_int32, ctypes.c_int64]),
+    "moe_ckpt_save_rows": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
+                                            _P, _P, _P, _P]),
+    "moe_ckpt_restore_rows": (ctypes.c_int32, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                               ctypes.c_int32, _P, _P, _P, _P, _P]),
+    "moe_expert_gate_up_train_ckpt": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32,
+                                                       ctypes.c_int64] + [_P] * 7),
+    "moe_expert_ffn_train_ckpt": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32,
+                                                   ctypes.c_int64] + [_P] * 8
+                                  + [ctypes.c_size_t, _P]),
+    "moe_expert_gate_up_backward_ckpt": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32,
+                                                          ctypes.c_int64] + [_P] * 8),
+    "moe_expert_ffn_backward_ckpt": (ctypes.c_int32, [_D, ctypes.c_int32, ctypes.c_int32,
+                                                      ctypes.c_int64] + [_P] * 11
+                                     + [ctypes.c_size_t, _P]),
+    "moe_balance_loss": (ctypes.c_int32, [ctypes.c_int32] * 4 + [_P] * 3 + [ctypes.c_float]
+                         + [_P] * 5 + [ctypes.c_size_t, _P]),
+    "moe_balance_loss_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 2),
+    "moe_balance_loss_backward": (ctypes.c_int32, [ctypes.c_int32] * 4 + [_P] * 3
+                                  + [ctypes.c_float] + [_P] * 6),
+    "moe_router_backward_dense": (ctypes.c_int32, [ctypes.c_int32] * 4 + [_P] * 3
+                                  + [ctypes.c_int32] + [_P] * 3 + [ctypes.c_size_t, _P]),
+    "moe_router_backward_dense_workspace_size": (ctypes.c_size_t, [ctypes.c_int32] * 3),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -1007,3 +1050,309 @@ def moe_muon_update(g, momentum, w, ws, lr, mu=0.95, weight_decay=0.0, scale=1.0
     _launch("moe_muon_update", dev, (
         *_sizes(g), ctypes.byref(d), *(ctypes.byref(m) for m in mats),
         _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0), stream)
+
+
+# ---------------------------------------------------------------------------
+# FP8 with block scales (include/moe_fp8.h). Codes are uint8 tensors (the bits
+# of torch.float8_e4m3fn), scales fp32. Runs on the first tensor's device.
+# ---------------------------------------------------------------------------
+def _blocks(n: int) -> int:
+    """Blocks of 128 in n columns."""
+    return (n + 127) // 128
+
+
+def moe_fp8_quantize_rows(x, codes, scales, stream=None):
+    """x [rows, K] fp32 or bf16 -> codes [rows, K] uint8, scales
+    [ceil(K/128), rows] fp32."""
+    rows, K = shape = _rows(x, "x")
+    dev = _device_of(x, "x")
+    _launch("moe_fp8_quantize_rows", dev, (
+        rows, K, _act_code(x, "x"),
+        _ptr_on(dev, x, "x", x.dtype),
+        _ptr_on(dev, codes, "codes", torch.uint8, shape),
+        _ptr_on(dev, scales, "scales", torch.float32, (_blocks(K), rows)),
+    ), stream)
+
+
+def moe_fp8_pack_weights(w, codes, scales, stream=None):
+    """w [n, K, N] fp32 or bf16 -> codes [n, N, K] uint8, scales
+    [n, ceil(N/128), ceil(K/128)] fp32."""
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w: expected [n, K, N]")
+    n, K, N = w.shape
+    dev = _device_of(w, "w")
+    _launch("moe_fp8_pack_weights", dev, (
+        n, K, N, _act_code(w, "w"),
+        _ptr_on(dev, w, "w", w.dtype),
+        _ptr_on(dev, codes, "codes", torch.uint8, (n, N, K)),
+        _ptr_on(dev, scales, "scales", torch.float32, (n, _blocks(N), _blocks(K))),
+    ), stream)
+
+
+def pack_expert_weights_fp8(w):
+    """(codes, scales) of stacked expert weights [n, K, N] (new tensors)."""
+    n, K, N = w.shape
+    codes = torch.empty(n, N, K, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(n, _blocks(N), _blocks(K), device=w.device)
+    moe_fp8_pack_weights(w, codes, scales)
+    return codes, scales
+
+
+def _rows_of(dev, t, name, dtype, rows, width):
+    """The address of at least rows x width values."""
+    p = _ptr_on(dev, t, name, dtype)
+    if t is not None and t.numel() < rows * width:
+        raise ValueError(f"{name}: {t.numel()} elements, need at least {rows * width}")
+    return p
+
+
+def _fp8_operands(dev, n, rows, K, N, xq, xs, offsets, wq, ws):
+    """Addresses of a product's operands. The scales of the rows are spaced by
+    cap_rows: their shape has to be exact."""
+    u8, f32 = torch.uint8, torch.float32
+    return (_rows_of(dev, xq, "codes", u8, rows, K),
+            _ptr_on(dev, xs, "scales", f32, (_blocks(K), rows)),
+            _ptr_on(dev, offsets, "offsets", torch.int32, (n + 1,)),
+            _ptr_on(dev, wq, "weight codes", u8, (n, N, K)),
+            _ptr_on(dev, ws, "weight scales", f32, (n, _blocks(N), _blocks(K))))
+
+
+def moe_expert_gate_up_fp8(d: moe_desc, n_experts, inter, cap_rows, xq, xs, offsets, w_gu_q,
+                           w_gu_s, h, stream=None):
+    """h [cap_rows, inter] bf16."""
+    dev, n, rows = _device_of(xq, "codes"), int(n_experts), int(cap_rows)
+    _launch("moe_expert_gate_up_fp8", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        *_fp8_operands(dev, n, rows, d.D, 2 * inter, xq, xs, offsets, w_gu_q, w_gu_s),
+        _rows_of(dev, h, "h", torch.bfloat16, rows, inter),
+    ), stream)
+
+
+def moe_expert_down_fp8(d: moe_desc, n_experts, inter, cap_rows, hq, hs, offsets, w_d_q, w_d_s,
+                        y_perm, stream=None):
+    """y_perm [cap_rows, D] fp32, or fp16 (the descriptor's expert_out_dtype)."""
+    dev, n, rows = _device_of(hq, "codes"), int(n_experts), int(cap_rows)
+    _launch("moe_expert_down_fp8", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        *_fp8_operands(dev, n, rows, inter, d.D, hq, hs, offsets, w_d_q, w_d_s),
+        _rows_of(dev, y_perm, "y_perm", _y_dtype(d), rows, d.D),
+    ), stream)
+
+
+def moe_ffn_fp8_workspace_size(d: moe_desc, inter: int, cap_rows: int) -> int:
+    return int(load_library().moe_ffn_fp8_workspace_size(ctypes.byref(d), int(inter),
+                                                         int(cap_rows)))
+
+
+def moe_expert_ffn_fp8(d: moe_desc, n_experts, inter, cap_rows, xq, xs, offsets, w_gu_q, w_gu_s,
+                       w_d_q, w_d_s, y_perm, ws, stream=None):
+    dev, n, rows, D = _device_of(xq, "codes"), int(n_experts), int(cap_rows), d.D
+    u8, f32 = torch.uint8, torch.float32
+    _launch("moe_expert_ffn_fp8", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        *_fp8_operands(dev, n, rows, D, 2 * inter, xq, xs, offsets, w_gu_q, w_gu_s),
+        _ptr_on(dev, w_d_q, "w_d_q", u8, (n, D, inter)),
+        _ptr_on(dev, w_d_s, "w_d_s", f32, (n, _blocks(D), _blocks(inter))),
+        _rows_of(dev, y_perm, "y_perm", _y_dtype(d), rows, D),
+        _ptr_on(dev, ws, "ws", u8), ws.numel() if ws is not None else 0,
+    ), stream)
+
+
+# ---------------------------------------------------------------------------
+# Activation checkpoints in 8 bits (include/moe_ckpt.h): codes int8, scales
+# bf16.
+# ---------------------------------------------------------------------------
+def moe_ckpt_save_rows(x, codes, scales, stream=None):
+    """x [rows, D] fp32 or bf16 -> codes [rows, D] int8, scales [rows, D/32]
+    bf16."""
+    rows, D = shape = _rows(x, "x")
+    dev = _device_of(x, "x")
+    _launch("moe_ckpt_save_rows", dev, (
+        rows, D, _act_code(x, "x"),
+        _ptr_on(dev, x, "x", x.dtype),
+        _ptr_on(dev, codes, "codes", torch.int8, shape),
+        _ptr_on(dev, scales, "scales", torch.bfloat16, (rows, D // 32)),
+    ), stream)
+
+
+def moe_ckpt_restore_rows(codes, scales, out, index=None, stream=None):
+    """out [n, D] fp32 or bf16 <- row index[i] (int32; i without an index) of
+    codes [rows, D], scales [rows, D/32]."""
+    rows, D = shape = _rows(codes, "codes")
+    n, width = _rows(out, "out")
+    if width != D:
+        raise ValueError(f"out: rows of {width}, codes of {D}")
+    dev = _device_of(codes, "codes")
+    _launch("moe_ckpt_restore_rows", dev, (
+        n, rows, D, _act_code(out, "out"),
+        _ptr_on(dev, codes, "codes", torch.int8, shape),
+        _ptr_on(dev, scales, "scales", torch.bfloat16, (rows, D // 32)),
+        _ptr_on(dev, index, "index", torch.int32, (n,)),
+        _ptr_on(dev, out, "out", out.dtype),
+    ), stream)
+
+
+def _ckpt_operands(dev, rows, inter, codes, scales):
+    return (_rows_of(dev, codes, "gu_codes", torch.int8, rows, 2 * inter),
+            _rows_of(dev, scales, "gu_scales", torch.bfloat16, rows, 2 * inter // 32))
+
+
+def moe_expert_gate_up_train_ckpt(d: moe_desc, n_experts, inter, cap_rows, x_perm, offsets,
+                                  w_gate_up, h, gu_codes, gu_scales, stream=None):
+    """h [cap_rows, inter] fp16; gu_codes [cap_rows, 2 inter] int8, gu_scales
+    [cap_rows, 2 inter / 32] bf16."""
+    dev, n, rows, D = _device_of(x_perm, "x_perm"), int(n_experts), int(cap_rows), d.D
+    bf = torch.bfloat16
+    _launch("moe_expert_gate_up_train_ckpt", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        _rows_of(dev, x_perm, "x_perm", bf, rows, D),
+        _ptr_on(dev, offsets, "offsets", torch.int32, (n + 1,)),
+        _rows_of(dev, w_gate_up, "w_gate_up", bf, n * D, 2 * inter),
+        _rows_of(dev, h, "h", torch.float16, rows, inter),
+        *_ckpt_operands(dev, rows, inter, gu_codes, gu_scales),
+    ), stream)
+
+
+def moe_expert_ffn_train_ckpt(d: moe_desc, n_experts, inter, cap_rows, x_perm, offsets, w_gate_up,
+                              w_down, y_perm, gu_codes, gu_scales, ws, stream=None):
+    dev, n, rows, D = _device_of(x_perm, "x_perm"), int(n_experts), int(cap_rows), d.D
+    bf = torch.bfloat16
+    _launch("moe_expert_ffn_train_ckpt", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        _rows_of(dev, x_perm, "x_perm", bf, rows, D),
+        _ptr_on(dev, offsets, "offsets", torch.int32, (n + 1,)),
+        _rows_of(dev, w_gate_up, "w_gate_up", bf, n * D, 2 * inter),
+        _rows_of(dev, w_down, "w_down", bf, n * inter, D),
+        _rows_of(dev, y_perm, "y_perm", torch.float32, rows, D),
+        *_ckpt_operands(dev, rows, inter, gu_codes, gu_scales),
+        _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0,
+    ), stream)
+
+
+def moe_expert_gate_up_backward_ckpt(d: moe_desc, n_experts, inter, cap_rows, dy_perm, offsets,
+                                     w_down, gu_codes, gu_scales, dgu, h, stream=None):
+    """dgu [cap_rows, 2 inter], h [cap_rows, inter] bf16."""
+    dev, n, rows, D = _device_of(dy_perm, "dy_perm"), int(n_experts), int(cap_rows), d.D
+    bf = torch.bfloat16
+    _launch("moe_expert_gate_up_backward_ckpt", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        _rows_of(dev, dy_perm, "dy_perm", bf, rows, D),
+        _ptr_on(dev, offsets, "offsets", torch.int32, (n + 1,)),
+        _rows_of(dev, w_down, "w_down", bf, n * inter, D),
+        *_ckpt_operands(dev, rows, inter, gu_codes, gu_scales),
+        _rows_of(dev, dgu, "dgu", bf, rows, 2 * inter),
+        _rows_of(dev, h, "h", bf, rows, inter),
+    ), stream)
+
+
+def moe_expert_ffn_backward_ckpt(d: moe_desc, n_experts, inter, cap_rows, x_perm, offsets,
+                                 w_gate_up, w_down, dy_perm, gu_codes, gu_scales, dx_perm,
+                                 dw_gate_up, dw_down, ws, stream=None):
+    """moe_expert_ffn_backward from the kept codes (workspace of
+    moe_ffn_backward_workspace_size bytes)."""
+    dev, n, rows, D = _device_of(x_perm, "x_perm"), int(n_experts), int(cap_rows), d.D
+    bf, f32 = torch.bfloat16, torch.float32
+    _launch("moe_expert_ffn_backward_ckpt", dev, (
+        ctypes.byref(d), n, int(inter), rows,
+        _rows_of(dev, x_perm, "x_perm", bf, rows, D),
+        _ptr_on(dev, offsets, "offsets", torch.int32, (n + 1,)),
+        _ptr_on(dev, w_gate_up, "w_gate_up", bf, (n, D, 2 * inter)),
+        _ptr_on(dev, w_down, "w_down", bf, (n, inter, D)),
+        _rows_of(dev, dy_perm, "dy_perm", bf, rows, D),
+        *_ckpt_operands(dev, rows, inter, gu_codes, gu_scales),
+        _rows_of(dev, dx_perm, "dx_perm", f32, rows, D),
+        _ptr_on(dev, dw_gate_up, "dw_gate_up", f32, (n, D, 2 * inter)),
+        _ptr_on(dev, dw_down, "dw_down", f32, (n, inter, D)),
+        _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0,
+    ), stream)
+
+
+# ---------------------------------------------------------------------------
+# Balance loss and the dense router backward (include/moe_balance.h).
+# ---------------------------------------------------------------------------
+_LOGIT_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+
+
+def _logits(t):
+    """(tokens, experts, dtype code) of a logits tensor."""
+    T, E = _rows(t, "logits")
+    code = _LOGIT_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"logits: dtype {t.dtype}, expected float32, bfloat16 or float16")
+    return T, E, code
+
+
+def _mask(dev, mask, T):
+    if mask is not None and isinstance(mask, torch.Tensor) and mask.dtype is torch.bool:
+        mask = mask.view(torch.uint8)
+    return _ptr_on(dev, mask, "mask", torch.uint8, (T,))
+
+
+def moe_balance_loss_workspace_size(T: int, E: int) -> int:
+    return int(load_library().moe_balance_loss_workspace_size(int(T), int(E)))
+
+
+def moe_balance_loss(logits, topk_idx, coef, counts, tokens, prob_sum, loss, ws, mask=None,
+                     stream=None):
+    """logits [T, E] fp32, bf16 or fp16; topk_idx [T, k] int32; mask [T] uint8
+    or bool (0: the token does not count); counts [E] int32, tokens [1] int32,
+    prob_sum [E] fp32 and loss [1] fp32 are written."""
+    T, E, code = _logits(logits)
+    dev, f32, i32 = _device_of(logits, "logits"), torch.float32, torch.int32
+    k = _rows(topk_idx, "topk_idx")[1]
+    _launch("moe_balance_loss", dev, (
+        T, E, k, code,
+        _ptr_on(dev, logits, "logits", logits.dtype),
+        _ptr_on(dev, topk_idx, "topk_idx", i32, (T, k)),
+        _mask(dev, mask, T), float(coef),
+        _ptr_on(dev, counts, "counts", i32, (E,)),
+        _ptr_on(dev, tokens, "tokens", i32, (1,)),
+        _ptr_on(dev, prob_sum, "prob_sum", f32, (E,)),
+        _ptr_on(dev, loss, "loss", f32, (1,)),
+        _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0,
+    ), stream)
+
+
+def moe_balance_loss_backward(logits, topk_idx, coef, counts, tokens, dloss, dlogits, mask=None,
+                              dlogit=None, stream=None):
+    """dlogits [T, E] fp32 <- the gradient of dloss [1] (None: 1) times the
+    loss, plus dlogit [T, k] (None: nothing) at each token's experts topk_idx
+    [T, k]."""
+    T, E, code = _logits(logits)
+    dev, f32, i32 = _device_of(logits, "logits"), torch.float32, torch.int32
+    k = _rows(topk_idx, "topk_idx")[1]
+    _launch("moe_balance_loss_backward", dev, (
+        T, E, k, code,
+        _ptr_on(dev, logits, "logits", logits.dtype),
+        _ptr_on(dev, topk_idx, "topk_idx", i32, (T, k)),
+        _mask(dev, mask, T), float(coef),
+        _ptr_on(dev, counts, "counts", i32, (E,)),
+        _ptr_on(dev, tokens, "tokens", i32, (1,)),
+        _ptr_on(dev, dloss, "dloss", f32, (1,)),
+        _ptr_on(dev, dlogit, "dlogit", f32, (T, k)),
+        _ptr_on(dev, dlogits, "dlogits", f32, (T, E)),
+    ), stream)
+
+
+def moe_router_backward_dense_workspace_size(T: int, E: int, D: int) -> int:
+    return int(load_library().moe_router_backward_dense_workspace_size(int(T), int(E), int(D)))
+
+
+def moe_router_backward_dense(dlogits, x, w_router, dx, dw_router, ws, accumulate=False,
+                              stream=None):
+    """dlogits [T, E] fp32, x [T, D] fp32 or bf16, w_router [E, D] fp32 -> dx
+    [T, D] fp32 (added to it with accumulate; None: not wanted), dw_router
+    [E, D] fp32 (or None)."""
+    T, E = _rows(dlogits, "dlogits")
+    D = _rows(x, "x")[1]
+    dev, f32 = _device_of(dlogits, "dlogits"), torch.float32
+    _launch("moe_router_backward_dense", dev, (
+        T, E, D, _act_code(x, "x"),
+        _ptr_on(dev, dlogits, "dlogits", f32),
+        _ptr_on(dev, x, "x", x.dtype, (T, D)),
+        _ptr_on(dev, w_router, "w_router", f32, (E, D)),
+        int(bool(accumulate)),
+        _ptr_on(dev, dx, "dx", f32, (T, D)),
+        _ptr_on(dev, dw_router, "dw_router", f32, (E, D)),
+        _ptr_on(dev, ws, "ws", torch.uint8), ws.numel() if ws is not None else 0,
+    ), stream)

@@ -11,6 +11,9 @@
 
 #include "moe_internal.h"
 #include "moe_backward.h"
+#include "moe_balance.h"
+#include "moe_ckpt.h"
+#include "moe_fp8.h"
 #include "moe_mxfp8.h"
 #include "moe_norm.h"
 #include "moe_update.h"
@@ -1137,4 +1140,347 @@ MOE_API moe_status moe_muon_update(int32_t n, int32_t rows, int32_t cols,
   if ((st = check_orth_ws(n, rows, cols, ws, ws_bytes)) != MOE_OK) return st;
   return hip_status(moe::launch_orth(n, rows, cols, *g, momentum, *w, *desc, ws,
                                      static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// FP8 with block scales
+// ---------------------------------------------------------------------------
+namespace {
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Sizes of a quantizer whose values, codes and grid (at least 4096 values a
+// workgroup) stay within 64-bit offsets and 2^32 threads.
+moe_status check_rows(int64_t rows, int32_t D, int32_t multiple, int32_t most, int32_t dtype) {
+  if (rows < 0 || D <= 0 || D % multiple != 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (D > most || rows > INT_MAX || rows >= (int64_t(1) << 34) / D) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t fp8_scales_bytes(int64_t rows, int K) {
+  return align_up(static_cast<size_t>((K + 127) / 128) * rows * sizeof(float));
+}
+
+// H in bf16, its codes and its scales.
+size_t ffn_fp8_ws(int inter, int64_t cap_rows) {
+  const size_t hs = static_cast<size_t>(cap_rows) * inter;
+  return align_up(hs * 2) + align_up(hs) + fp8_scales_bytes(cap_rows, inter);
+}
+
+moe_status check_ffn_fp8(const moe_desc* desc, int32_t n_experts, int32_t inter,
+                         int64_t cap_rows, const int32_t* offsets) {
+  moe_status st = check_ffn_args(desc, n_experts, inter, cap_rows);
+  if (st != MOE_OK) return st;
+  if (offsets == nullptr && n_experts != 1) return MOE_ERR_INVALID_ARG;
+  return desc->act_dtype == MOE_BF16 ? MOE_OK : MOE_ERR_UNSUPPORTED;
+}
+}  // namespace
+
+MOE_API moe_status moe_fp8_quantize_rows(int64_t rows, int32_t K, int32_t dtype, const void* x,
+                                         void* codes, float* scales, void* stream) {
+  moe_status st = check_rows(rows, K, 64, MOE_MAX_WIDTH, dtype);
+  if (st != MOE_OK || rows == 0) return st;
+  if (x == nullptr || codes == nullptr || scales == nullptr || !aligned16(x) || !aligned16(codes))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_fp8_quantize_rows(dtype == MOE_BF16, rows, K, x, codes, scales,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_fp8_pack_weights(int32_t n, int32_t K, int32_t N, int32_t dtype,
+                                        const void* w, void* codes, float* scales, void* stream) {
+  if (n < 0 || K <= 0 || K % 64 != 0 || N <= 0 || N % 64 != 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (n > MOE_MAX_EXPERTS || K > 2 * MOE_MAX_WIDTH || N > 2 * MOE_MAX_WIDTH ||
+      static_cast<int64_t>(n) * ((K + 127) / 128) * ((N + 127) / 128) >= (int64_t(1) << 24))
+    return MOE_ERR_UNSUPPORTED;
+  if (n == 0) return MOE_OK;
+  if (w == nullptr || codes == nullptr || scales == nullptr || !aligned16(w) || !aligned16(codes))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_fp8_pack_weights(dtype == MOE_BF16, n, K, N, w, codes, scales,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+MOE_API size_t moe_ffn_fp8_workspace_size(const moe_desc* desc, int32_t inter, int64_t cap_rows) {
+  if (check_ffn_args(desc, 1, inter, cap_rows) != MOE_OK || desc->act_dtype != MOE_BF16) return 0;
+  return ffn_fp8_ws(inter, cap_rows);
+}
+
+MOE_API moe_status moe_expert_gate_up_fp8(const moe_desc* desc, int32_t n_experts, int32_t inter,
+                                          int64_t cap_rows, const void* xq, const float* xs,
+                                          const int32_t* offsets, const void* w_gu_q,
+                                          const float* w_gu_s, void* h, void* stream) {
+  moe_status st = check_ffn_fp8(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK || cap_rows == 0) return st;
+  if (xq == nullptr || xs == nullptr || w_gu_q == nullptr || w_gu_s == nullptr || h == nullptr ||
+      !aligned16(xq) || !aligned16(w_gu_q) || !aligned16(h))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_gate_up_fp8(n_experts, cap_rows, desc->D, inter, xq, xs, offsets,
+                                            w_gu_q, w_gu_s, h, static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_expert_down_fp8(const moe_desc* desc, int32_t n_experts, int32_t inter,
+                                       int64_t cap_rows, const void* hq, const float* hs,
+                                       const int32_t* offsets, const void* w_d_q,
+                                       const float* w_d_s, void* y_perm, void* stream) {
+  moe_status st = check_ffn_fp8(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK || cap_rows == 0) return st;
+  if (hq == nullptr || hs == nullptr || w_d_q == nullptr || w_d_s == nullptr ||
+      y_perm == nullptr || !aligned16(hq) || !aligned16(w_d_q) || !aligned16(y_perm))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_down_fp8(n_experts, cap_rows, desc->D, inter, hq, hs, offsets,
+                                         w_d_q, w_d_s, y_perm, y_half(*desc),
+                                         static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_expert_ffn_fp8(const moe_desc* desc, int32_t n_experts, int32_t inter,
+                                      int64_t cap_rows, const void* xq, const float* xs,
+                                      const int32_t* offsets, const void* w_gu_q,
+                                      const float* w_gu_s, const void* w_d_q, const float* w_d_s,
+                                      void* y_perm, void* ws, size_t ws_bytes, void* stream) {
+  moe_status st = check_ffn_fp8(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK || cap_rows == 0) return st;
+  if (check_rows(cap_rows, inter, 64, MOE_MAX_WIDTH, MOE_BF16) != MOE_OK)
+    return MOE_ERR_UNSUPPORTED;
+  if (xq == nullptr || xs == nullptr || w_gu_q == nullptr || w_gu_s == nullptr ||
+      w_d_q == nullptr || w_d_s == nullptr || y_perm == nullptr || ws == nullptr ||
+      !aligned16(xq) || !aligned16(w_gu_q) || !aligned16(w_d_q) || !aligned16(y_perm) ||
+      !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < ffn_fp8_ws(inter, cap_rows)) return MOE_ERR_WORKSPACE;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t hs = static_cast<size_t>(cap_rows) * inter;
+  char* h = static_cast<char*>(ws);
+  char* hq = h + align_up(hs * 2);
+  float* hsc = reinterpret_cast<float*>(hq + align_up(hs));
+  hipError_t e = moe::launch_gate_up_fp8(n_experts, cap_rows, desc->D, inter, xq, xs, offsets,
+                                         w_gu_q, w_gu_s, h, s);
+  if (e == hipSuccess) e = moe::launch_fp8_quantize_rows(true, cap_rows, inter, h, hq, hsc, s);
+  if (e == hipSuccess)
+    e = moe::launch_down_fp8(n_experts, cap_rows, desc->D, inter, hq, hsc, offsets, w_d_q, w_d_s,
+                             y_perm, y_half(*desc), s);
+  return hip_status(e);
+}
+
+// ---------------------------------------------------------------------------
+// Activation checkpoints in 8 bits
+// ---------------------------------------------------------------------------
+MOE_API moe_status moe_ckpt_save_rows(int64_t rows, int32_t D, int32_t dtype, const void* x,
+                                      void* codes, void* scales, void* stream) {
+  moe_status st = check_rows(rows, D, 32, 2 * MOE_MAX_WIDTH, dtype);
+  if (st != MOE_OK || rows == 0) return st;
+  if (x == nullptr || codes == nullptr || scales == nullptr || !aligned16(x) || !aligned16(codes))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_ckpt_save(dtype == MOE_BF16, rows, D, x, codes, scales,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_ckpt_restore_rows(int64_t n, int64_t rows, int32_t D, int32_t dtype,
+                                         const void* codes, const void* scales,
+                                         const int32_t* index, void* out, void* stream) {
+  moe_status st = check_rows(n, D, 32, 2 * MOE_MAX_WIDTH, dtype);
+  if (st == MOE_OK) st = check_rows(rows, D, 32, 2 * MOE_MAX_WIDTH, dtype);
+  if (st != MOE_OK) return st;
+  if (index == nullptr && n > rows) return MOE_ERR_INVALID_ARG;
+  if (n == 0 || rows == 0) return MOE_OK;  // no row has an index in [0, 0)
+  if (codes == nullptr || scales == nullptr || out == nullptr || !aligned16(codes) ||
+      !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_ckpt_restore(dtype == MOE_BF16, n, rows, D, codes, scales, index,
+                                             out, static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+// The training forward's checks (as moe_expert_ffn_train) and the backward's.
+moe_status check_train_ckpt(const moe_desc* desc, int32_t n_experts, int32_t inter,
+                            int64_t cap_rows, const int32_t* offsets) {
+  moe_status st = check_ffn_args(desc, n_experts, inter, cap_rows);
+  if (st != MOE_OK) return st;
+  if (!is_bf16(*desc) || packed(*desc) || y_half(*desc)) return MOE_ERR_UNSUPPORTED;
+  return offsets == nullptr && n_experts != 1 ? MOE_ERR_INVALID_ARG : MOE_OK;
+}
+moe_status check_bwd_ckpt(const moe_desc* desc, int32_t n_experts, int32_t inter,
+                          int64_t cap_rows, const int32_t* offsets) {
+  moe_status st = check_ffn_bwd(desc, n_experts, inter, cap_rows);
+  return st == MOE_OK ? check_train_ckpt(desc, n_experts, inter, cap_rows, offsets) : st;
+}
+inline bool ckpt_ok(const void* codes, const void* scales) {
+  return codes != nullptr && scales != nullptr && aligned16(codes);
+}
+}  // namespace
+
+MOE_API moe_status moe_expert_gate_up_train_ckpt(const moe_desc* desc, int32_t n_experts,
+                                                 int32_t inter, int64_t cap_rows,
+                                                 const void* x_perm, const int32_t* offsets,
+                                                 const void* w_gate_up, void* h, void* gu_codes,
+                                                 void* gu_scales, void* stream) {
+  moe_status st = check_train_ckpt(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK || cap_rows == 0) return st;
+  if (x_perm == nullptr || w_gate_up == nullptr || h == nullptr || !ckpt_ok(gu_codes, gu_scales))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_gate_up_ckpt_bf16(n_experts, cap_rows, desc->D, inter, x_perm,
+                                                  offsets, w_gate_up, h, gu_codes, gu_scales,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_expert_ffn_train_ckpt(const moe_desc* desc, int32_t n_experts,
+                                             int32_t inter, int64_t cap_rows, const void* x_perm,
+                                             const int32_t* offsets, const void* w_gate_up,
+                                             const void* w_down, void* y_perm, void* gu_codes,
+                                             void* gu_scales, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  moe_status st = check_train_ckpt(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK || cap_rows == 0) return st;
+  if (x_perm == nullptr || w_gate_up == nullptr || w_down == nullptr || y_perm == nullptr ||
+      ws == nullptr || !ckpt_ok(gu_codes, gu_scales))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < ffn_ws(*desc, inter, cap_rows)) return MOE_ERR_WORKSPACE;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = moe::launch_gate_up_ckpt_bf16(n_experts, cap_rows, desc->D, inter, x_perm,
+                                               offsets, w_gate_up, ws, gu_codes, gu_scales, s);
+  if (e == hipSuccess)
+    e = run_down(*desc, n_experts, cap_rows, inter, ws, offsets, w_down, y_perm, s,
+                 static_cast<char*>(ws) + ffn_h_bytes(*desc, inter, cap_rows),
+                 tail_bytes(*desc, cap_rows));
+  return hip_status(e);
+}
+
+MOE_API moe_status moe_expert_gate_up_backward_ckpt(const moe_desc* desc, int32_t n_experts,
+                                                    int32_t inter, int64_t cap_rows,
+                                                    const void* dy_perm, const int32_t* offsets,
+                                                    const void* w_down, const void* gu_codes,
+                                                    const void* gu_scales, void* dgu, void* h,
+                                                    void* stream) {
+  moe_status st = check_bwd_ckpt(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK || cap_rows == 0) return st;
+  if (dy_perm == nullptr || w_down == nullptr || dgu == nullptr || h == nullptr ||
+      !ckpt_ok(gu_codes, gu_scales))
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_dh_swiglu_ckpt(n_experts, cap_rows, desc->D, inter, dy_perm,
+                                               offsets, w_down, gu_codes, gu_scales, dgu, h,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_expert_ffn_backward_ckpt(const moe_desc* desc, int32_t n_experts,
+                                                int32_t inter, int64_t cap_rows,
+                                                const void* x_perm, const int32_t* offsets,
+                                                const void* w_gate_up, const void* w_down,
+                                                const void* dy_perm, const void* gu_codes,
+                                                const void* gu_scales, float* dx_perm,
+                                                float* dw_gate_up, float* dw_down, void* ws,
+                                                size_t ws_bytes, void* stream) {
+  moe_status st = check_bwd_ckpt(desc, n_experts, inter, cap_rows, offsets);
+  if (st != MOE_OK) return st;
+  if (w_gate_up == nullptr || w_down == nullptr || dw_gate_up == nullptr || dw_down == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (cap_rows > 0 && (x_perm == nullptr || dy_perm == nullptr || ws == nullptr ||
+                       !ckpt_ok(gu_codes, gu_scales)))
+    return MOE_ERR_INVALID_ARG;
+  if (cap_rows > 0 && ws_bytes < ffn_bwd_ws(*desc, inter, cap_rows)) return MOE_ERR_WORKSPACE;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t r = static_cast<size_t>(cap_rows);
+  char* dgu = static_cast<char*>(ws);
+  char* h = dgu + align_up(r * 2 * inter * 2);
+  hipError_t e = moe::launch_dh_swiglu_ckpt(n_experts, cap_rows, desc->D, inter, dy_perm, offsets,
+                                            w_down, gu_codes, gu_scales, dgu, h, s);
+  if (e == hipSuccess && dx_perm != nullptr)
+    e = moe::launch_dx_perm_bwd(n_experts, cap_rows, desc->D, inter, dgu, offsets, w_gate_up,
+                                dx_perm, s);
+  if (e == hipSuccess)
+    e = moe::launch_wgrad_bf16(n_experts, cap_rows, h, inter, dy_perm, desc->D, offsets, dw_down,
+                               s);
+  if (e == hipSuccess)
+    e = moe::launch_wgrad_bf16(n_experts, cap_rows, x_perm, desc->D, dgu, 2 * inter, offsets,
+                               dw_gate_up, s);
+  return hip_status(e);
+}
+
+// ---------------------------------------------------------------------------
+// Balance loss and the dense router backward
+// ---------------------------------------------------------------------------
+namespace {
+moe_status check_balance(int32_t T, int32_t E, int32_t k, int32_t dtype, float coef) {
+  if (T < 0 || E < 1 || k < 1 || k > E || !isfinite(coef)) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16 && dtype != MOE_F16) return MOE_ERR_UNSUPPORTED;
+  if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status check_router_dense(int32_t T, int32_t E, int32_t D, int32_t dtype) {
+  if (T < 0 || E < 1 || D <= 0 || D % 64 != 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (E > MOE_MAX_EXPERTS || D > MOE_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
+  // fewer than 2^24 workgroups a launch
+  if ((static_cast<int64_t>(T) + 63) / 64 * (D / 64) >= (int64_t(1) << 24))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+}  // namespace
+
+MOE_API size_t moe_balance_loss_workspace_size(int32_t T, int32_t E) {
+  if (check_balance(T, E, 1, MOE_F32, 0.f) != MOE_OK) return 0;
+  return moe::balance_ws_bytes(T, E);
+}
+
+MOE_API moe_status moe_balance_loss(int32_t T, int32_t E, int32_t k, int32_t dtype,
+                                    const void* logits, const int32_t* topk_idx,
+                                    const uint8_t* mask, float coef, int32_t* counts,
+                                    int32_t* tokens, float* prob_sum, float* loss, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  moe_status st = check_balance(T, E, k, dtype, coef);
+  if (st != MOE_OK) return st;
+  if (counts == nullptr || tokens == nullptr || prob_sum == nullptr || loss == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (logits == nullptr || topk_idx == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe::balance_ws_bytes(T, E)) return MOE_ERR_WORKSPACE;
+  }
+  return hip_status(moe::launch_balance_loss(dtype, T, E, k, logits, topk_idx, mask, coef, counts,
+                                             tokens, prob_sum, loss, ws,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+MOE_API moe_status moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t dtype,
+                                             const void* logits, const int32_t* topk_idx,
+                                             const uint8_t* mask, float coef,
+                                             const int32_t* counts, const int32_t* tokens,
+                                             const float* dloss, const float* dlogit,
+                                             float* dlogits, void* stream) {
+  moe_status st = check_balance(T, E, k, dtype, coef);
+  if (st != MOE_OK) return st;
+  if (T == 0) return MOE_OK;
+  if (dlogit != nullptr && topk_idx == nullptr) return MOE_ERR_INVALID_ARG;
+  if (logits == nullptr || counts == nullptr || tokens == nullptr || dlogits == nullptr)
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(moe::launch_balance_bwd(dtype, T, E, k, logits, topk_idx, mask, coef, counts,
+                                            tokens, dloss, dlogit, dlogits,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+MOE_API size_t moe_router_backward_dense_workspace_size(int32_t T, int32_t E, int32_t D) {
+  if (check_router_dense(T, E, D, MOE_F32) != MOE_OK) return 0;
+  return moe::router_dense_ws_floats(T, E, D) * sizeof(float);
+}
+
+MOE_API moe_status moe_router_backward_dense(int32_t T, int32_t E, int32_t D, int32_t dtype,
+                                             const float* dlogits, const void* x,
+                                             const float* w_router, int32_t accumulate, float* dx,
+                                             float* dw_router, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  moe_status st = check_router_dense(T, E, D, dtype);
+  if (st != MOE_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (dlogits == nullptr || (dx != nullptr && w_router == nullptr) ||
+                (dw_router != nullptr && x == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(dx) || !aligned16(dw_router) ||
+      !aligned16(ws))
+    return MOE_ERR_INVALID_ARG;
+  if (dw_router != nullptr) {
+    const size_t need = moe::router_dense_ws_floats(T, E, D) * sizeof(float);
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  }
+  return hip_status(moe::launch_router_dense_bwd(dtype == MOE_BF16, T, E, D, dlogits, x, w_router,
+                                                 accumulate, dx, dw_router,
+                                                 static_cast<float*>(ws),
+                                                 static_cast<hipStream_t>(stream)));
 }

@@ -67,6 +67,7 @@
 #include <cmath>
 #include <type_traits>
 
+#include "ckpt.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -154,8 +155,9 @@ constexpr int vmcnt_lgkm0_imm(int n) { return (n & 15) | (7 << 4) | ((n >> 4) <<
 // epilogue, writes dG | dU = dH U SiLU'(G) | dH SiLU(G) ([rows, 2 N_out],
 // bf16) and H = SiLU(G) U ([rows, N_out], bf16).
 // GEMM 1 of a training forward: as kGateUp, and the pre-activations G | U
-// are also stored in fp32 ([rows, 2 N_out], gu_out) for the backward.
-enum Mode { kGateUp = 0, kDown = 1, kGateUpBwd = 2, kGateUpSave = 3 };
+// are also stored in fp32 ([rows, 2 N_out], gu_out) for the backward; or in 8
+// bits, codes [rows, 2 N_out] in gu_out and scales [rows, 2 N_out / 32] in h_out.
+enum Mode { kGateUp = 0, kDown = 1, kGateUpBwd = 2, kGateUpSave = 3, kGateUpCkpt = 4 };
 
 // One 32x32x16 product added into c (activation fragment xa, weight fragment
 // wb). Gated GEMMs give the weight fragment as the MFMA's first operand, so
@@ -844,12 +846,51 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_bf16(
           out_rsrc(MODE == kGateUpBwd ? static_cast<void*>(h_out) : Cout, N_out * 2);
       const __amdgpu_buffer_rsrc_t gu_rsrc =
           out_rsrc(MODE == kGateUpSave ? static_cast<void*>(gu_out) : Cout, N_out * 8);
+      const __amdgpu_buffer_rsrc_t gq_rsrc =
+          out_rsrc(MODE == kGateUpCkpt ? static_cast<void*>(gu_out) : Cout, N_out * 2);
+      const __amdgpu_buffer_rsrc_t gs_rsrc =
+          out_rsrc(MODE == kGateUpCkpt ? static_cast<void*>(h_out) : Cout, N_out / 8);
     #pragma unroll
       for (int mb = 0; mb < NMB; ++mb) {
         if (MODE == kGateUpBwd && mb + 1 < NMB) load_dh(mb + 1, dpre[(mb + 1) & 1]);
         const int r = rowbase + mb * 32 + (lane & 31);  // row within the tile
     #pragma unroll
         for (int q = 0; q < NQ / 2; ++q) {
+          if constexpr (MODE == kGateUpCkpt) {
+            // The 32 columns of a checkpoint block are this lane's 16 and
+            // those of lane l ^ 32. Lanes 0..31 then store columns 0..15 of
+            // the block, lanes 32..63 columns 16..31.
+            const int col = n0 + wn * (WNW / 2) + q * 32;
+            const bool ok = col < N_out;
+    #pragma unroll
+            for (int part_gu = 0; part_gu < 2; ++part_gu) {
+              __builtin_amdgcn_sched_barrier(0);
+              const auto& a = acc[mb][q + part_gu * (NQ / 2)];
+              uint32_t amax = 0;
+    #pragma unroll
+              for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(a[i]) & 0x7fffffffu);
+              const auto both = __builtin_amdgcn_permlane32_swap(amax, amax, false, false);
+              const uint32_t sb = ckpt_scale_bits(max(static_cast<uint32_t>(both[0]),
+                                                      static_cast<uint32_t>(both[1])));
+              const float rs = 1.0f / __uint_as_float(sb << 16);
+              uint32_t w[4];
+    #pragma unroll
+              for (int g = 0; g < 4; ++g)
+                w[g] = ckpt_codes4(a[4 * g], a[4 * g + 1], a[4 * g + 2], a[4 * g + 3], rs);
+              const auto lo = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+              const auto hi = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+              const int o = ok ? r * 2 * N_out + part_gu * N_out + col + 16 * half : kOutOfRange;
+              const int os =
+                  ok && half == 0 ? (r * (N_out / 16) + part_gu * (N_out / 32) + col / 32) * 2
+                                  : kOutOfRange;
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  u32x4{static_cast<unsigned>(lo[0]), static_cast<unsigned>(lo[1]),
+                        static_cast<unsigned>(hi[0]), static_cast<unsigned>(hi[1])},
+                  gq_rsrc, o, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b16(static_cast<unsigned short>(sb), gs_rsrc, os,
+                                                    0, 0);
+            }
+          }
     #pragma unroll
           for (int g = 0; g < 4; ++g) {
             // (one group of 4 columns at a time: left to itself the scheduler
@@ -1281,6 +1322,15 @@ hipError_t launch_gate_up_save_bf16(int n_experts, int64_t cap_rows, int D, int 
   if (cap_rows == 0) return hipSuccess;
   return launch_ffn<kGateUpSave>(n_experts, cap_rows, D, inter, x_perm, offsets, w_gate_up, h, s,
                                  nullptr, nullptr, nullptr, gu);
+}
+
+hipError_t launch_gate_up_ckpt_bf16(int n_experts, int64_t cap_rows, int D, int inter,
+                                    const void* x_perm, const int32_t* offsets,
+                                    const void* w_gate_up, void* h, void* codes, void* scales,
+                                    hipStream_t s) {
+  if (cap_rows == 0) return hipSuccess;
+  return launch_ffn<kGateUpCkpt>(n_experts, cap_rows, D, inter, x_perm, offsets, w_gate_up, h, s,
+                                 nullptr, scales, nullptr, static_cast<float*>(codes));
 }
 
 hipError_t launch_gate_up_bwd_bf16(int n_experts, int64_t cap_rows, int D, int inter,

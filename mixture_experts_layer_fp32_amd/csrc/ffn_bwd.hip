@@ -34,6 +34,7 @@
 // an expert without rows gets a zero gradient.
 #include <algorithm>
 
+#include "ckpt.h"
 #include "moe_internal.h"
 
 namespace moe {
@@ -111,18 +112,21 @@ __device__ __forceinline__ int a_off(int row, int chunk) {
   return row * 128 + ((chunk ^ a_swz(row)) << 4);
 }
 
-enum NtEpilogue { kStoreF32 = 0, kSwigluSaved = 1 };
+enum NtEpilogue { kStoreF32 = 0, kSwigluSaved = 1, kSwigluCkpt = 2 };
 
 // kStoreF32: C [cap, N_out] fp32: row r of expert e's segment times W_e^T.
 // kSwigluSaved: C = dH [rows, N_out = I]; gu holds the forward's G | U
 //   [cap, 2 I] (fp32); writes dgu = dG | dU [cap, 2 I] and h [cap, I]
 //   (bf16). The G | U values of a 32-row block are loaded while the previous
 //   block is computed (those of the first block before the K loop).
+// kSwigluCkpt: the same with G | U in 8 bits: codes [cap, 2 I] in gu, scales
+//   [cap, 2 I / 32] (bf16) in gu_scales.
 template <int EPI>
 __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
     const uint16_t* __restrict__ A, const int32_t* __restrict__ offsets, int n_experts,
     int64_t cap_rows, const uint16_t* __restrict__ W, int K, int N_out, float* __restrict__ cf,
-    const float* __restrict__ gu, uint16_t* __restrict__ dgu, uint16_t* __restrict__ hout) {
+    const float* __restrict__ gu, uint16_t* __restrict__ dgu, uint16_t* __restrict__ hout,
+    const uint16_t* __restrict__ gu_scales) {
   using namespace nt;
   constexpr int kLds = 2 * kTileA + NSB * kTileB;
   static_assert(kLds + 2 * (kMaxTableExperts + 1) * 4 <= 160 * 1024, "LDS budget");
@@ -335,6 +339,30 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
       }
     };
     if (EPI == kSwigluSaved && nmb > 0) load_gu(0, gpre[0], upre[0]);
+    // kSwigluCkpt: the same block's codes (four columns a word) and scales
+    // (G's in the low half).
+    constexpr int NQC = EPI == kSwigluCkpt ? NQ : 1;
+    uint32_t gq[2][NQC][4], uq[2][NQC][4], sq[2][NQC][4];
+    auto load_ckpt = [&](int mb, uint32_t(&g8)[NQC][4], uint32_t(&u8)[NQC][4],
+                         uint32_t(&s2)[NQC][4]) {
+      const uint8_t* codes = reinterpret_cast<const uint8_t*>(gu);
+#pragma unroll
+      for (int q = 0; q < NQC; ++q) {
+        const int col = n0 + wn * WN + q * 32 + (lane & 28);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int row = row_begin + rowbase + mb * 32 + 8 * g + 4 * half + (lane & 3);
+          const bool ok = row < row_begin + rows && col < N_out;
+          const int64_t gi = static_cast<int64_t>(row) * 2 * N_out + col;
+          g8[q][g] = ok ? *reinterpret_cast<const uint32_t*>(codes + gi) : 0u;
+          u8[q][g] = ok ? *reinterpret_cast<const uint32_t*>(codes + gi + N_out) : 0u;
+          s2[q][g] = ok ? gu_scales[gi >> 5] |
+                              (static_cast<uint32_t>(gu_scales[(gi + N_out) >> 5]) << 16)
+                        : 0u;
+        }
+      }
+    };
+    if (EPI == kSwigluCkpt && nmb > 0) load_ckpt(0, gq[0], uq[0], sq[0]);
     static_assert(NA + NB <= 4 * kMaxMB, "copy items fit the MFMA groups");
     switch (nmb) {
       case 5: run(std::integral_constant<int, 5>{}); break;
@@ -352,6 +380,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
         if (mb >= nmb) break;
         if (EPI == kSwigluSaved && mb + 1 < nmb)
           load_gu(mb + 1, gpre[(mb + 1) & 1], upre[(mb + 1) & 1]);
+        if (EPI == kSwigluCkpt && mb + 1 < nmb)
+          load_ckpt(mb + 1, gq[(mb + 1) & 1], uq[(mb + 1) & 1], sq[(mb + 1) & 1]);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           const int col = n0 + wn * WN + q * 32 + (lane & 28);
@@ -369,9 +399,17 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
               continue;
             }
             // SiLU(g) = g s, s = 1 / (1 + exp(-g)); SiLU'(g) = s + SiLU(g) (1 - s).
-            const float4 g4 = gpre[mb & 1][q < NQE ? q : 0][g];
-            const float4 u4 = upre[mb & 1][q < NQE ? q : 0][g];
-            const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
+            float gs[4], us[4];
+            if (EPI == kSwigluCkpt) {
+              const uint32_t sc = sq[mb & 1][q < NQC ? q : 0][g];
+              ckpt_values4(gq[mb & 1][q < NQC ? q : 0][g], __uint_as_float(sc << 16), gs);
+              ckpt_values4(uq[mb & 1][q < NQC ? q : 0][g], __uint_as_float(sc & 0xffff0000u), us);
+            } else {
+              const float4 g4 = gpre[mb & 1][q < NQE ? q : 0][g];
+              const float4 u4 = upre[mb & 1][q < NQE ? q : 0][g];
+              gs[0] = g4.x, gs[1] = g4.y, gs[2] = g4.z, gs[3] = g4.w;
+              us[0] = u4.x, us[1] = u4.y, us[2] = u4.z, us[3] = u4.w;
+            }
             float dg[4], du[4], hv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -621,7 +659,8 @@ int num_cus_bwd() {
 template <int EPI>
 hipError_t launch_nt(int n_experts, int64_t cap_rows, int K, int n_out, const void* a,
                      const int32_t* offsets, const void* w, float* cf, hipStream_t s,
-                     const float* gu = nullptr, void* dgu = nullptr, void* h = nullptr) {
+                     const float* gu = nullptr, void* dgu = nullptr, void* h = nullptr,
+                     const void* gu_scales = nullptr) {
   using namespace nt;
   const int64_t mtiles = (cap_rows + BM - 1) / BM + (offsets ? n_experts : 0);
   const int64_t tiles = mtiles * ((n_out + BN - 1) / BN);
@@ -630,7 +669,7 @@ hipError_t launch_nt(int n_experts, int64_t cap_rows, int K, int n_out, const vo
   gemm_nt_bf16<EPI><<<static_cast<unsigned>(g), kThreads, 0, s>>>(
       static_cast<const uint16_t*>(a), offsets, n_experts, cap_rows,
       static_cast<const uint16_t*>(w), K, n_out, cf, gu, static_cast<uint16_t*>(dgu),
-      static_cast<uint16_t*>(h));
+      static_cast<uint16_t*>(h), static_cast<const uint16_t*>(gu_scales));
   return hipGetLastError();
 }
 
@@ -640,6 +679,15 @@ hipError_t launch_dh_bwd(int n_experts, int64_t cap_rows, int D, int inter, cons
                          const int32_t* offsets, const void* w_down, float* dh, hipStream_t s) {
   if (cap_rows == 0) return hipSuccess;
   return launch_nt<kStoreF32>(n_experts, cap_rows, D, inter, dy_perm, offsets, w_down, dh, s);
+}
+
+hipError_t launch_dh_swiglu_ckpt(int n_experts, int64_t cap_rows, int D, int inter,
+                                 const void* dy_perm, const int32_t* offsets, const void* w_down,
+                                 const void* codes, const void* scales, void* dgu, void* h,
+                                 hipStream_t s) {
+  if (cap_rows == 0) return hipSuccess;
+  return launch_nt<kSwigluCkpt>(n_experts, cap_rows, D, inter, dy_perm, offsets, w_down, nullptr,
+                                s, static_cast<const float*>(codes), dgu, h, scales);
 }
 
 hipError_t launch_dh_swiglu_saved(int n_experts, int64_t cap_rows, int D, int inter,

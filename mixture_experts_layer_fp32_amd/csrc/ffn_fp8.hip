@@ -1,0 +1,414 @@
+// Grouped expert products in FP8 with block scales (formats in moe_fp8.h), on
+// gfx950's 16x16x128 FP8 matrix instruction.
+//
+//   y[r, c] = sum_b xs[b, r] ws[c / 128, b] sum_{k in block b} xq[r, k] wq[c, k]
+// and, gated, h = SiLU(y_gate) y_up.
+//
+// One matrix instruction sums exactly one block of 128: it starts from zero,
+// and its 16 x 16 sums are added to the fp32 accumulators with one FMA each,
+// scaled by xs ws. The weights are the instruction's first operand: a lane
+// then holds four output columns of one row, so xs is one value per lane and
+// row block, ws one scalar per 64 columns, and a scale costs no more than its
+// FMA. The FMAs (4 per instruction, 16 cycles of vector issue) run beside the
+// matrix core's 32 cycles: a wave issues an instruction's FMAs two
+// instructions later, and two waves share a SIMD.
+#include <algorithm>
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
+
+constexpr int kXcds = 8;
+constexpr int kMaxTableExperts = MOE_MAX_EXPERTS;
+constexpr int kOutOfRange = 0x40000000;  // a load offset past every buffer (all < 2^30)
+
+enum OutKind { kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2 };
+
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 16 (4) bytes a lane global -> LDS at lds_base + 16 (4) * lane; offsets past
+// the resource write zeros. Counted by vmcnt.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
+                                      unsigned lds_base) {
+  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds_base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
+                                     unsigned lds_base) {
+  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds_base) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+__device__ __forceinline__ uint32_t f16_sat_bits(float f) {
+  const float c = f > 65504.f ? 65504.f : (f < -65504.f ? -65504.f : f);
+  return __builtin_bit_cast(unsigned short, static_cast<_Float16>(c));
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g * u * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+}
+
+__device__ __forceinline__ f32x4 mma(const i32x8& w, const i32x8& x) {
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// LDS rows hold 128 codes; 16-byte chunk c of a row sits at c ^ swz(i), i the
+// row's place in its 16-row fragment: the eight rows of every group of lanes
+// that a 16-byte read serves together then cover all banks.
+__device__ __forceinline__ int swz(int i) { return (i & 7) ^ ((i >> 3) & 1); }
+// Fragment b (0 .. 3) of a 64-column group takes its columns
+// 16 (i / 4) + 4 b + i % 4: lane group g of the four results then holds the
+// 16 adjacent columns 16 g .. 16 g + 15, which it stores at once.
+__device__ __forceinline__ int w_place(int j) { return (j & 3) | ((j >> 2) & 12); }
+
+// Sixteen adjacent outputs of a row.
+template <int KIND>
+__device__ __forceinline__ void store16(void* out, int64_t o, const float (&v)[16]) {
+  if (KIND == kOutF32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  } else {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = KIND == kOutF16
+                 ? f16_sat_bits(v[2 * i]) | (f16_sat_bits(v[2 * i + 1]) << 16)
+                 : f32_to_bf16(v[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16);
+    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o);
+    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Tiles before each expert (s_pref) and first rows (s_off, clamped to
+// cap_rows), by wave 0.
+__device__ __forceinline__ void tile_table(const int32_t* __restrict__ offsets, int n_exp,
+                                           int64_t cap_rows, int bm, int nt, int lane,
+                                           int* s_pref, int* s_off) {
+  int base = 0;
+  for (int e0 = 0; e0 < n_exp; e0 += 64) {
+    const int e = e0 + lane;
+    int beg = 0, end = 0;
+    if (e < n_exp) {
+      if (offsets) {
+        beg = offsets[e];
+        end = offsets[e + 1];
+      } else {
+        end = static_cast<int>(cap_rows);
+      }
+      beg = static_cast<int>(min(max(static_cast<int64_t>(beg), int64_t(0)), cap_rows));
+      end = static_cast<int>(
+          min(max(static_cast<int64_t>(end), static_cast<int64_t>(beg)), cap_rows));
+    }
+    const int tiles = (end - beg + bm - 1) / bm * nt;
+    int incl = tiles;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int y = __shfl_up(incl, off, 64);
+      if (lane >= off) incl += y;
+    }
+    if (e < n_exp) {
+      s_pref[e] = base + incl - tiles;
+      s_off[e] = beg;
+      if (e == n_exp - 1) {
+        s_pref[n_exp] = base + incl;
+        s_off[n_exp] = end;
+      }
+    }
+    base += __shfl(incl, 63, 64);
+  }
+}
+
+// The expert of tile t: the last one whose tiles begin at or before t.
+__device__ __forceinline__ int find_expert(const int* s_pref, int n_exp, int t, int lane) {
+  int expert = 0;
+  for (int e0 = 1; e0 <= n_exp; e0 += 64) {
+    const int idx = e0 + lane;
+    const bool le = idx <= n_exp && s_pref[idx] <= t;
+    expert += __popcll(__ballot(le));
+    if (__ballot(idx <= n_exp && !le)) break;
+  }
+  return __builtin_amdgcn_readfirstlane(expert);
+}
+
+// ---------------------------------------------------------------------------
+// Large tiles: up to 256 rows x 256 product columns (gated: 128 gate and the
+// matching 128 up columns), eight waves, wave (wr, wc) a quarter of the rows
+// x 128 columns: 128 accumulators a lane. Both operands of a K step (one
+// block of 128) are copied to LDS one step ahead (2 x 64 KB), with the rows'
+// 256 scales. One workgroup per CU works through its share of the tile list,
+// which is dealt to the XCDs in contiguous runs.
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 512;
+constexpr int BM = 256, BN = 256, BK = 128;
+constexpr int kTile = BM * BK;           // bytes of one operand's slot
+constexpr int kOffW = 2 * kTile, kOffS = 4 * kTile;
+constexpr int kLds = kOffS + 2 * BM * 4;
+
+template <bool GATED, int KIND>
+__global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
+    const uint8_t* __restrict__ Xq, const float* __restrict__ Xs,
+    const int32_t* __restrict__ offsets, int n_experts, int64_t cap_rows,
+    const uint8_t* __restrict__ Wq, const float* __restrict__ Ws, void* __restrict__ out, int K,
+    int N) {
+  constexpr int BN_OUT = GATED ? BN / 2 : BN;
+  static_assert(kLds + 2 * (kMaxTableExperts + 1) * 4 <= 160 * 1024, "LDS budget");
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds];
+  __shared__ int s_tab[2 * (kMaxTableExperts + 1)];
+  int* s_pref = s_tab;
+  int* s_off = s_tab + kMaxTableExperts + 1;
+
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n_exp = offsets ? n_experts : 1;
+  const int nt = (N + BN_OUT - 1) / BN_OUT;
+  const int ncols = GATED ? 2 * N : N;          // weight rows per expert
+  const int nk = (K + BK - 1) / BK;             // K steps = scale blocks
+  const int nnb = (ncols + 127) / 128;
+  const bool k_tail = (K & 64) != 0;            // the last step holds 64 codes a row
+  if (wave == 0) tile_table(offsets, n_exp, cap_rows, BM, nt, tid, s_pref, s_off);
+  __syncthreads();
+  const int R = __builtin_amdgcn_readfirstlane(s_pref[n_exp]);
+  const int G8 = static_cast<int>(gridDim.x) / kXcds;
+  const int xcd = static_cast<int>(blockIdx.x) % kXcds, slot = static_cast<int>(blockIdx.x) / kXcds;
+  const int per = (R + kXcds - 1) / kXcds;
+  const int run_end = min((xcd + 1) * per, R);
+  const unsigned lds0 = (unsigned)(uintptr_t)(lds_u8*)smem;
+  for (int t = xcd * per + slot; t < run_end; t += G8) {
+    // Lane-derived values are computed per tile (not hoisted out of the loop).
+    int lane_t = tid & 63;
+    asm volatile("" : "+v"(lane_t));
+    const int lane = lane_t;
+    const int expert = find_expert(s_pref, n_exp, t, lane);
+    const int seg_beg = __builtin_amdgcn_readfirstlane(s_off[expert]);
+    const int seg_end = __builtin_amdgcn_readfirstlane(s_off[expert + 1]);
+    const int local = t - __builtin_amdgcn_readfirstlane(s_pref[expert]);
+    const int cnt = seg_end - seg_beg;
+    const int mt = (cnt + BM - 1) / BM;
+    const int chunk = (cnt + mt - 1) / mt;      // near-equal row blocks
+    const int nb = local / mt, mb = local - nb * mt;
+    const int row_begin = seg_beg + mb * chunk;
+    const int rows = min(chunk, seg_end - row_begin);  // <= BM
+    if (rows <= 0) continue;  // (uniform)
+    const int n0 = nb * BN_OUT;
+    const int wr = wave >> 1, wc = wave & 1;
+
+    // Rows past the tile's (weight rows past the expert's) lie past the
+    // resource and read zeros; a gate column past N reads up columns, whose
+    // results are not stored.
+    const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(Xq + static_cast<int64_t>(row_begin) * K), 0, rows * K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(Wq + static_cast<int64_t>(expert) * ncols * K), 0, ncols * K, 0x00020000);
+    // Copies: wave w takes the 8-row groups w + 8 i of each operand (rows
+    // 64 i further on for the next i; gated: up columns from i = 2); lane ->
+    // row l / 8, LDS chunk l % 8.
+    const int crow = 8 * wave + (lane >> 3);
+    const int xc = (lane & 7) ^ swz(crow & 15), wk = (lane & 7) ^ swz(w_place(crow));
+    const int x_voff = crow * K + 16 * xc;
+    const int w_voff = (n0 + crow) * K + 16 * wk;
+    const int s_voff = 4 * (64 * (wave & 3) + lane);
+    // Weight scales of the wave's column groups.
+    const float* ws_row[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int c = GATED ? q * N + n0 + 64 * wc : n0 + 128 * wc + 64 * q;
+      ws_row[q] = Ws + (static_cast<int64_t>(expert) * nnb + min(c / 128, nnb - 1)) * nk;
+    }
+
+    auto run = [&](auto nxb_c) {
+      constexpr int NX = decltype(nxb_c)::value;  // 16-row blocks per wave
+      const int rowbase = wr * NX * 16;
+      f32x4 acc[2][4][NX];
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+          for (int x = 0; x < NX; ++x) acc[q][b][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // LDS addresses of fragments: row (l % 16), chunks l / 16 and 4 + l / 16.
+      int x_addr[2], w_addr[2];
+      {
+        const int i = lane & 15, g = lane >> 4;
+        const int wrow = (GATED ? 64 * wc : 128 * wc) + 16 * (i >> 2) + (i & 3);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          x_addr[p] = (rowbase + i) * 128 + (((g + 4 * p) ^ swz(i)) << 4);
+          w_addr[p] = kOffW + wrow * 128 + (((g + 4 * p) ^ swz(i)) << 4);
+        }
+      }
+      auto frag = [&](int base, const int(&a)[2]) {
+        const int4 lo = *reinterpret_cast<const int4*>(smem + base + a[0]);
+        const int4 hi = *reinterpret_cast<const int4*>(smem + base + a[1]);
+        return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      };
+      // Copies of step kt: x_at, w_at are the lane's offsets in it (out of
+      // range past the last step and in the half that a short last block
+      // lacks, which then reads zeros).
+      int x_at, w_at;
+      auto copy_begin = [&](int kt) {
+        const bool cut = k_tail && kt == nk - 1;
+        x_at = kt >= nk || (cut && xc >= 4) ? kOutOfRange : x_voff + kt * BK;
+        w_at = kt >= nk || (cut && wk >= 4) ? kOutOfRange : w_voff + kt * BK;
+        const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+            (void*)(Xs + static_cast<int64_t>(min(kt, nk - 1)) * cap_rows + row_begin), 0,
+            rows * 4, 0x00020000);
+        dma4(s_rsrc, s_voff, 0, lds0 + kOffS + (kt & 1) * BM * 4 + (wave & 3) * 256);
+      };
+      // Copy i (0 .. 3 weights, then NX of the activations).
+      auto copy = [&](int i, int kt) {
+        const int sl = (kt & 1) * kTile;
+        if (i < 4)
+          dma16(w_rsrc, w_at + (GATED && i >= 2 ? N + 64 * (i - 2) : 64 * i) * K, 0,
+                lds0 + kOffW + sl + (wave + 8 * i) * 1024);
+        else if (i - 4 < NX)
+          dma16(x_rsrc, x_at + 64 * (i - 4) * K, 0, lds0 + sl + (wave + 8 * (i - 4)) * 1024);
+      };
+      copy_begin(0);
+#pragma unroll
+      for (int i = 0; i < 4 + NX; ++i) copy(i, 0);
+      float wsv[2] = {0.f, 0.f};
+      for (int kt = 0; kt < nk; ++kt) {
+        if ((kt & 63) == 0) {  // 64 steps' weight scales, one a lane
+#pragma unroll
+          for (int q = 0; q < 2; ++q) wsv[q] = ws_row[q][min(kt + lane, nk - 1)];
+        }
+        // This step's copies are done, and after the barrier every wave's,
+        // and every wave has read what the next copies overwrite.
+        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        const int sl = (kt & 1) * kTile;
+        copy_begin(kt + 1);
+        i32x8 xf[NX], wf[2];
+        float s[2][NX];
+#pragma unroll
+        for (int x = 0; x < NX; ++x) xf[x] = frag(sl + x * 16 * 128, x_addr);
+        wf[0] = frag(sl, w_addr);
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          const float sx = *reinterpret_cast<const float*>(
+              smem + kOffS + (kt & 1) * BM * 4 + (rowbase + 16 * x + (lane & 15)) * 4);
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+            s[q][x] = sx * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                                         __builtin_bit_cast(int, wsv[q]), kt & 63));
+        }
+        constexpr int LAG = 2, M = 8 * NX;
+        f32x4 part[LAG + 1];
+#pragma unroll
+        for (int m = 0; m < M + LAG; ++m) {
+          if (m < M) {
+            const int f = m / NX, x = m % NX;
+            if (x == 0) {
+              if (f + 1 < 8) {
+                const int q = (f + 1) >> 2, b = (f + 1) & 3;
+                wf[(f + 1) & 1] = frag(sl + (q * (GATED ? 128 : 64) + 4 * b) * 128, w_addr);
+              }
+              copy(f, kt + 1);
+            }
+            part[m % (LAG + 1)] = mma(wf[f & 1], xf[x]);
+          }
+          if (m >= LAG) {
+            const int o = m - LAG, f = o / NX, x = o % NX;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[f >> 2][f & 3][x][r] = __builtin_fmaf(part[o % (LAG + 1)][r], s[f >> 2][x],
+                                                        acc[f >> 2][f & 3][x][r]);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      // ---- epilogue: lane group g = l / 16 holds columns 16 g .. + 15 of a
+      // 64-column group, row l % 16 of each row block ----
+      const int g = lane >> 4;
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        const int r = rowbase + 16 * x + (lane & 15);
+        if (r < rows) {
+          const int64_t o = static_cast<int64_t>(row_begin + r) * N;
+          float v[16];
+          if (GATED) {
+            const int c = n0 + 64 * wc + 16 * g;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              v[i] = silu_mul(acc[0][i >> 2][x][i & 3], acc[1][i >> 2][x][i & 3]);
+            if (c < N) store16<KIND>(out, o + c, v);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const int c = n0 + 128 * wc + 64 * q + 16 * g;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = acc[q][i >> 2][x][i & 3];
+              if (c < N) store16<KIND>(out, o + c, v);
+            }
+          }
+        }
+      }
+    };
+    const int nblk = (rows + 15) / 16;
+    switch ((nblk + 3) / 4) {
+      case 4: run(std::integral_constant<int, 4>{}); break;
+      case 3: run(std::integral_constant<int, 3>{}); break;
+      case 2: run(std::integral_constant<int, 2>{}); break;
+      default: run(std::integral_constant<int, 1>{}); break;
+    }
+    // Every wave is done with this tile's LDS before the next tile's copies.
+    __syncthreads();
+  }
+}
+
+int num_cus() {
+  static int cus = 0;
+  if (cus == 0) {
+    int dev = 0;
+    hipDeviceProp_t p;
+    if (hipGetDevice(&dev) == hipSuccess && hipGetDeviceProperties(&p, dev) == hipSuccess)
+      cus = p.multiProcessorCount;
+    if (cus <= 0) cus = 256;
+  }
+  return cus;
+}
+
+template <bool GATED, int KIND>
+hipError_t launch_gemm(int n_experts, int64_t cap_rows, int K, int N, const void* xq,
+                       const float* xs, const int32_t* offsets, const void* wq, const float* ws,
+                       void* out, hipStream_t s) {
+  const int bn = GATED ? BN / 2 : BN;
+  const int64_t mt =
+      std::min<int64_t>(cap_rows, (cap_rows + BM - 1) / BM + (offsets ? n_experts : 0));
+  const int64_t tiles = mt * ((N + bn - 1) / bn);
+  const int64_t cus = std::max<int64_t>(kXcds, num_cus() / kXcds * kXcds);
+  const int64_t g = std::min((tiles + kXcds - 1) / kXcds * kXcds, cus);
+  fp8_gemm_kernel<GATED, KIND><<<static_cast<unsigned>(g), kThreads, 0, s>>>(
+      static_cast<const uint8_t*>(xq), xs, offsets, n_experts, cap_rows,
+      static_cast<const uint8_t*>(wq), ws, out, K, N);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gate_up_fp8(int n_experts, int64_t cap_rows, int D, int inter, const void* xq,
+                              const float* xs, const int32_t* offsets, const void* wq,
+                              const float* ws, void* h, hipStream_t s) {
+  if (cap_rows == 0) return hipSuccess;
+  return launch_gemm<true, kOutBf16>(n_experts, cap_rows, D, inter, xq, xs, offsets, wq, ws, h, s);
+}
+
+hipError_t launch_down_fp8(int n_experts, int64_t cap_rows, int D, int inter, const void* hq,
+                           const float* hs, const int32_t* offsets, const void* wq,
+                           const float* ws, void* y, bool y_half, hipStream_t s) {
+  if (cap_rows == 0) return hipSuccess;
+  auto* f = y_half ? launch_gemm<false, kOutF16> : launch_gemm<false, kOutF32>;
+  return f(n_experts, cap_rows, inter, D, hq, hs, offsets, wq, ws, y, s);
+}
+
+}  // namespace moe

@@ -240,4 +240,49 @@ int64_t orth_tiles(int n, int rows, int cols);
 hipError_t launch_orth(int n, int rows, int cols, const moe_matrices& g, const moe_matrices* mom,
                        const moe_matrices& w, const moe_muon_desc& d, void* ws, hipStream_t s);
 
+// FP8 with block scales (fp8_quant.hip, ffn_fp8.hip).
+hipError_t launch_fp8_quantize_rows(bool bf16, int64_t rows, int K, const void* x, void* codes,
+                                    float* scales, hipStream_t s);
+hipError_t launch_fp8_pack_weights(bool bf16, int n, int K, int N, const void* w, void* codes,
+                                   float* scales, hipStream_t s);
+hipError_t launch_gate_up_fp8(int n_experts, int64_t cap_rows, int D, int inter, const void* xq,
+                              const float* xs, const int32_t* offsets, const void* wq,
+                              const float* ws, void* h, hipStream_t s);
+hipError_t launch_down_fp8(int n_experts, int64_t cap_rows, int D, int inter, const void* hq,
+                           const float* hs, const int32_t* offsets, const void* wq,
+                           const float* ws, void* y, bool y_half, hipStream_t s);
+
+// Activation checkpoints in 8 bits: rows (ckpt.hip), and G | U in the
+// epilogues of the training forward's GEMM 1 (ffn_bf16.hip) and of the dH GEMM
+// (ffn_bwd.hip): codes [cap, 2 inter], scales [cap, 2 inter / 32].
+hipError_t launch_ckpt_save(bool bf16, int64_t rows, int D, const void* x, void* codes,
+                            void* scales, hipStream_t s);
+hipError_t launch_ckpt_restore(bool bf16, int64_t n, int64_t rows, int D, const void* codes,
+                               const void* scales, const int32_t* index, void* out,
+                               hipStream_t s);
+hipError_t launch_gate_up_ckpt_bf16(int n_experts, int64_t cap_rows, int D, int inter,
+                                    const void* x_perm, const int32_t* offsets,
+                                    const void* w_gate_up, void* h, void* codes, void* scales,
+                                    hipStream_t s);
+hipError_t launch_dh_swiglu_ckpt(int n_experts, int64_t cap_rows, int D, int inter,
+                                 const void* dy_perm, const int32_t* offsets, const void* w_down,
+                                 const void* codes, const void* scales, void* dgu, void* h,
+                                 hipStream_t s);
+
+// Balance loss and the dense router backward (balance.hip).
+size_t balance_ws_bytes(int T, int E);
+hipError_t launch_balance_loss(int dtype, int T, int E, int k, const void* logits,
+                               const int32_t* topk, const uint8_t* mask, float coef,
+                               int32_t* counts, int32_t* tokens, float* prob_sum, float* loss,
+                               void* ws, hipStream_t s);
+hipError_t launch_balance_bwd(int dtype, int T, int E, int k, const void* logits,
+                              const int32_t* topk, const uint8_t* mask, float coef,
+                              const int32_t* counts, const int32_t* tokens, const float* dloss,
+                              const float* dlogit, float* dlogits, hipStream_t s);
+// Floats of the parts of dW (0: one part); the grid's size is checked there.
+size_t router_dense_ws_floats(int T, int E, int D);
+hipError_t launch_router_dense_bwd(bool bf16, int T, int E, int D, const float* dlogits,
+                                   const void* x, const float* w, int accumulate, float* dx,
+                                   float* dw, float* ws, hipStream_t s);
+
 }  // namespace moe
