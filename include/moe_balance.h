@@ -80,8 +80,9 @@ moe_status moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t dt
  * moe_router_backward_dense - gradients of logits = x W_r^T from dense dlogits:
  *   dx[t]     = sum_e dlogits[t, e] w_router[e]   (added to dx if accumulate)
  *   dw_router = dlogits^T x
- * on the fp32 matrix instructions (products and sums in fp32), summed over
- * tokens in an order that depends on the sizes alone.
+ * with products and sums as exact as fp32's (on the bf16 matrix cores, fp32
+ * operands as the sum of three bf16 parts; an infinite operand gives NaN),
+ * summed over tokens in an order that depends on the sizes alone.
  *
  *  T, E, D    0 .. INT32_MAX; 1 .. MOE_MAX_EXPERTS; a positive multiple of
  *             64, at most MOE_MAX_WIDTH

@@ -3,12 +3,13 @@
 // moe_balance.h).
 //
 // Forward and backward are bound by reading the logits (and writing their
-// gradients) once: a token's E logits sit in the registers of L lanes
-// (L = 8 .. 64, the power of two that covers E, 64 beyond), lane l holding
-// experts l, l + L, ...; maximum and sum are exchanged between the L lanes.
-// The forward sums p over a workgroup's tokens in registers, then over its
-// lane groups in LDS, writes one partial of E values, and a second launch
-// adds the partials in fp64 (one workgroup needs no second launch).
+// gradients) once: a token's E logits sit in the registers of L lanes, lane l
+// holding experts l, l + L, ... (NI of them): few lanes a token (L = 4 .. 64,
+// up to 8 logits each) keep several tokens in a wave and the exchanges of
+// maximum and sum short. The forward sums p over a workgroup's tokens in
+// registers, then over its lane groups in LDS, writes one partial of E values,
+// and a second launch adds the partials in fp64 (one workgroup needs no second
+// launch).
 #include <algorithm>
 #include <type_traits>
 
@@ -18,23 +19,37 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxParts = 256;   // workgroups of the forward
+constexpr int kLossThreads = 512;
+constexpr int kMaxParts = 128;   // workgroups of the forward
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float load_logit(const _Float16* p) { return static_cast<float>(*p); }
 
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int off = L / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, L));
+// Exchanges between the L lanes of a token: inside 16 lanes by DPP, beyond by
+// shuffles.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+template <int L, typename F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  if (L > 1) v = f(v, dpp<0xB1>(v));    // lane ^ 1
+  if (L > 2) v = f(v, dpp<0x4E>(v));    // lane ^ 2
+  if (L > 4) v = f(v, dpp<0x141>(v));   // 7 - lane in groups of 8
+  if (L > 8) v = f(v, dpp<0x140>(v));   // 15 - lane in groups of 16
+  if (L > 16) v = f(v, __shfl_xor(v, 16, 64));
+  if (L > 32) v = f(v, __shfl_xor(v, 32, 64));
   return v;
 }
 template <int L>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int L>
 __device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int off = L / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, L);
-  return v;
+  return group_reduce<L>(v, [](float a, float b) { return a + b; });
 }
 
 // p of one token: e[i] = exp(z - max) on return, the factor 1 / sum returned.
@@ -60,41 +75,38 @@ __device__ __forceinline__ float softmax_row(const T* __restrict__ z, int E, int
   return s == 0.f ? 0.f : 1.f / s;
 }
 
-// ws: prob[parts][E] fp32, count[parts][E], tokens[parts] (with one part the
-// results are written at once).
-__device__ __forceinline__ void write_loss(int E, int k, float coef, const int32_t* counts,
-                                           int32_t n, const double* prob, int32_t* tokens,
-                                           float* loss, double* s_red) {
-  double v = 0.0;
-  for (int e = threadIdx.x; e < E; e += blockDim.x) v += prob[e] * counts[e];
-  s_red[threadIdx.x] = v;
+// The loss from the sums: v, each thread's share of sum c P, is added over the
+// workgroup (waves by shuffles, then in order).
+__device__ __forceinline__ void write_loss(int E, int k, float coef, double v, int32_t n,
+                                           int32_t* tokens, float* loss, double* s_red) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
   __syncthreads();
-  for (int w = static_cast<int>(blockDim.x) / 2; w > 0; w >>= 1) {
-    if (static_cast<int>(threadIdx.x) < w) s_red[threadIdx.x] += s_red[threadIdx.x + w];
-    __syncthreads();
-  }
   if (threadIdx.x == 0) {
+    for (int w = 1; w < static_cast<int>(blockDim.x) / 64; ++w) v += s_red[w];
     const double N = n;
     *tokens = n;
-    *loss = n > 0 ? static_cast<float>(coef * (static_cast<double>(E) / (k * N * N)) * s_red[0])
-                  : 0.f;
+    *loss = n > 0 ? static_cast<float>(coef * (static_cast<double>(E) / (k * N * N)) * v) : 0.f;
   }
 }
 
+// With more than one part, each writes p_prob[part][E] fp32, p_count[part][E]
+// and p_tok[part] (the workspace, in this order).
 template <typename T, int L, int NI>
-__global__ __launch_bounds__(kThreads) void balance_part_kernel(
+__global__ __launch_bounds__(kLossThreads) void balance_part_kernel(
     int Tn, int E, int k, const T* __restrict__ logits, const int32_t* __restrict__ topk,
     const uint8_t* __restrict__ mask, float coef, int parts, float* __restrict__ p_prob,
     int32_t* __restrict__ p_count, int32_t* __restrict__ p_tok, int32_t* __restrict__ counts,
     int32_t* __restrict__ tokens, float* __restrict__ prob_sum, float* __restrict__ loss) {
-  constexpr int G = kThreads / L;   // tokens at a time
+  constexpr int G = kLossThreads / L;   // tokens at a time
   constexpr int EC = L * NI;
-  __shared__ float s_prob[kThreads * NI];        // [G][EC]
+  __shared__ float s_prob[kLossThreads * NI];    // [G][EC]
   __shared__ int32_t s_count[EC];
   __shared__ int32_t s_tok;
-  __shared__ double s_d[EC + kThreads];
+  __shared__ double s_red[kLossThreads / 64];
   const int tid = threadIdx.x, l = tid % L, g = tid / L;
-  for (int e = tid; e < EC; e += kThreads) s_count[e] = 0;
+  for (int e = tid; e < EC; e += kLossThreads) s_count[e] = 0;
   if (tid == 0) s_tok = 0;
   __syncthreads();
   const int64_t t0 = static_cast<int64_t>(Tn) * blockIdx.x / parts;
@@ -109,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(
     for (int i = 0; i < NI; ++i) acc[i] += e[i] * r;
     tok += l == 0;
   }
-  for (int64_t q = t0 * k + tid; q < t1 * k; q += kThreads) {
+  for (int64_t q = t0 * k + tid; q < t1 * k; q += kLossThreads) {
     const int e = topk[q];
     if (e >= 0 && e < E && !(mask && mask[q / k] == 0)) atomicAdd(&s_count[e], 1);
   }
@@ -117,13 +129,18 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(
 #pragma unroll
   for (int i = 0; i < NI; ++i) s_prob[g * EC + l + L * i] = acc[i];
   __syncthreads();
-  for (int e = tid; e < E; e += kThreads) {
-    float v = 0.f;
-    for (int j = 0; j < G; ++j) v += s_prob[j * EC + e];
+  // Sum over the G lane groups: two halves until one is left.
+  for (int w = G / 2; w > 0; w >>= 1) {
+    for (int q = tid; q < w * EC; q += kLossThreads) s_prob[q] += s_prob[q + w * EC];
+    __syncthreads();
+  }
+  double cp = 0.0;
+  for (int e = tid; e < E; e += kLossThreads) {
+    const float v = s_prob[e];
     if (parts == 1) {
       counts[e] = s_count[e];
       prob_sum[e] = v;
-      s_d[e] = v;
+      cp += static_cast<double>(v) * s_count[e];
     } else {
       p_prob[static_cast<int64_t>(blockIdx.x) * E + e] = v;
       p_count[static_cast<int64_t>(blockIdx.x) * E + e] = s_count[e];
@@ -133,8 +150,7 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(
     if (tid == 0) p_tok[blockIdx.x] = s_tok;
     return;
   }
-  __syncthreads();
-  write_loss(E, k, coef, s_count, s_tok, s_d, tokens, loss, s_d + EC);
+  write_loss(E, k, coef, cp, s_tok, tokens, loss, s_red);
 }
 
 // One workgroup of 1024 threads: the partials of an expert are summed by
@@ -147,36 +163,49 @@ __global__ __launch_bounds__(1024) void balance_finish_kernel(
     float* __restrict__ loss) {
   __shared__ double s_prob[1024];
   __shared__ int32_t s_count[1024];
-  __shared__ double s_red[1024];
-  __shared__ int32_t s_tok;
+  __shared__ double s_red[16];
   const int tid = threadIdx.x, e = tid % EP, j = tid / EP, J = 1024 / EP;
-  if (tid == 0) s_tok = 0;
+  // Tokens: every wave adds the parts' numbers up for itself.
+  int n = 0;
+  for (int p = tid & 63; p < parts; p += 64) n += p_tok[p];
   double v = 0.0;
   int c = 0;
-  if (e < E)
-    for (int p = j; p < parts; p += J) {
-      v += p_prob[static_cast<int64_t>(p) * E + e];
-      c += p_count[static_cast<int64_t>(p) * E + e];
+  if (e < E) {
+    for (int p0 = j; p0 < parts; p0 += 16 * J) {  // sixteen parts' loads in flight
+      float f[16];
+      int m[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int p = min(p0 + i * J, parts - 1);
+        f[i] = p_prob[static_cast<int64_t>(p) * E + e];
+        m[i] = p_count[static_cast<int64_t>(p) * E + e];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (p0 + i * J < parts) {
+          v += f[i];
+          c += m[i];
+        }
     }
-  s_red[tid] = v;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, 64);
+  s_prob[tid] = v;
   s_count[tid] = c;
   __syncthreads();
-  if (tid < parts) atomicAdd(&s_tok, p_tok[tid]);
+  double cp = 0.0;
   if (j == 0) {
     for (int i = 1; i < J; ++i) {
-      v += s_red[i * EP + e];
+      v += s_prob[i * EP + e];
       c += s_count[i * EP + e];
     }
     if (e < E) {
       counts[e] = c;
       prob_sum[e] = static_cast<float>(v);
-      s_prob[e] = v;
+      cp = v * c;
     }
   }
-  __syncthreads();
-  if (j == 0 && e < E) s_count[e] = c;
-  __syncthreads();
-  write_loss(E, k, coef, s_count, s_tok, s_prob, tokens, loss, s_red);
+  write_loss(E, k, coef, cp, n, tokens, loss, s_red);
 }
 
 __global__ void balance_empty_kernel(int E, int32_t* counts, int32_t* tokens, float* prob_sum,
@@ -237,62 +266,329 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Dense router backward on v_mfma_f32_32x32x2_f32.
+// Dense router backward
 //   dx [T, D] = dz [T, E] W [E, D]    (contraction over experts)
 //   dW [E, D] = dz^T [E, T] x [T, D]  (contraction over tokens, in parts)
-// C [M, N] = sum_k A(k, m) B(k, n), a 64 x 64 tile per workgroup of four
-// waves (one 32 x 32 block each), K in steps of 16 through LDS.
+// with fp32 precision on the bf16 matrix cores: an fp32 value is the exact sum
+// of three bf16 values (its 24 significant bits cut into 8 each), a product of
+// two is nine bf16 products, of which those below 2^-24 of it (lo mid, mid lo
+// and lo lo) are left out; x in bf16 needs three. That is six (three)
+// instructions at 16 times the rate of the fp32 one. (Infinities come out as
+// NaN.)
 // ---------------------------------------------------------------------------
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-constexpr int TM = 64, TN = 64, TK = 16, kLdsPitch = 68;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) unsigned char lds_u8;
 
-// A_KM: A is [K][M] in memory (dz for dW), else [M][K] (dz for dx).
-template <typename TB, bool A_KM>
-__global__ __launch_bounds__(kThreads) void router_dense_kernel(
-    const float* __restrict__ A, const TB* __restrict__ B, float* __restrict__ C, int64_t M,
-    int N, int64_t K, int parts, int accumulate) {
-  __shared__ float sa[TK * kLdsPitch], sb[TK * kLdsPitch];
+// The three parts of two values, packed (a in the low half).
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& mid,
+                                       uint32_t& lo) {
+  const uint32_t a1 = __float_as_uint(a), b1 = __float_as_uint(b);
+  const float ar = a - __uint_as_float(a1 & 0xffff0000u);
+  const float br = b - __uint_as_float(b1 & 0xffff0000u);
+  const uint32_t a2 = __float_as_uint(ar), b2 = __float_as_uint(br);
+  const uint32_t a3 = __float_as_uint(ar - __uint_as_float(a2 & 0xffff0000u));
+  const uint32_t b3 = __float_as_uint(br - __uint_as_float(b2 & 0xffff0000u));
+  hi = __builtin_amdgcn_perm(b1, a1, 0x07060302);
+  mid = __builtin_amdgcn_perm(b2, a2, 0x07060302);
+  lo = __builtin_amdgcn_perm(b3, a3, 0x07060302);
+}
+__device__ __forceinline__ void split8(const float (&f)[8], uint4 (&p)[3]) {
+  uint32_t w[3][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split2(f[2 * i], f[2 * i + 1], w[0][i], w[1][i], w[2][i]);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) p[q] = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+}
+__device__ __forceinline__ f32x16 mma32(const uint4& a, const uint4& b, const f32x16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+// c += a b from the parts, smallest products first.
+__device__ __forceinline__ f32x16 mma_parts(const uint4 (&a)[3], const uint4 (&b)[3], f32x16 c) {
+  c = mma32(a[2], b[0], c);
+  c = mma32(a[0], b[2], c);
+  c = mma32(a[1], b[1], c);
+  c = mma32(a[1], b[0], c);
+  c = mma32(a[0], b[1], c);
+  return mma32(a[0], b[0], c);
+}
+
+// dx: a workgroup takes 64 tokens and a range of columns. Its dz, up to KC
+// experts at a time, is split into LDS ([part][KC / 64][64 tokens][64], 16-byte
+// chunk c of token r at c ^ (r & 7) ^ ((r >> 3) & 1)); every wave takes blocks
+// of 32 columns, reads W from memory in the fragments' own order (a lane 8
+// experts of one column) one block ahead and splits it in registers: W is
+// read once per workgroup, mostly from L2, and needs no workspace.
+constexpr int kDxTokens = 64;
+constexpr unsigned kOutOfRange = 0x80000000u;  // past W (at most 2^30 bytes), and so is a chunk's
+template <int KC>
+__global__ __launch_bounds__(kThreads, KC == 256 ? 1 : 2) void router_dx_kernel(
+    const float* __restrict__ dz, const float* __restrict__ W, float* __restrict__ dx, int T,
+    int E, int D, int cols, int col_tiles, int accumulate) {
+  constexpr int NK = KC / 16, kPlane = kDxTokens * KC * 2;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[3 * kPlane];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int nt = (N + TN - 1) / TN;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x / nt) * TM;
-  const int n0 = static_cast<int>(blockIdx.x % nt) * TN;
-  const int64_t k0 = K * blockIdx.y / parts, k1 = K * (blockIdx.y + 1) / parts;
-  C += static_cast<int64_t>(blockIdx.y) * M * N;
-  const int wm = 32 * (wave >> 1), wn = 32 * (wave & 1);
-  f32x16 acc;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / col_tiles) * kDxTokens;
+  const int c_begin = static_cast<int>(blockIdx.x % col_tiles) * cols;
+  const int c_end = min(c_begin + cols, D);
+  const int half = lane >> 5, l31 = lane & 31;
+  for (int e0 = 0; e0 < E; e0 += KC) {
+    if (e0 > 0) __syncthreads();
+    for (int q = tid; q < kDxTokens * (KC / 8); q += kThreads) {
+      const int r = q / (KC / 8), c = q % (KC / 8);
+      float f[8];
 #pragma unroll
-  for (int r = 0; r < 16; ++r) acc[r] = 0.f;
-  for (int64_t kb = k0; kb < k1; kb += TK) {
+      for (int j = 0; j < 8; ++j) {
+        const int e = e0 + 8 * c + j;
+        f[j] = t0 + r < T && e < E ? dz[(t0 + r) * E + e] : 0.f;
+      }
+      uint4 p[3];
+      split8(f, p);
+      const int o = (c >> 3) * (kDxTokens * 128) + r * 128 +
+                    (((c & 7) ^ (r & 7) ^ ((r >> 3) & 1)) << 4);
 #pragma unroll
-    for (int i = 0; i < TK * TM / kThreads; ++i) {
-      const int q = tid + kThreads * i;
-      const int kk = A_KM ? q / TM : q % TK, m = A_KM ? q % TM : q / TK;
-      const bool ok = kb + kk < k1 && m0 + m < M;
-      sa[kk * kLdsPitch + m] =
-          ok ? A[A_KM ? (kb + kk) * M + m0 + m : (m0 + m) * K + kb + kk] : 0.f;
-      const int bk = q / TN, n = q % TN;
-      const bool okb = kb + bk < k1 && n0 + n < N;
-      sb[bk * kLdsPitch + n] = okb ? load_act(B + (kb + bk) * N + n0 + n) : 0.f;
+      for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(smem + i * kPlane + o) = p[i];
     }
     __syncthreads();
+    const bool add = accumulate || e0 > 0;
+    // W's rows from e0 on; rows past E lie past the resource and read zeros.
+    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(W + static_cast<int64_t>(e0) * D), 0, (E - e0) * D * 4, 0x00020000);
+    // dx's rows of this workgroup (rows past T: neither read nor written).
+    const __amdgpu_buffer_rsrc_t d_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        dx + t0 * D, 0, static_cast<int>(min(static_cast<int64_t>(kDxTokens), T - t0)) * D * 4,
+        0x00020000);
+    float wf[NK][8];
+    auto fetch = [&](int ks, int c0) {
+      const unsigned voff = c0 < c_end ? (8 * half * D + c0 + l31) * 4 : kOutOfRange;
 #pragma unroll
-    for (int kk = 0; kk < TK; kk += 2) {
-      const int ks = kk + (lane >> 5);
-      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sa[ks * kLdsPitch + wm + (lane & 31)],
-                                                 sb[ks * kLdsPitch + wn + (lane & 31)], acc, 0, 0,
-                                                 0);
+      for (int j = 0; j < 8; ++j)
+        wf[ks][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                  w_rsrc, static_cast<int>(voff + (16 * ks + j) * D * 4), 0, 0));
+    };
+#pragma unroll
+    for (int ks = 0; ks < NK; ++ks) fetch(ks, c_begin + 32 * wave);
+    for (int c0 = c_begin + 32 * wave; c0 < c_end; c0 += 128) {
+      f32x16 acc[2];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[m][r] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        uint4 b[3], a[2][3];
+        split8(wf[ks], b);
+        fetch(ks, c0 + 128);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int r = 32 * m + l31, c = 2 * ks + half;
+          const int o = (c >> 3) * (kDxTokens * 128) + r * 128 +
+                        (((c & 7) ^ (r & 7) ^ ((r >> 3) & 1)) << 4);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            a[m][i] = *reinterpret_cast<const uint4*>(smem + i * kPlane + o);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) acc[m] = mma32(a[m][kA[i]], b[kB[i]], acc[m]);
+      }
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int o = ((4 * half) * D + c0 + l31) * 4 + (32 * m + 8 * (r / 4) + r % 4) * D * 4;
+          float v = acc[m][r];
+          if (add)
+            v += __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(d_rsrc, o, 0, 0));
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), d_rsrc, o, 0, 0);
+        }
     }
+  }
+}
+
+// dW: a workgroup takes up to ME experts, 128 columns and a part of the
+// tokens, in steps of 32 tokens: dz and x go through registers (the next
+// step's loads run beside this step's products) into LDS rows [token][...],
+// dz in its parts, and are read transposed. ME = 128: a 2 x 2 layout of waves
+// of 64 experts x 64 columns, each part its own 256-byte rows; ME = 32: every
+// wave all experts x 32 columns, the parts side by side in one row.
+template <typename TX, int ME>
+struct DwShape {
+  static constexpr bool kF32 = sizeof(TX) == 4;
+  static constexpr int BQ = 128, BK = 32, ROW = 256;
+  static constexpr int NPB = kF32 ? 3 : 1;                  // parts of x
+  static constexpr int NRA = ME == 128 ? 3 : 1;             // row blocks of dz
+  static constexpr int MP = ME == 128 ? 2 : 1, MQ = ME == 128 ? 2 : 1;
+  static constexpr int SLOT = (NRA + NPB) * BK * ROW;
+};
+__device__ __forceinline__ int t_off(int k, int col) {
+  return k * 256 + (((col >> 3) ^ ((k & 3) << 2)) << 4) + ((col & 7) << 1);
+}
+
+template <typename TX, int ME>
+__global__ __launch_bounds__(kThreads, 2) void router_dw_kernel(
+    const float* __restrict__ dz, const TX* __restrict__ x, float* __restrict__ C, int T, int E,
+    int D, int parts, int vec) {
+  using S = DwShape<TX, ME>;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * S::SLOT];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int nt = (D + S::BQ - 1) / S::BQ;
+  const int m0 = static_cast<int>(blockIdx.x / nt) * ME, n0 = static_cast<int>(blockIdx.x % nt) * S::BQ;
+  const int64_t k0 = static_cast<int64_t>(T) * blockIdx.y / parts;
+  const int64_t k1 = static_cast<int64_t>(T) * (blockIdx.y + 1) / parts;
+  C += static_cast<int64_t>(blockIdx.y) * E * D;
+  // dz: thread -> token tid / 8, ME / 8 adjacent experts; x: token tid / 16
+  // (and + 16), 8 adjacent columns.
+  constexpr int NE = ME / 8;
+  float fz[NE], fx[S::kF32 ? 16 : 1];
+  uint4 ux[2];
+  const int zt = tid >> 3, ze = (tid & 7) * NE, xt = tid >> 4, xc = (tid & 15) * 8;
+  auto fetch = [&](int64_t kb) {
+    const int64_t t = kb + zt;
+    const float* p = dz + t * E + m0 + ze;
+#pragma unroll
+    for (int j = 0; j < NE; j += 4) {
+      if (vec) {
+        const float4 v = t < k1 && m0 + ze + j < E ? *reinterpret_cast<const float4*>(p + j)
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        fz[j] = v.x, fz[j + 1] = v.y, fz[j + 2] = v.z, fz[j + 3] = v.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) fz[j + i] = t < k1 && m0 + ze + j + i < E ? p[j + i] : 0.f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t tx = kb + xt + 16 * i;
+      const bool ok = tx < k1 && n0 + xc < D;
+      const TX* q = x + tx * D + n0 + xc;
+      if constexpr (S::kF32) {
+        const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = ok ? reinterpret_cast<const float4*>(q)[0] : z4;
+        const float4 b = ok ? reinterpret_cast<const float4*>(q)[1] : z4;
+        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) fx[8 * i + j] = v[j];
+      } else {
+        ux[i] = ok ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
+      }
+    }
+  };
+  auto put = [&](int slot) {
+    unsigned char* base = smem + slot * S::SLOT;
+    if constexpr (ME == 128) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fz[8 * h + j];
+        uint4 p[3];
+        split8(f, p);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          *reinterpret_cast<uint4*>(base + i * S::BK * S::ROW + t_off(zt, ze + 8 * h)) = p[i];
+      }
+    } else {
+      uint32_t w[3][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) split2(fz[2 * j], fz[2 * j + 1], w[0][j], w[1][j], w[2][j]);
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        *reinterpret_cast<uint2*>(base + t_off(zt, 32 * i + ze)) = make_uint2(w[i][0], w[i][1]);
+    }
+    base += S::NRA * S::BK * S::ROW;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int o = t_off(xt + 16 * i, xc);
+      if constexpr (S::kF32) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = fx[8 * i + j];
+        uint4 p[3];
+        split8(f, p);
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          *reinterpret_cast<uint4*>(base + q * S::BK * S::ROW + o) = p[q];
+      } else {
+        *reinterpret_cast<uint4*>(base + o) = ux[i];
+      }
+    }
+  };
+  // Transposed fragment of the 32 columns from col of 16 rows (tokens): lane l
+  // gets tokens 8 (l / 32) .. + 7 of column col + l % 32.
+  const int grp = lane >> 4, j16 = lane & 15;
+  auto frag = [&](const unsigned char* rows, int col) {
+    const lds_u8* p = (const lds_u8*)rows + t_off(8 * (grp >> 1) + (j16 >> 2),
+                                                  col + 16 * (grp & 1) + 4 * (j16 & 3));
+    const uint2 lo = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p));
+    const uint2 hi = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * S::ROW)));
+    return make_uint4(lo.x, lo.y, hi.x, hi.y);
+  };
+  const int wm = ME == 128 ? 64 * (wave >> 1) : 0;
+  const int wn = ME == 128 ? 64 * (wave & 1) : 32 * wave;
+  f32x16 acc[S::MP][S::MQ];
+#pragma unroll
+  for (int i = 0; i < S::MP; ++i)
+#pragma unroll
+    for (int j = 0; j < S::MQ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+  if (k0 < k1) {
+    fetch(k0);
+    put(0);
+  }
+  int slot = 0;
+  for (int64_t kb = k0; kb < k1; kb += S::BK, slot ^= 1) {
     __syncthreads();
+    const bool more = kb + S::BK < k1;
+    if (more) fetch(kb + S::BK);
+    const unsigned char* za = smem + slot * S::SLOT;
+    const unsigned char* xb = za + S::NRA * S::BK * S::ROW;
+#pragma unroll
+    for (int kk = 0; kk < S::BK; kk += 16) {
+      uint4 fa[S::MP][3], fb[S::MQ][S::NPB];
+#pragma unroll
+      for (int i = 0; i < S::MP; ++i)
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          fa[i][q] = ME == 128 ? frag(za + q * S::BK * S::ROW + kk * S::ROW, wm + 32 * i)
+                               : frag(za + kk * S::ROW, 32 * q);
+#pragma unroll
+      for (int j = 0; j < S::MQ; ++j)
+#pragma unroll
+        for (int q = 0; q < S::NPB; ++q)
+          fb[j][q] = frag(xb + q * S::BK * S::ROW + kk * S::ROW, wn + 32 * j);
+#pragma unroll
+      for (int i = 0; i < S::MP; ++i)
+#pragma unroll
+        for (int j = 0; j < S::MQ; ++j) {
+          if constexpr (S::kF32) {
+            acc[i][j] = mma_parts(fa[i], fb[j], acc[i][j]);
+          } else {
+#pragma unroll
+            for (int q = 2; q >= 0; --q) acc[i][j] = mma32(fa[i][q], fb[j][0], acc[i][j]);
+          }
+        }
+    }
+    if (more) put(slot ^ 1);
   }
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
-    const int64_t m = m0 + wm + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-    const int n = n0 + wn + (lane & 31);
-    if (m < M && n < N) {
-      float* c = C + m * N + n;
-      *c = accumulate ? *c + acc[r] : acc[r];
-    }
-  }
+  for (int i = 0; i < S::MP; ++i)
+#pragma unroll
+    for (int j = 0; j < S::MQ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int e = m0 + wm + 32 * i + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+        const int c = n0 + wn + 32 * j + (lane & 31);
+        if (e < E && c < D) C[static_cast<int64_t>(e) * D + c] = acc[i][j][r];
+      }
 }
 
 __global__ __launch_bounds__(kThreads) void router_dense_sum_kernel(const float4* __restrict__ part,
@@ -317,25 +613,28 @@ int balance_parts(int T, int E) {
   return static_cast<int>(std::min<int64_t>(std::max<int64_t>(n, 1), kMaxParts));
 }
 
-// Parts of the tokens in dW: enough workgroups for the chip, at least 256
-// tokens each.
+// Experts of a dW tile, and the parts its tokens are cut into: two workgroups
+// for every CU, at least 64 tokens each (two steps).
+int dw_experts(int E) { return E <= 32 ? 32 : 128; }
 int dense_parts(int T, int E, int D) {
-  const int64_t tiles = static_cast<int64_t>((E + TM - 1) / TM) * ((D + TN - 1) / TN);
-  const int64_t want = (1024 + tiles - 1) / tiles;
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, (T + 255) / 256)));
+  const int me = dw_experts(E);
+  const int64_t tiles = static_cast<int64_t>((E + me - 1) / me) * ((D + 127) / 128);
+  const int64_t want = std::max<int64_t>(1, 512 / tiles);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(want, T / 64)));
 }
 
 // f(lanes per token, registers per lane) for E experts.
 template <typename F>
 hipError_t for_experts(int E, F f) {
-  if (E <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-  if (E <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  if (E <= 32) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 1>{});
-  if (E <= 64) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
-  if (E <= 128) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
-  if (E <= 256) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
-  if (E <= 512) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
-  return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 16>{});
+  using std::integral_constant;
+  if (E <= 8) return f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
+  if (E <= 16) return f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  if (E <= 32) return f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+  if (E <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  if (E <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+  if (E <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+  if (E <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 
 template <typename T>
@@ -348,7 +647,7 @@ hipError_t balance_loss(int Tn, int E, int k, const T* logits, const int32_t* to
   int32_t* p_tok = p_count + static_cast<int64_t>(parts) * E;
   hipError_t e = for_experts(E, [&](auto L, auto NI) {
     balance_part_kernel<T, decltype(L)::value, decltype(NI)::value>
-        <<<parts, kThreads, 0, s>>>(Tn, E, k, logits, topk, mask, coef, parts, p_prob, p_count,
+        <<<parts, kLossThreads, 0, s>>>(Tn, E, k, logits, topk, mask, coef, parts, p_prob, p_count,
                                     p_tok, counts, tokens, prob_sum, loss);
     return hipGetLastError();
   });
@@ -381,19 +680,26 @@ template <typename TX>
 hipError_t dense_bwd(int T, int E, int D, const float* dlogits, const TX* x, const float* w,
                      int accumulate, float* dx, float* dw, float* ws, hipStream_t s) {
   hipError_t e = hipSuccess;
-  const int nt = (D + TN - 1) / TN;
   if (dx != nullptr && T > 0) {
-    const int64_t mt = (static_cast<int64_t>(T) + TM - 1) / TM;
-    router_dense_kernel<float, false><<<static_cast<unsigned>(mt * nt), kThreads, 0, s>>>(
-        dlogits, w, dx, T, D, E, 1, accumulate);
+    const int64_t mt = (static_cast<int64_t>(T) + kDxTokens - 1) / kDxTokens;
+    // Columns of a workgroup: all, or fewer until there are some 512 of them.
+    const int64_t want = std::max<int64_t>(1, 512 / mt);
+    const int cols = static_cast<int>((D + 128 * want - 1) / (128 * want) * 128);
+    const int ct = (D + cols - 1) / cols;
+    auto* k = E <= 64    ? router_dx_kernel<64>
+              : E <= 128 ? router_dx_kernel<128>
+                         : router_dx_kernel<256>;
+    k<<<static_cast<unsigned>(mt * ct), kThreads, 0, s>>>(dlogits, w, dx, T, E, D, cols, ct,
+                                                          accumulate);
     e = hipGetLastError();
   }
   if (e == hipSuccess && dw != nullptr) {
-    const int parts = T > 0 ? dense_parts(T, E, D) : 1;
-    const int64_t mt = (E + TM - 1) / TM;
-    const dim3 grid(static_cast<unsigned>(mt * nt), static_cast<unsigned>(parts));
-    router_dense_kernel<TX, true><<<grid, kThreads, 0, s>>>(dlogits, x, parts > 1 ? ws : dw, E, D,
-                                                            T, parts, 0);
+    const int parts = T > 0 ? dense_parts(T, E, D) : 1, me = dw_experts(E);
+    const dim3 grid(static_cast<unsigned>((E + me - 1) / me * ((D + 127) / 128)),
+                    static_cast<unsigned>(parts));
+    const int vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0;
+    auto* k = me == 32 ? router_dw_kernel<TX, 32> : router_dw_kernel<TX, 128>;
+    k<<<grid, kThreads, 0, s>>>(dlogits, x, parts > 1 ? ws : dw, T, E, D, parts, vec);
     e = hipGetLastError();
     if (e == hipSuccess && parts > 1) {
       const int64_t n4 = static_cast<int64_t>(E) * D / 4;
