@@ -316,28 +316,30 @@ __device__ __forceinline__ f32x16 mma_parts(const uint4 (&a)[3], const uint4 (&b
   return mma32(a[0], b[0], c);
 }
 
-// dx: a workgroup takes 64 tokens and a range of columns. Its dz, up to KC
-// experts at a time, is split into LDS ([part][KC / 64][64 tokens][64], 16-byte
+// dx: a workgroup takes MT tokens and a range of columns. Its dz, up to KC
+// experts at a time, is split into LDS ([part][KC / 64][MT tokens][64], 16-byte
 // chunk c of token r at c ^ (r & 7) ^ ((r >> 3) & 1)); every wave takes blocks
 // of 32 columns, reads W from memory in the fragments' own order (a lane 8
 // experts of one column) one block ahead and splits it in registers: W is
-// read once per workgroup, mostly from L2, and needs no workspace.
-constexpr int kDxTokens = 64;
+// read once per workgroup, mostly from L2, and needs no workspace. Eight waves
+// over 128 tokens for up to 128 experts (with four over 64 tokens, two
+// workgroups a CU, W is read and split twice as often: 63 us for T = 16384,
+// E = 128, D = 2048), four over 64 tokens beyond (LDS).
 constexpr unsigned kOutOfRange = 0x80000000u;  // past W (at most 2^30 bytes), and so is a chunk's
-template <int KC>
-__global__ __launch_bounds__(kThreads, KC == 256 ? 1 : 2) void router_dx_kernel(
+template <int KC, int MT, int THREADS>
+__global__ __launch_bounds__(THREADS, 1) void router_dx_kernel(
     const float* __restrict__ dz, const float* __restrict__ W, float* __restrict__ dx, int T,
     int E, int D, int cols, int col_tiles, int accumulate) {
-  constexpr int NK = KC / 16, kPlane = kDxTokens * KC * 2;
+  constexpr int NM = MT / 32, NW = THREADS / 64, NK = KC / 16, kPlane = MT * KC * 2;
   __shared__ __attribute__((aligned(16))) unsigned char smem[3 * kPlane];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x / col_tiles) * kDxTokens;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x / col_tiles) * MT;
   const int c_begin = static_cast<int>(blockIdx.x % col_tiles) * cols;
   const int c_end = min(c_begin + cols, D);
   const int half = lane >> 5, l31 = lane & 31;
   for (int e0 = 0; e0 < E; e0 += KC) {
     if (e0 > 0) __syncthreads();
-    for (int q = tid; q < kDxTokens * (KC / 8); q += kThreads) {
+    for (int q = tid; q < MT * (KC / 8); q += THREADS) {
       const int r = q / (KC / 8), c = q % (KC / 8);
       float f[8];
 #pragma unroll
@@ -347,7 +349,7 @@ __global__ __launch_bounds__(kThreads, KC == 256 ? 1 : 2) void router_dx_kernel(
       }
       uint4 p[3];
       split8(f, p);
-      const int o = (c >> 3) * (kDxTokens * 128) + r * 128 +
+      const int o = (c >> 3) * (MT * 128) + r * 128 +
                     (((c & 7) ^ (r & 7) ^ ((r >> 3) & 1)) << 4);
 #pragma unroll
       for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4*>(smem + i * kPlane + o) = p[i];
@@ -359,50 +361,60 @@ __global__ __launch_bounds__(kThreads, KC == 256 ? 1 : 2) void router_dx_kernel(
         (void*)(W + static_cast<int64_t>(e0) * D), 0, (E - e0) * D * 4, 0x00020000);
     // dx's rows of this workgroup (rows past T: neither read nor written).
     const __amdgpu_buffer_rsrc_t d_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        dx + t0 * D, 0, static_cast<int>(min(static_cast<int64_t>(kDxTokens), T - t0)) * D * 4,
+        dx + t0 * D, 0, static_cast<int>(min(static_cast<int64_t>(MT), T - t0)) * D * 4,
         0x00020000);
     float wf[NK][8];
     auto fetch = [&](int ks, int c0) {
-      const unsigned voff = c0 < c_end ? (8 * half * D + c0 + l31) * 4 : kOutOfRange;
+      unsigned voff = c0 < c_end ? ((16 * ks + 8 * half) * D + c0 + l31) * 4 : kOutOfRange;
+      asm volatile("" : "+v"(voff));  // (kept in one register, not one per row and step)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         wf[ks][j] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                                  w_rsrc, static_cast<int>(voff + (16 * ks + j) * D * 4), 0, 0));
+                                                  w_rsrc, static_cast<int>(voff + j * D * 4), 0, 0));
     };
 #pragma unroll
     for (int ks = 0; ks < NK; ++ks) fetch(ks, c_begin + 32 * wave);
-    for (int c0 = c_begin + 32 * wave; c0 < c_end; c0 += 128) {
-      f32x16 acc[2];
+    for (int c0 = c_begin + 32 * wave; c0 < c_end; c0 += 32 * NW) {
+      f32x16 acc[NM];
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[m][r] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < NK; ++ks) {
-        uint4 b[3], a[2][3];
+        uint4 b[3];
         split8(wf[ks], b);
-        fetch(ks, c0 + 128);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int r = 32 * m + l31, c = 2 * ks + half;
-          const int o = (c >> 3) * (kDxTokens * 128) + r * 128 +
-                        (((c & 7) ^ (r & 7) ^ ((r >> 3) & 1)) << 4);
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            a[m][i] = *reinterpret_cast<const uint4*>(smem + i * kPlane + o);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        fetch(ks, c0 + 32 * NW);
         constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
+        for (int m0 = 0; m0 < NM; m0 += 2) {
+          uint4 a[2][3];
 #pragma unroll
-          for (int m = 0; m < 2; ++m) acc[m] = mma32(a[m][kA[i]], b[kB[i]], acc[m]);
+          for (int m = 0; m < 2; ++m) {
+            const int r = 32 * (m0 + m) + l31, c = 2 * ks + half;
+            const int o = (c >> 3) * (MT * 128) + r * 128 +
+                          (((c & 7) ^ (r & 7) ^ ((r >> 3) & 1)) << 4);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              a[m][i] = *reinterpret_cast<const uint4*>(smem + i * kPlane + o);
+          }
+#pragma unroll
+          for (int i = 0; i < 6; ++i)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) acc[m0 + m] = mma32(a[m][kA[i]], b[kB[i]], acc[m0 + m]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+      int at = 0;
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int o = ((4 * half) * D + c0 + l31) * 4 + (32 * m + 8 * (r / 4) + r % 4) * D * 4;
+          if (r % 4 == 0) {
+            at = ((32 * m + 8 * (r / 4) + 4 * half) * D + c0 + l31) * 4;
+            asm volatile("" : "+v"(at));
+          }
+          const int o = at + (r % 4) * D * 4;
           float v = acc[m][r];
           if (add)
             v += __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(d_rsrc, o, 0, 0));
@@ -681,16 +693,27 @@ hipError_t dense_bwd(int T, int E, int D, const float* dlogits, const TX* x, con
                      int accumulate, float* dx, float* dw, float* ws, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (dx != nullptr && T > 0) {
-    const int64_t mt = (static_cast<int64_t>(T) + kDxTokens - 1) / kDxTokens;
-    // Columns of a workgroup: all, or fewer until there are some 512 of them.
-    const int64_t want = std::max<int64_t>(1, 512 / mt);
-    const int cols = static_cast<int>((D + 128 * want - 1) / (128 * want) * 128);
-    const int ct = (D + cols - 1) / cols;
-    auto* k = E <= 64    ? router_dx_kernel<64>
-              : E <= 128 ? router_dx_kernel<128>
-                         : router_dx_kernel<256>;
-    k<<<static_cast<unsigned>(mt * ct), kThreads, 0, s>>>(dlogits, w, dx, T, E, D, cols, ct,
-                                                          accumulate);
+    auto launch = [&](auto kc, auto tokens, auto threads) {
+      constexpr int MT = decltype(tokens)::value, NT = decltype(threads)::value;
+      const int64_t mt = (static_cast<int64_t>(T) + MT - 1) / MT;
+      // Columns of a workgroup: all, or fewer until there are some 2^15 / MT.
+      const int64_t want = std::max<int64_t>(1, (1 << 15) / MT / mt);
+      const int step = NT / 2;  // 32 columns a wave
+      const int cols = static_cast<int>((D + step * want - 1) / (step * want) * step);
+      const int ct = (D + cols - 1) / cols;
+      router_dx_kernel<decltype(kc)::value, MT, NT><<<static_cast<unsigned>(mt * ct), NT, 0, s>>>(
+          dlogits, w, dx, T, E, D, cols, ct, accumulate);
+    };
+    using std::integral_constant;
+    if (E <= 64)
+      launch(integral_constant<int, 64>{}, integral_constant<int, 128>{},
+             integral_constant<int, 512>{});
+    else if (E <= 128)
+      launch(integral_constant<int, 128>{}, integral_constant<int, 128>{},
+             integral_constant<int, 512>{});
+    else
+      launch(integral_constant<int, 256>{}, integral_constant<int, 64>{},
+             integral_constant<int, 256>{});
     e = hipGetLastError();
   }
   if (e == hipSuccess && dw != nullptr) {
