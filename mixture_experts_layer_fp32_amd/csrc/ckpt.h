@@ -17,24 +17,29 @@ __device__ __forceinline__ uint32_t ckpt_scale_bits(uint32_t amax_bits) {
 
 // Four codes: the nearest integers to v r, in -127 .. 127 since r <= 127 / amax
 // up to one rounding. Adding 1.5 * 2^23 rounds to the nearest even integer and
-// leaves it in the low bits. (Blocks with a NaN or an infinity have scale NaN
-// or infinity and code * scale is NaN whatever the code, unless it is finite
-// times infinity: v r is then 0 or NaN; NaN's bits are replaced by 0.)
-__device__ __forceinline__ uint32_t ckpt_code(float v, float r) {
-#pragma clang fp contract(off)  // the product is rounded before the sum
-  const float t = v * r;
-  const float m = t == t ? t : 0.f;
-  return __float_as_uint(m + 12582912.f) & 0xffu;
-}
+// leaves it in the low byte. (In a block with a NaN or an infinity the codes
+// mean nothing: its scale is NaN, or infinite with codes 0.)
 __device__ __forceinline__ uint32_t ckpt_codes4(float a, float b, float c, float d, float r) {
-  return ckpt_code(a, r) | ckpt_code(b, r) << 8 | ckpt_code(c, r) << 16 | ckpt_code(d, r) << 24;
+#pragma clang fp contract(off)  // the product is rounded before the sum
+  const float ar = a * r, br = b * r, cr = c * r, dr = d * r;
+  const uint32_t ab = __builtin_amdgcn_perm(__float_as_uint(br + 12582912.f),
+                                            __float_as_uint(ar + 12582912.f), 0x0c0c0400);
+  const uint32_t cd = __builtin_amdgcn_perm(__float_as_uint(dr + 12582912.f),
+                                            __float_as_uint(cr + 12582912.f), 0x04000c0c);
+  return ab | cd;
 }
 
 // The values of four codes (exact in fp32: 7 bits times 8).
 __device__ __forceinline__ void ckpt_values4(uint32_t q, float s, float* f) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    f[j] = static_cast<float>(static_cast<int32_t>(q << (24 - 8 * j)) >> 24) * s;
+  for (int j = 0; j < 4; ++j) f[j] = static_cast<float>(static_cast<int8_t>(q >> (8 * j))) * s;
+}
+
+// Two values to bf16 (v_cvt_pk_bf16_f32: to nearest even, NaN kept).
+typedef float ckpt_f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 ckpt_bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t cvt_bf16x2(float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(ckpt_f32x2{a, b}, ckpt_bf16x2));
 }
 
 }  // namespace moe

@@ -2,8 +2,8 @@
 // each 32 columns, and back, through an index if wanted.
 //
 // Both are bound by memory: (es + 1 + 1/16) bytes a value to save, (1 + 1/16)
-// read and es written to restore. A thread takes 8 columns (16 bytes of bf16,
-// 8 of codes), the four lanes of a DPP quad one 32-column block.
+// read and es written to restore. A thread takes 16 adjacent columns at a time
+// (a 16-byte access of codes), two lanes share a scale.
 #include "ckpt.h"
 #include "moe_internal.h"
 
@@ -12,91 +12,133 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// Sixteen values, at 16-column vector vec.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t vec, float (&f)[8]) {
-  if (BF16) {
-    const uint4 v = static_cast<const uint4*>(p)[vec];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void load16(const void* p, int64_t vec, uint4 (&w)[BF16 ? 2 : 4]) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 2 : 4); ++i)
+    w[i] = static_cast<const uint4*>(p)[vec * (BF16 ? 2 : 4) + i];
+}
+template <bool BF16>
+__device__ __forceinline__ void values16(const uint4 (&w)[BF16 ? 2 : 4], float (&f)[16]) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 2 : 4); ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      f[2 * j] = __uint_as_float(w[j] << 16);
-      f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      if (BF16) {
+        f[8 * i + 2 * j] = __uint_as_float(u[j] << 16);
+        f[8 * i + 2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      } else {
+        f[4 * i + j] = __uint_as_float(u[j]);
+      }
     }
-  } else {
-    const float4 a = static_cast<const float4*>(p)[2 * vec];
-    const float4 b = static_cast<const float4*>(p)[2 * vec + 1];
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = v[j];
   }
 }
 
 template <bool BF16>
-__device__ __forceinline__ void store8(void* p, int64_t vec, const float (&f)[8]) {
+__device__ __forceinline__ void store16(void* p, int64_t vec, const float (&f)[16]) {
   if (BF16) {
-    uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = f32_to_bf16(f[2 * j]) | (static_cast<uint32_t>(f32_to_bf16(f[2 * j + 1])) << 16);
-    static_cast<uint4*>(p)[vec] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 2; ++i)
+      static_cast<uint4*>(p)[2 * vec + i] =
+          make_uint4(cvt_bf16x2(f[8 * i], f[8 * i + 1]), cvt_bf16x2(f[8 * i + 2], f[8 * i + 3]),
+                     cvt_bf16x2(f[8 * i + 4], f[8 * i + 5]), cvt_bf16x2(f[8 * i + 6], f[8 * i + 7]));
   } else {
-    static_cast<float4*>(p)[2 * vec] = make_float4(f[0], f[1], f[2], f[3]);
-    static_cast<float4*>(p)[2 * vec + 1] = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      static_cast<float4*>(p)[4 * vec + i] =
+          make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
   }
 }
 
+// NV vectors a thread, their loads in flight together.
+constexpr int kSaveVecs = 2;
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void ckpt_save_kernel(const void* __restrict__ x,
                                                              int64_t n_vec,
-                                                             uint2* __restrict__ codes,
+                                                             uint4* __restrict__ codes,
                                                              uint16_t* __restrict__ scales) {
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  float f[8] = {};
-  const bool live = v < n_vec;  // n_vec is a multiple of 4: quads live or die together
-  if (live) load8<BF16>(x, v, f);
-  uint32_t amax = 0;
+  const int64_t v0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kSaveVecs) + threadIdx.x;
+  uint4 w[kSaveVecs][BF16 ? 2 : 4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(f[j]) & 0x7fffffffu);
-  amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(amax), 0xB1, 0xF, 0xF, false)));
-  amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(amax), 0x4E, 0xF, 0xF, false)));
-  const uint32_t s = ckpt_scale_bits(amax);
-  const float r = 1.0f / __uint_as_float(s << 16);
-  if (live) {
-    codes[v] = make_uint2(ckpt_codes4(f[0], f[1], f[2], f[3], r),
-                          ckpt_codes4(f[4], f[5], f[6], f[7], r));
-    if ((threadIdx.x & 3) == 0) scales[v >> 2] = static_cast<uint16_t>(s);
+  for (int i = 0; i < kSaveVecs; ++i) {
+    // (n_vec is even: both lanes of a block are past the end, or none)
+    const int64_t v = v0 + i * kThreads;
+    if (v < n_vec) load16<BF16>(x, v, w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kSaveVecs; ++i) {
+    const int64_t v = v0 + i * kThreads;
+    float f[16] = {};
+    if (v < n_vec) values16<BF16>(w[i], f);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(f[j]) & 0x7fffffffu);
+    amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(amax), 0xB1, 0xF, 0xF, false)));
+    const uint32_t s = ckpt_scale_bits(amax);
+    const float r = 1.0f / __uint_as_float(s << 16);
+    if (v < n_vec) {
+      codes[v] = make_uint4(ckpt_codes4(f[0], f[1], f[2], f[3], r),
+                            ckpt_codes4(f[4], f[5], f[6], f[7], r),
+                            ckpt_codes4(f[8], f[9], f[10], f[11], r),
+                            ckpt_codes4(f[12], f[13], f[14], f[15], r));
+      if ((threadIdx.x & 1) == 0) scales[v >> 1] = static_cast<uint16_t>(s);
+    }
   }
 }
 
-// vecs: 8-column vectors of a row.
+// 2^lanes_log threads take a row's vecs 16-column vectors, a workgroup
+// kThreads >> lanes_log rows at a time, kRestoreRows times.
+constexpr int kRestoreRows = 4;
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void ckpt_restore_kernel(
-    const uint2* __restrict__ codes, const uint16_t* __restrict__ scales,
-    const int32_t* __restrict__ index, int64_t n_vec, int64_t rows, int vecs,
+    const uint4* __restrict__ codes, const uint16_t* __restrict__ scales,
+    const int32_t* __restrict__ index, int64_t n, int64_t rows, int vecs, int lanes_log,
     void* __restrict__ out) {
-  const int64_t v = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (v >= n_vec) return;
-  const int64_t i = v / vecs;
-  const int64_t j = index ? static_cast<int64_t>(index[i]) : i;
-  if (j < 0 || j >= rows) return;
-  const int64_t src = j * vecs + (v - i * vecs);
-  const uint2 q = codes[src];
-  const float s = __uint_as_float(static_cast<uint32_t>(scales[src >> 2]) << 16);
-  float f[8];
-  ckpt_values4(q.x, s, f);
-  ckpt_values4(q.y, s, f + 4);
-  store8<BF16>(out, v, f);
+  const int lane = threadIdx.x & ((1 << lanes_log) - 1);
+  const int per = kThreads >> lanes_log;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * (per * kRestoreRows) + (threadIdx.x >> lanes_log);
+  int64_t src[kRestoreRows];  // row of codes, -1: none
+#pragma unroll
+  for (int r = 0; r < kRestoreRows; ++r) {
+    const int64_t i = i0 + r * per;
+    const int64_t j = i < n ? (index ? static_cast<int64_t>(index[i]) : i) : -1;
+    src[r] = j >= 0 && j < rows ? j : -1;
+  }
+  for (int c = lane; c < vecs; c += 1 << lanes_log) {
+    uint4 q[kRestoreRows];
+    uint32_t s[kRestoreRows];
+#pragma unroll
+    for (int r = 0; r < kRestoreRows; ++r)
+      if (src[r] >= 0) {
+        q[r] = codes[src[r] * vecs + c];
+        s[r] = scales[(src[r] * vecs + c) >> 1];
+      }
+#pragma unroll
+    for (int r = 0; r < kRestoreRows; ++r)
+      if (src[r] >= 0) {
+        const float sv = __uint_as_float(s[r] << 16);
+        float f[16];
+        ckpt_values4(q[r].x, sv, f);
+        ckpt_values4(q[r].y, sv, f + 4);
+        ckpt_values4(q[r].z, sv, f + 8);
+        ckpt_values4(q[r].w, sv, f + 12);
+        store16<BF16>(out, (i0 + r * per) * vecs + c, f);
+      }
+  }
 }
 
 }  // namespace
 
 hipError_t launch_ckpt_save(bool bf16, int64_t rows, int D, const void* x, void* codes,
                             void* scales, hipStream_t s) {
-  const int64_t n_vec = rows * D / 8;
+  const int64_t n_vec = rows * D / 16;
   if (n_vec == 0) return hipSuccess;
-  const unsigned grid = static_cast<unsigned>((n_vec + kThreads - 1) / kThreads);
+  constexpr int kPer = kThreads * kSaveVecs;
+  const unsigned grid = static_cast<unsigned>((n_vec + kPer - 1) / kPer);
   auto* k = bf16 ? ckpt_save_kernel<true> : ckpt_save_kernel<false>;
-  k<<<grid, kThreads, 0, s>>>(x, n_vec, static_cast<uint2*>(codes),
+  k<<<grid, kThreads, 0, s>>>(x, n_vec, static_cast<uint4*>(codes),
                               static_cast<uint16_t*>(scales));
   return hipGetLastError();
 }
@@ -104,13 +146,16 @@ hipError_t launch_ckpt_save(bool bf16, int64_t rows, int D, const void* x, void*
 hipError_t launch_ckpt_restore(bool bf16, int64_t n, int64_t rows, int D, const void* codes,
                                const void* scales, const int32_t* index, void* out,
                                hipStream_t s) {
-  const int64_t n_vec = n * D / 8;
-  if (n_vec == 0) return hipSuccess;
-  const unsigned grid = static_cast<unsigned>((n_vec + kThreads - 1) / kThreads);
+  if (n == 0) return hipSuccess;
+  const int vecs = D / 16;
+  int lanes_log = 0;  // a power of two of at most vecs lanes a row
+  while (lanes_log < 8 && (2 << lanes_log) <= vecs) ++lanes_log;
+  const int64_t per = static_cast<int64_t>(kThreads >> lanes_log) * kRestoreRows;
+  const unsigned grid = static_cast<unsigned>((n + per - 1) / per);
   auto* k = bf16 ? ckpt_restore_kernel<true> : ckpt_restore_kernel<false>;
-  k<<<grid, kThreads, 0, s>>>(static_cast<const uint2*>(codes),
-                              static_cast<const uint16_t*>(scales), index, n_vec, rows, D / 8,
-                              out);
+  k<<<grid, kThreads, 0, s>>>(static_cast<const uint4*>(codes),
+                              static_cast<const uint16_t*>(scales), index, n, rows, vecs,
+                              lanes_log, out);
   return hipGetLastError();
 }
 

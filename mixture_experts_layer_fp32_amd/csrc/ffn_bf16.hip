@@ -890,6 +890,32 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_bf16(
               __builtin_amdgcn_raw_buffer_store_b16(static_cast<unsigned short>(sb), gs_rsrc, os,
                                                     0, 0);
             }
+            // H as below, exchanged likewise: 16 adjacent columns a lane.
+            uint32_t hw[4][2];
+    #pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              __builtin_amdgcn_sched_barrier(0);
+              float v[4];
+    #pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float gt = acc[mb][q][4 * g + i], up = acc[mb][q + NQ / 2][4 * g + i];
+                v[i] = gt * up *
+                       __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * gt));
+              }
+              hw[g][0] = f16_sat_bits(v[0]) | (f16_sat_bits(v[1]) << 16);
+              hw[g][1] = f16_sat_bits(v[2]) | (f16_sat_bits(v[3]) << 16);
+            }
+            const int oh = ok ? (r * N_out + col + 16 * half) * 2 : kOutOfRange;
+    #pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              const auto a2 = __builtin_amdgcn_permlane32_swap(hw[p][0], hw[p + 2][0], false, false);
+              const auto b2 = __builtin_amdgcn_permlane32_swap(hw[p][1], hw[p + 2][1], false, false);
+              __builtin_amdgcn_raw_buffer_store_b128(
+                  u32x4{static_cast<unsigned>(a2[0]), static_cast<unsigned>(b2[0]),
+                        static_cast<unsigned>(a2[1]), static_cast<unsigned>(b2[1])},
+                  c_rsrc, oh + 16 * p, 0, 0);
+            }
+            continue;
           }
     #pragma unroll
           for (int g = 0; g < 4; ++g) {

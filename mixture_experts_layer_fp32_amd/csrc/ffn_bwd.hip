@@ -306,10 +306,15 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
           for (int mb = 0; mb < kMaxMB; ++mb) {
             if (mb < NMB) {
 #pragma unroll
-              for (int q = 0; q < NQ; ++q)
-                acc[mb][q] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8, fa[kk & 1][mb]),
-                    __builtin_bit_cast(bf16x8, fb[kk & 1][q]), acc[mb][q], 0, 0, 0);
+              for (int q = 0; q < NQ; ++q) {
+                const bf16x8 xa = __builtin_bit_cast(bf16x8, fa[kk & 1][mb]);
+                const bf16x8 xb = __builtin_bit_cast(bf16x8, fb[kk & 1][q]);
+                // kSwigluCkpt: the block transposed, so that a lane holds 16
+                // columns of one row.
+                acc[mb][q] = EPI == kSwigluCkpt
+                                 ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(xb, xa, acc[mb][q], 0, 0, 0)
+                                 : __builtin_amdgcn_mfma_f32_32x32x16_bf16(xa, xb, acc[mb][q], 0, 0, 0);
+              }
             }
             __builtin_amdgcn_sched_barrier(0);
             copy_item(kk * kMaxMB + mb, do_a, kt + 1, slot_a, do_b, kt + 2, slot_b);
@@ -339,30 +344,39 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
       }
     };
     if (EPI == kSwigluSaved && nmb > 0) load_gu(0, gpre[0], upre[0]);
-    // kSwigluCkpt: the same block's codes (four columns a word) and scales
-    // (G's in the low half).
+    // kSwigluCkpt: codes and scales of row block mb, as the forward stored them:
+    // lane l has row l % 32, columns 16 (l / 32) .. + 15 of each 32-column
+    // block. (Through resources over the tile's rows: what lies past them or
+    // past N_out reads zeros.)
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int kPastTile = 0x40000000;  // (a tile of any output is below 2^29 bytes)
     constexpr int NQC = EPI == kSwigluCkpt ? NQ : 1;
-    uint32_t gq[2][NQC][4], uq[2][NQC][4], sq[2][NQC][4];
-    auto load_ckpt = [&](int mb, uint32_t(&g8)[NQC][4], uint32_t(&u8)[NQC][4],
-                         uint32_t(&s2)[NQC][4]) {
-      const uint8_t* codes = reinterpret_cast<const uint8_t*>(gu);
+    u32x4 gq[2][NQC], uq[2][NQC];
+    uint32_t gsc[2][NQC], usc[2][NQC];
+    auto tile_rsrc = [&](const void* base, int pitch) {
+      return __builtin_amdgcn_make_buffer_rsrc(
+          (char*)base + (EPI == kSwigluCkpt ? static_cast<int64_t>(row_begin) * pitch : 0), 0,
+          EPI == kSwigluCkpt ? rows * pitch : 0, 0x00020000);
+    };
+    const __amdgpu_buffer_rsrc_t q_rsrc = tile_rsrc(gu, 2 * N_out);
+    const __amdgpu_buffer_rsrc_t s_rsrc = tile_rsrc(gu_scales, N_out / 8);
+    auto load_ckpt = [&](int mb, u32x4(&g8)[NQC], u32x4(&u8)[NQC], uint32_t(&gs)[NQC],
+                         uint32_t(&us)[NQC]) {
+      const int r = rowbase + mb * 32 + (lane & 31);
 #pragma unroll
       for (int q = 0; q < NQC; ++q) {
-        const int col = n0 + wn * WN + q * 32 + (lane & 28);
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int row = row_begin + rowbase + mb * 32 + 8 * g + 4 * half + (lane & 3);
-          const bool ok = row < row_begin + rows && col < N_out;
-          const int64_t gi = static_cast<int64_t>(row) * 2 * N_out + col;
-          g8[q][g] = ok ? *reinterpret_cast<const uint32_t*>(codes + gi) : 0u;
-          u8[q][g] = ok ? *reinterpret_cast<const uint32_t*>(codes + gi + N_out) : 0u;
-          s2[q][g] = ok ? gu_scales[gi >> 5] |
-                              (static_cast<uint32_t>(gu_scales[(gi + N_out) >> 5]) << 16)
-                        : 0u;
-        }
+        const int col = n0 + wn * WN + q * 32;
+        const int o = col < N_out ? r * 2 * N_out + col + 16 * half : kPastTile;
+        const int os = col < N_out ? (r * (N_out / 16) + col / 32) * 2 : kPastTile;
+        g8[q] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q_rsrc, o, 0, 0));
+        u8[q] = __builtin_bit_cast(u32x4,
+                                   __builtin_amdgcn_raw_buffer_load_b128(q_rsrc, o + N_out, 0, 0));
+        gs[q] = static_cast<unsigned short>(__builtin_amdgcn_raw_buffer_load_b16(s_rsrc, os, 0, 0));
+        us[q] = static_cast<unsigned short>(
+            __builtin_amdgcn_raw_buffer_load_b16(s_rsrc, os + N_out / 16, 0, 0));
       }
     };
-    if (EPI == kSwigluCkpt && nmb > 0) load_ckpt(0, gq[0], uq[0], sq[0]);
+    if (EPI == kSwigluCkpt && nmb > 0) load_ckpt(0, gq[0], uq[0], gsc[0], usc[0]);
     static_assert(NA + NB <= 4 * kMaxMB, "copy items fit the MFMA groups");
     switch (nmb) {
       case 5: run(std::integral_constant<int, 5>{}); break;
@@ -375,13 +389,86 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
     if (nmb > 0) {
       const int quad = lane & 3;
       const int row_end = row_begin + rows;
+      const __amdgpu_buffer_rsrc_t d_rsrc = tile_rsrc(dgu, 4 * N_out);
+      const __amdgpu_buffer_rsrc_t h_rsrc = tile_rsrc(hout, 2 * N_out);
+      if constexpr (EPI == kSwigluCkpt) {
+        // A loop over the row blocks, each moved to the first block's
+        // registers: unrolled, these some 700 instructions a block are fetched
+        // from memory at every launch (8192 x 1024 x 2048: 113 us; 777 rows of
+        // 320 x 192, 25 us).
+#pragma nounroll
+        for (int mb = 0; mb < nmb; ++mb) {
+          load_ckpt(mb + 1, gq[1], uq[1], gsc[1], usc[1]);  // (past the tile: zeros)
+          const int r = rowbase + mb * 32 + (lane & 31);
 #pragma unroll
-      for (int mb = 0; mb < kMaxMB; ++mb) {
+          for (int q = 0; q < NQ; ++q) {
+            const int col = n0 + wn * WN + q * 32;
+            const u32x4 lg = gq[0][q], lu = uq[0][q];
+            const float sg = __uint_as_float(gsc[0][q] << 16);
+            const float su = __uint_as_float(usc[0][q] << 16);
+            // Exchange with lane l ^ 32: word g then holds this lane's columns
+            // 8 g + 4 (l / 32) .. + 3, as accumulator registers 4 g .. 4 g + 3.
+            const auto g01 = __builtin_amdgcn_permlane32_swap(lg[0], lg[1], false, false);
+            const auto g23 = __builtin_amdgcn_permlane32_swap(lg[2], lg[3], false, false);
+            const auto u01 = __builtin_amdgcn_permlane32_swap(lu[0], lu[1], false, false);
+            const auto u23 = __builtin_amdgcn_permlane32_swap(lu[2], lu[3], false, false);
+            const uint32_t gw[4] = {g01[0], g23[0], g01[1], g23[1]};
+            const uint32_t uw[4] = {u01[0], u23[0], u01[1], u23[1]};
+            uint32_t w[3][4][2];  // dG, dU, H; run g; two columns a word
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              float gs[4], us[4], dg[4], du[4], hv[4];
+              ckpt_values4(gw[g], sg, gs);
+              ckpt_values4(uw[g], su, us);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float dh = acc[0][q][4 * g + i];
+                const float sig = __builtin_amdgcn_rcpf(
+                    1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * gs[i]));
+                const float silu = gs[i] * sig;
+                dg[i] = dh * us[i] * (sig + silu * (1.f - sig));
+                du[i] = dh * silu;
+                hv[i] = silu * us[i];
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                w[0][g][i] = cvt_bf16x2(dg[2 * i], dg[2 * i + 1]);
+                w[1][g][i] = cvt_bf16x2(du[2 * i], du[2 * i + 1]);
+                w[2][g][i] = cvt_bf16x2(hv[2 * i], hv[2 * i + 1]);
+              }
+            }
+            // Back to 16 adjacent columns a lane: two 16-byte stores each.
+            const bool ok = col < N_out;
+            const int og = ok ? (r * 2 * N_out + col + 16 * half) * 2 : kPastTile;
+            const int oh = ok ? (r * N_out + col + 16 * half) * 2 : kPastTile;
+#pragma unroll
+            for (int k3 = 0; k3 < 3; ++k3) {
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const auto a2 = __builtin_amdgcn_permlane32_swap(w[k3][p][0], w[k3][p + 2][0], false, false);
+                const auto b2 = __builtin_amdgcn_permlane32_swap(w[k3][p][1], w[k3][p + 2][1], false, false);
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    u32x4{static_cast<unsigned>(a2[0]), static_cast<unsigned>(b2[0]),
+                          static_cast<unsigned>(a2[1]), static_cast<unsigned>(b2[1])},
+                    k3 == 2 ? h_rsrc : d_rsrc,
+                    (k3 == 2 ? oh : og + k3 * 2 * N_out) + 16 * p, 0, 0);
+              }
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) {
+            gq[0][q] = gq[1][q], uq[0][q] = uq[1][q];
+            gsc[0][q] = gsc[1][q], usc[0][q] = usc[1][q];
+#pragma unroll
+            for (int m = 0; m + 1 < kMaxMB; ++m) acc[m][q] = acc[m + 1][q];
+          }
+        }
+      }
+#pragma unroll
+      for (int mb = 0; mb < (EPI == kSwigluCkpt ? 0 : kMaxMB); ++mb) {
         if (mb >= nmb) break;
         if (EPI == kSwigluSaved && mb + 1 < nmb)
           load_gu(mb + 1, gpre[(mb + 1) & 1], upre[(mb + 1) & 1]);
-        if (EPI == kSwigluCkpt && mb + 1 < nmb)
-          load_ckpt(mb + 1, gq[(mb + 1) & 1], uq[(mb + 1) & 1], sq[(mb + 1) & 1]);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
           const int col = n0 + wn * WN + q * 32 + (lane & 28);
@@ -399,17 +486,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
               continue;
             }
             // SiLU(g) = g s, s = 1 / (1 + exp(-g)); SiLU'(g) = s + SiLU(g) (1 - s).
-            float gs[4], us[4];
-            if (EPI == kSwigluCkpt) {
-              const uint32_t sc = sq[mb & 1][q < NQC ? q : 0][g];
-              ckpt_values4(gq[mb & 1][q < NQC ? q : 0][g], __uint_as_float(sc << 16), gs);
-              ckpt_values4(uq[mb & 1][q < NQC ? q : 0][g], __uint_as_float(sc & 0xffff0000u), us);
-            } else {
-              const float4 g4 = gpre[mb & 1][q < NQE ? q : 0][g];
-              const float4 u4 = upre[mb & 1][q < NQE ? q : 0][g];
-              gs[0] = g4.x, gs[1] = g4.y, gs[2] = g4.z, gs[3] = g4.w;
-              us[0] = u4.x, us[1] = u4.y, us[2] = u4.z, us[3] = u4.w;
-            }
+            const float4 g4 = gpre[mb & 1][q < NQE ? q : 0][g];
+            const float4 u4 = upre[mb & 1][q < NQE ? q : 0][g];
+            const float gs[4] = {g4.x, g4.y, g4.z, g4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
             float dg[4], du[4], hv[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

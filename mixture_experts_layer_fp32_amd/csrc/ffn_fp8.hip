@@ -15,12 +15,14 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "ckpt.h"
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 
@@ -83,11 +85,25 @@ __device__ __forceinline__ void store16(void* out, int64_t o, const float (&v)[1
     for (int i = 0; i < 8; ++i)
       w[i] = KIND == kOutF16
                  ? f16_sat_bits(v[2 * i]) | (f16_sat_bits(v[2 * i + 1]) << 16)
-                 : f32_to_bf16(v[2 * i]) | (static_cast<uint32_t>(f32_to_bf16(v[2 * i + 1])) << 16);
+                 : cvt_bf16x2(v[2 * i], v[2 * i + 1]);
     uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o);
     p[0] = make_uint4(w[0], w[1], w[2], w[3]);
     p[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+
+// Four adjacent outputs of a row.
+template <int KIND>
+__device__ __forceinline__ void store4(void* out, int64_t o, const f32x4& v) {
+  if (KIND == kOutF32)
+    *reinterpret_cast<f32x4*>(static_cast<float*>(out) + o) = v;
+  else if (KIND == kOutF16)
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) =
+        make_uint2(f16_sat_bits(v[0]) | (f16_sat_bits(v[1]) << 16),
+                   f16_sat_bits(v[2]) | (f16_sat_bits(v[3]) << 16));
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + o) =
+        make_uint2(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]));
 }
 
 // Tiles before each expert (s_pref) and first rows (s_off, clamped to
@@ -195,10 +211,9 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
     const int local = t - __builtin_amdgcn_readfirstlane(s_pref[expert]);
     const int cnt = seg_end - seg_beg;
     const int mt = (cnt + BM - 1) / BM;
-    const int chunk = (cnt + mt - 1) / mt;      // near-equal row blocks
     const int nb = local / mt, mb = local - nb * mt;
-    const int row_begin = seg_beg + mb * chunk;
-    const int rows = min(chunk, seg_end - row_begin);  // <= BM
+    const int row_begin = seg_beg + mb * BM;    // full row blocks, then the rest
+    const int rows = min(BM, seg_end - row_begin);
     if (rows <= 0) continue;  // (uniform)
     const int n0 = nb * BN_OUT;
     const int wr = wave >> 1, wc = wave & 1;
@@ -327,6 +342,9 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      // The copies past the last step have landed before the LDS is used again
+      // or the wave ends.
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       // ---- epilogue: lane group g = l / 16 holds columns 16 g .. + 15 of a
       // 64-column group, row l % 16 of each row block ----
       const int g = lane >> 4;
@@ -366,6 +384,192 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows an expert (decoding): the time is that of reading the weights of
+// the experts that are hit. A tile is up to 32 rows x 128 product columns
+// (gated: 64 gate columns and the matching 64 up columns); the four waves of a
+// workgroup cut K (wave w takes blocks w, w + 4, ...), load the weight and
+// activation fragments straight into registers, a whole block (16 KB of
+// weights) ahead of its use and without a barrier, and add their sums in LDS.
+// Two workgroups a CU keep 128 KB in flight there. One new token on eight
+// experts (7168 x 4096 codes each, 235 MB): 44 us, 5.3 TB/s, what a copy
+// reaches; 78 us with the large tiles.
+// ---------------------------------------------------------------------------
+constexpr int kSmallThreads = 256, kWaves = kSmallThreads / 64;
+constexpr int SM = 32, SN = 128;
+
+template <bool GATED, int KIND>
+__global__ __launch_bounds__(kSmallThreads, 2) void fp8_small_kernel(
+    const uint8_t* __restrict__ Xq, const float* __restrict__ Xs,
+    const int32_t* __restrict__ offsets, int n_experts, int64_t cap_rows,
+    const uint8_t* __restrict__ Wq, const float* __restrict__ Ws, void* __restrict__ out, int K,
+    int N) {
+  constexpr int SN_OUT = GATED ? SN / 2 : SN;
+  __shared__ f32x4 red[kWaves * 8 * (SM / 16) * 64];
+  __shared__ int s_tab[2 * (kMaxTableExperts + 1)];
+  int* s_pref = s_tab;
+  int* s_off = s_tab + kMaxTableExperts + 1;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int n_exp = offsets ? n_experts : 1;
+  const int nt = (N + SN_OUT - 1) / SN_OUT;
+  const int ncols = GATED ? 2 * N : N;
+  const int nk = (K + BK - 1) / BK;
+  const int nnb = (ncols + 127) / 128;
+  const bool k_tail = (K & 64) != 0;
+  if (wave == 0) tile_table(offsets, n_exp, cap_rows, SM, nt, tid, s_pref, s_off);
+  __syncthreads();
+  const int R = __builtin_amdgcn_readfirstlane(s_pref[n_exp]);
+  const int G8 = static_cast<int>(gridDim.x) / kXcds;
+  const int xcd = static_cast<int>(blockIdx.x) % kXcds, slot = static_cast<int>(blockIdx.x) / kXcds;
+  const int per = (R + kXcds - 1) / kXcds;
+  const int run_end = min((xcd + 1) * per, R);
+  for (int t = xcd * per + slot; t < run_end; t += G8) {
+    const int expert = find_expert(s_pref, n_exp, t, lane);
+    const int seg_beg = __builtin_amdgcn_readfirstlane(s_off[expert]);
+    const int seg_end = __builtin_amdgcn_readfirstlane(s_off[expert + 1]);
+    const int local = t - __builtin_amdgcn_readfirstlane(s_pref[expert]);
+    const int cnt = seg_end - seg_beg;
+    const int mt = (cnt + SM - 1) / SM;
+    const int chunk = (cnt + mt - 1) / mt;
+    const int nb = local / mt, mb = local - nb * mt;
+    const int row_begin = seg_beg + mb * chunk;
+    const int rows = min(chunk, seg_end - row_begin);  // <= SM
+    if (rows <= 0) continue;  // (uniform)
+    const int n0 = nb * SN_OUT;
+    // Rows past the tile's lie past the resource and read zeros.
+    const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(Xq + static_cast<int64_t>(row_begin) * K), 0, rows * K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(Wq + static_cast<int64_t>(expert) * ncols * K), 0, ncols * K, 0x00020000);
+    // First weight row of the two 64-column groups (a second group past N
+    // repeats the first and is not stored), and their scales.
+    int col[2];
+    const float* ws_row[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      col[q] = GATED ? q * N + n0 : n0 + (n0 + 64 * q < N ? 64 * q : 0);
+      ws_row[q] = Ws + (static_cast<int64_t>(expert) * nnb + col[q] / 128) * nk;
+    }
+    auto run = [&](auto nx_c) {
+      constexpr int NX = decltype(nx_c)::value;  // 16-row blocks
+      const int i = lane & 15, g = lane >> 4;
+      // A lane reads chunks g and 4 + g of a block of its row (the latter lie
+      // beyond the end of a last block of 64).
+      const int w_lane = (16 * (i >> 2) + (i & 3)) * K + 16 * g;
+      const int x_lane = i * K + 16 * g;
+      f32x4 acc[8][NX];
+#pragma unroll
+      for (int f = 0; f < 8; ++f)
+#pragma unroll
+        for (int x = 0; x < NX; ++x) acc[f][x] = f32x4{0.f, 0.f, 0.f, 0.f};
+      i32x8 wf[8], xf[2][NX];
+      float sx[2][NX], wsv[2] = {0.f, 0.f};
+      auto load = [&](__amdgpu_buffer_rsrc_t r, int voff, int soff, bool cut) {
+        const i32x4 lo =
+            __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0));
+        const i32x4 hi = __builtin_bit_cast(
+            i32x4,
+            __builtin_amdgcn_raw_buffer_load_b128(r, cut ? kOutOfRange : voff + 64, soff, 0));
+        return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      };
+      auto load_w = [&](int f, int kt) {
+        wf[f] = load(w_rsrc, w_lane, (col[f >> 2] + 4 * (f & 3)) * K + kt * BK,
+                     k_tail && kt == nk - 1);
+      };
+      auto load_x = [&](int b, int kt) {
+#pragma unroll
+        for (int x = 0; x < NX; ++x) {
+          xf[b][x] = load(x_rsrc, x_lane + 16 * x * K, kt * BK, k_tail && kt == nk - 1);
+          sx[b][x] = 16 * x + i < rows
+                         ? Xs[static_cast<int64_t>(kt) * cap_rows + row_begin + 16 * x + i]
+                         : 0.f;
+        }
+      };
+      // Step j is block wave + kWaves j; past this wave's last one the last
+      // block is loaded again and not used.
+      const int steps = (nk - wave + kWaves - 1) / kWaves;
+      if (steps > 0) {
+        load_x(0, wave);
+#pragma unroll
+        for (int f = 0; f < 8; ++f) load_w(f, wave);
+      }
+      auto step = [&](int j, auto b_c) {
+        constexpr int b = decltype(b_c)::value;
+        if ((j & 63) == 0) {  // 64 steps' weight scales, one a lane
+#pragma unroll
+          for (int q = 0; q < 2; ++q) wsv[q] = ws_row[q][min(wave + kWaves * (j + lane), nk - 1)];
+        }
+        const int next = min(wave + kWaves * (j + 1), nk - 1);
+        load_x(b ^ 1, next);
+        float s[2][NX];
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int x = 0; x < NX; ++x)
+            s[q][x] = sx[b][x] * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
+                                     __builtin_bit_cast(int, wsv[q]), j & 63));
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          f32x4 part[NX];
+#pragma unroll
+          for (int x = 0; x < NX; ++x) part[x] = mma(wf[f], xf[b][x]);
+          load_w(f, next);
+#pragma unroll
+          for (int x = 0; x < NX; ++x)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[f][x][r] = __builtin_fmaf(part[x][r], s[f >> 2][x], acc[f][x][r]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      };
+      for (int j = 0; j < steps; j += 2) {
+        step(j, std::integral_constant<int, 0>{});
+        if (j + 1 < steps) step(j + 1, std::integral_constant<int, 1>{});
+      }
+      // ---- sums of the waves, in order: [wave][fragment][row block][lane] ----
+#pragma unroll
+      for (int f = 0; f < 8; ++f)
+#pragma unroll
+        for (int x = 0; x < NX; ++x) red[((wave * 8 + f) * NX + x) * 64 + lane] = acc[f][x];
+      __syncthreads();
+      auto total = [&](int f, int x) {
+        f32x4 v = red[(f * NX + x) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) {
+          const f32x4 u = red[((w * 8 + f) * NX + x) * 64 + lane];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[r] += u[r];
+        }
+        return v;
+      };
+      // Wave w takes fragment w of each column group.
+#pragma unroll
+      for (int x = 0; x < NX; ++x) {
+        const int row = row_begin + 16 * x + i;
+        f32x4 v[2] = {total(wave, x), total(wave + 4, x)};
+        if (GATED) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[0][r] = silu_mul(v[0][r], v[1][r]);
+        }
+        if (16 * x + i < rows) {
+#pragma unroll
+          for (int q = 0; q < (GATED ? 1 : 2); ++q) {
+            const int c = n0 + 64 * q + 16 * g + 4 * wave;
+            if (c < N) store4<KIND>(out, static_cast<int64_t>(row) * N + c, v[q]);
+          }
+        }
+      }
+    };
+    if (rows <= 16)
+      run(std::integral_constant<int, 1>{});
+    else
+      run(std::integral_constant<int, 2>{});
+    // The sums have been read before the next tile's are written.
+    __syncthreads();
+  }
+}
+
 int num_cus() {
   static int cus = 0;
   if (cus == 0) {
@@ -382,13 +586,25 @@ template <bool GATED, int KIND>
 hipError_t launch_gemm(int n_experts, int64_t cap_rows, int K, int N, const void* xq,
                        const float* xs, const int32_t* offsets, const void* wq, const float* ws,
                        void* out, hipStream_t s) {
-  const int bn = GATED ? BN / 2 : BN;
-  const int64_t mt =
-      std::min<int64_t>(cap_rows, (cap_rows + BM - 1) / BM + (offsets ? n_experts : 0));
-  const int64_t tiles = mt * ((N + bn - 1) / bn);
+  const int n = offsets ? n_experts : 1;
   const int64_t cus = std::max<int64_t>(kXcds, num_cus() / kXcds * kXcds);
-  const int64_t g = std::min((tiles + kXcds - 1) / kXcds * kXcds, cus);
-  fp8_gemm_kernel<GATED, KIND><<<static_cast<unsigned>(g), kThreads, 0, s>>>(
+  // Small tiles read the weights once for each 32 rows, large ones for 256. Up
+  // to 32 rows an expert (of cap_rows: the counts are on the device) small
+  // ones win where K is long or large ones leave CUs idle, to 64 where those
+  // leave half of them idle. Measured, large against small: 32 experts of
+  // 7168 x 4096, 16 rows each, 184 : 168 us; 8 of 14336 x 4096, 64 rows each,
+  // 165 : 141 us (96: 185 : 201); 16 of 2048 x 1024, 4 rows, 17 : 13 us; but 16
+  // of 1024 x 4096 (256 large tiles), 15 : 18 us, 128 of 768 x 2048, 40 : 47 us.
+  const int64_t large =
+      std::min<int64_t>(cap_rows, n) * ((N + BN / (GATED ? 2 : 1) - 1) / (BN / (GATED ? 2 : 1)));
+  const bool small = (cap_rows <= 32 * n && (K >= 2048 || large < cus)) ||
+                     (cap_rows <= 64 * n && 2 * large <= cus);
+  const int bm = small ? SM : BM, bn = (small ? SN : BN) / (GATED ? 2 : 1);
+  const int64_t mt = std::min<int64_t>(cap_rows, cap_rows / bm + n);
+  const int64_t tiles = mt * ((N + bn - 1) / bn);
+  const int64_t g = std::min((tiles + kXcds - 1) / kXcds * kXcds, small ? 2 * cus : cus);
+  auto* k = small ? fp8_small_kernel<GATED, KIND> : fp8_gemm_kernel<GATED, KIND>;
+  k<<<static_cast<unsigned>(g), small ? kSmallThreads : kThreads, 0, s>>>(
       static_cast<const uint8_t*>(xq), xs, offsets, n_experts, cap_rows,
       static_cast<const uint8_t*>(wq), ws, out, K, N);
   return hipGetLastError();
