@@ -10,8 +10,9 @@
 // then holds four output columns of one row, so xs is one value per lane and
 // row block, ws one scalar per 64 columns, and a scale costs no more than its
 // FMA. The FMAs (4 per instruction, 16 cycles of vector issue) run beside the
-// matrix core's 32 cycles: a wave issues an instruction's FMAs two
-// instructions later, and two waves share a SIMD.
+// matrix core's 32 cycles (a loop of both alone loses 2 % to a loop without
+// the FMAs): a wave issues an instruction's FMAs three instructions later, and
+// two waves share a SIMD.
 #include <algorithm>
 #include <type_traits>
 
@@ -162,8 +163,14 @@ __device__ __forceinline__ int find_expert(const int* s_pref, int n_exp, int t, 
 // matching 128 up columns), eight waves, wave (wr, wc) a quarter of the rows
 // x 128 columns: 128 accumulators a lane. Both operands of a K step (one
 // block of 128) are copied to LDS one step ahead (2 x 64 KB), with the rows'
-// 256 scales. One workgroup per CU works through its share of the tile list,
-// which is dealt to the XCDs in contiguous runs.
+// 256 scales; the LDS holds no third slot. One workgroup per CU works through
+// its share of the tile list, which is dealt to the XCDs in contiguous runs.
+// Mixtral-style gate_up (16384 rows, 4096 x 28672): 1.77 ms, 2.17 PFLOP/s,
+// against 2.66 that a library's plain FP8 product of 8192^3 reaches and 3.7 of
+// a loop of the instruction alone (random operands: the clock falls to
+// 2.0 GHz); its steps take 1.9 us, 1.1 of them matrix instructions: what is
+// left is the wait for copies that come one step ahead, and the reads that
+// start a step.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 512;
 constexpr int BM = 256, BN = 256, BK = 128;
@@ -199,47 +206,115 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
   const int xcd = static_cast<int>(blockIdx.x) % kXcds, slot = static_cast<int>(blockIdx.x) / kXcds;
   const int per = (R + kXcds - 1) / kXcds;
   const int run_end = min((xcd + 1) * per, R);
+  int t = xcd * per + slot;
+  if (t >= run_end) return;  // (the whole workgroup)
   const unsigned lds0 = (unsigned)(uintptr_t)(lds_u8*)smem;
-  for (int t = xcd * per + slot; t < run_end; t += G8) {
-    // Lane-derived values are computed per tile (not hoisted out of the loop).
-    int lane_t = tid & 63;
-    asm volatile("" : "+v"(lane_t));
-    const int lane = lane_t;
-    const int expert = find_expert(s_pref, n_exp, t, lane);
-    const int seg_beg = __builtin_amdgcn_readfirstlane(s_off[expert]);
-    const int seg_end = __builtin_amdgcn_readfirstlane(s_off[expert + 1]);
-    const int local = t - __builtin_amdgcn_readfirstlane(s_pref[expert]);
-    const int cnt = seg_end - seg_beg;
-    const int mt = (cnt + BM - 1) / BM;
-    const int nb = local / mt, mb = local - nb * mt;
-    const int row_begin = seg_beg + mb * BM;    // full row blocks, then the rest
-    const int rows = min(BM, seg_end - row_begin);
-    if (rows <= 0) continue;  // (uniform)
-    const int n0 = nb * BN_OUT;
-    const int wr = wave >> 1, wc = wave & 1;
+  const int lane = tid & 63;
+  const int wr = wave >> 1, wc = wave & 1;
 
-    // Rows past the tile's (weight rows past the expert's) lie past the
-    // resource and read zeros; a gate column past N reads up columns, whose
-    // results are not stored.
-    const __amdgpu_buffer_rsrc_t x_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(Xq + static_cast<int64_t>(row_begin) * K), 0, rows * K, 0x00020000);
-    const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(Wq + static_cast<int64_t>(expert) * ncols * K), 0, ncols * K, 0x00020000);
-    // Copies: wave w takes the 8-row groups w + 8 i of each operand (rows
-    // 64 i further on for the next i; gated: up columns from i = 2); lane ->
-    // row l / 8, LDS chunk l % 8.
-    const int crow = 8 * wave + (lane >> 3);
-    const int xc = (lane & 7) ^ swz(crow & 15), wk = (lane & 7) ^ swz(w_place(crow));
-    const int x_voff = crow * K + 16 * xc;
-    const int w_voff = (n0 + crow) * K + 16 * wk;
-    const int s_voff = 4 * (64 * (wave & 3) + lane);
-    // Weight scales of the wave's column groups.
-    const float* ws_row[2];
+  struct Tile {
+    int expert, row, rows, n0;
+  };
+  auto decode = [&](int tile) {
+    Tile d;
+    d.expert = find_expert(s_pref, n_exp, tile, lane);
+    const int seg_beg = __builtin_amdgcn_readfirstlane(s_off[d.expert]);
+    const int seg_end = __builtin_amdgcn_readfirstlane(s_off[d.expert + 1]);
+    const int local = tile - __builtin_amdgcn_readfirstlane(s_pref[d.expert]);
+    const int mt = (seg_end - seg_beg + BM - 1) / BM;
+    const int nb = local / mt, mb = local - nb * mt;
+    d.row = seg_beg + mb * BM;  // full row blocks, then the rest
+    d.rows = min(BM, seg_end - d.row);
+    d.n0 = nb * BN_OUT;
+    return d;
+  };
+  // Weight scales of the wave's two 64-column groups, 64 steps from kt on, one
+  // a lane.
+  auto load_ws = [&](const Tile& d, int kt, float (&v)[2]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const int c = GATED ? q * N + n0 + 64 * wc : n0 + 128 * wc + 64 * q;
-      ws_row[q] = Ws + (static_cast<int64_t>(expert) * nnb + min(c / 128, nnb - 1)) * nk;
+      const int c = GATED ? q * N + d.n0 + 64 * wc : d.n0 + 128 * wc + 64 * q;
+      v[q] = Ws[(static_cast<int64_t>(d.expert) * nnb + min(c / 128, nnb - 1)) * nk +
+                min(kt + lane, nk - 1)];
     }
+  };
+
+  // Copies: wave w takes the 8-row groups w + 8 i of each operand (rows 64 i
+  // further on for the next i; gated: up columns from i = 2); lane -> row
+  // l / 8, LDS chunk l % 8. Rows past the tile's (weight rows past the
+  // expert's) lie past the resources and read zeros, as does the half that a
+  // short last block lacks (its offsets are out of range); a gate column past
+  // N reads up columns, whose results are not stored.
+  const int crow = 8 * wave + (lane >> 3);
+  const int xc = (lane & 7) ^ swz(crow & 15), wk = (lane & 7) ^ swz(w_place(crow));
+  const int x_voff = crow * K + 16 * xc, w_voff = crow * K + 16 * wk;
+  const int s_voff = 4 * (64 * (wave & 3) + lane);
+  auto rsrc = [&](const void* base, int bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(base);
+    const uint64_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a)));
+    const uint64_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32)));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(lo | hi << 32), 0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+  };
+  // Where the next step to be copied lies: its tile's operands, the step kc.
+  struct Copy {
+    const uint8_t *x, *w;
+    const float* s;
+    int x_bytes, w_bytes, s_bytes, kc;
+  };
+  auto copy_from = [&](const Tile& d, bool any) {
+    Copy c;
+    c.x = Xq + static_cast<int64_t>(d.row) * K;
+    c.w = Wq + (static_cast<int64_t>(d.expert) * ncols + d.n0) * K;
+    c.s = Xs + d.row;
+    c.x_bytes = any ? d.rows * K : 0;
+    c.w_bytes = any ? (ncols - d.n0) * K : 0;
+    c.s_bytes = any ? d.rows * 4 : 0;
+    c.kc = 0;
+    return c;
+  };
+  auto copy_scales = [&](const Copy& c, int sl) {
+    dma4(rsrc(c.s, c.s_bytes), s_voff, 0,
+         lds0 + kOffS + sl * BM * 4 + (wave & 3) * 256);
+  };
+  // Copy i: 0 .. 3 weights, 4 .. 7 activations, into slot sl.
+  auto copy = [&](const Copy& c, int i, int sl) {
+    const bool cut = k_tail && c.kc == nk - 1;
+    if (i < 4)
+      dma16(rsrc(c.w, c.w_bytes),
+            (cut && wk >= 4 ? kOutOfRange : w_voff + c.kc * BK) +
+                (GATED && i >= 2 ? N + 64 * (i - 2) : 64 * i) * K,
+            0, lds0 + kOffW + sl * kTile + (wave + 8 * i) * 1024);
+    else
+      dma16(rsrc(c.x, c.x_bytes),
+            (cut && xc >= 4 ? kOutOfRange : x_voff + c.kc * BK) + 64 * (i - 4) * K, 0,
+            lds0 + sl * kTile + (wave + 8 * (i - 4)) * 1024);
+  };
+  auto advance = [&](Copy& c) {
+    c.s += cap_rows;
+    ++c.kc;
+  };
+
+  // A tile's first step is copied during the last one of the tile before it,
+  // so that the tiles follow one another without a gap: `first` is the slot of
+  // the tile's step 0.
+  Tile cur = decode(t);
+  int first = 0;
+  float ws_next[2];
+  load_ws(cur, 0, ws_next);
+  Copy c = copy_from(cur, true);
+  {
+    copy_scales(c, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) copy(c, i, 0);
+    advance(c);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  while (true) {
+    const bool has_next = t + G8 < run_end;
+    const Tile next = has_next ? decode(t + G8) : cur;
+    float wsv[2] = {ws_next[0], ws_next[1]};
+    load_ws(next, 0, ws_next);
 
     auto run = [&](auto nxb_c) {
       constexpr int NX = decltype(nxb_c)::value;  // 16-row blocks per wave
@@ -251,15 +326,17 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
         for (int b = 0; b < 4; ++b)
 #pragma unroll
           for (int x = 0; x < NX; ++x) acc[q][b][x] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // LDS addresses of fragments: row (l % 16), chunks l / 16 and 4 + l / 16.
+      // LDS addresses of fragments: row (l % 16), chunks 2 (l / 16) and + 1
+      // (the lanes that are served together then meet no bank twice; with
+      // chunks l / 16 and 4 + l / 16 half of the LDS cycles were conflicts).
       int x_addr[2], w_addr[2];
+      const int i16 = lane & 15, g = lane >> 4;
       {
-        const int i = lane & 15, g = lane >> 4;
-        const int wrow = (GATED ? 64 * wc : 128 * wc) + 16 * (i >> 2) + (i & 3);
+        const int wrow = (GATED ? 64 * wc : 128 * wc) + 16 * (i16 >> 2) + (i16 & 3);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          x_addr[p] = (rowbase + i) * 128 + (((g + 4 * p) ^ swz(i)) << 4);
-          w_addr[p] = kOffW + wrow * 128 + (((g + 4 * p) ^ swz(i)) << 4);
+          x_addr[p] = (rowbase + i16) * 128 + (((2 * g + p) ^ swz(i16)) << 4);
+          w_addr[p] = kOffW + wrow * 128 + (((2 * g + p) ^ swz(i16)) << 4);
         }
       }
       auto frag = [&](int base, const int(&a)[2]) {
@@ -267,42 +344,13 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
         const int4 hi = *reinterpret_cast<const int4*>(smem + base + a[1]);
         return i32x8{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       };
-      // Copies of step kt: x_at, w_at are the lane's offsets in it (out of
-      // range past the last step and in the half that a short last block
-      // lacks, which then reads zeros).
-      int x_at, w_at;
-      auto copy_begin = [&](int kt) {
-        const bool cut = k_tail && kt == nk - 1;
-        x_at = kt >= nk || (cut && xc >= 4) ? kOutOfRange : x_voff + kt * BK;
-        w_at = kt >= nk || (cut && wk >= 4) ? kOutOfRange : w_voff + kt * BK;
-        const __amdgpu_buffer_rsrc_t s_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            (void*)(Xs + static_cast<int64_t>(min(kt, nk - 1)) * cap_rows + row_begin), 0,
-            rows * 4, 0x00020000);
-        dma4(s_rsrc, s_voff, 0, lds0 + kOffS + (kt & 1) * BM * 4 + (wave & 3) * 256);
-      };
-      // Copy i (0 .. 3 weights, then NX of the activations).
-      auto copy = [&](int i, int kt) {
-        const int sl = (kt & 1) * kTile;
-        if (i < 4)
-          dma16(w_rsrc, w_at + (GATED && i >= 2 ? N + 64 * (i - 2) : 64 * i) * K, 0,
-                lds0 + kOffW + sl + (wave + 8 * i) * 1024);
-        else if (i - 4 < NX)
-          dma16(x_rsrc, x_at + 64 * (i - 4) * K, 0, lds0 + sl + (wave + 8 * (i - 4)) * 1024);
-      };
-      copy_begin(0);
-#pragma unroll
-      for (int i = 0; i < 4 + NX; ++i) copy(i, 0);
-      float wsv[2] = {0.f, 0.f};
       for (int kt = 0; kt < nk; ++kt) {
-        if ((kt & 63) == 0) {  // 64 steps' weight scales, one a lane
-#pragma unroll
-          for (int q = 0; q < 2; ++q) wsv[q] = ws_row[q][min(kt + lane, nk - 1)];
-        }
-        // This step's copies are done, and after the barrier every wave's,
-        // and every wave has read what the next copies overwrite.
-        asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-        const int sl = (kt & 1) * kTile;
-        copy_begin(kt + 1);
+        if (kt > 0 && (kt & 63) == 0) load_ws(cur, kt, wsv);
+        // Every wave's copies of this step are done (each has waited for its
+        // own), and every wave has read what the next copies overwrite.
+        asm volatile("s_barrier" ::: "memory");
+        const int slot_k = (first + kt) & 1, sl = slot_k * kTile;
+        if (kt + 1 == nk) c = copy_from(next, has_next);
         i32x8 xf[NX], wf[2];
         float s[2][NX];
 #pragma unroll
@@ -311,13 +359,14 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
 #pragma unroll
         for (int x = 0; x < NX; ++x) {
           const float sx = *reinterpret_cast<const float*>(
-              smem + kOffS + (kt & 1) * BM * 4 + (rowbase + 16 * x + (lane & 15)) * 4);
+              smem + kOffS + slot_k * BM * 4 + (rowbase + 16 * x + i16) * 4);
 #pragma unroll
           for (int q = 0; q < 2; ++q)
             s[q][x] = sx * __builtin_bit_cast(float, __builtin_amdgcn_readlane(
                                                          __builtin_bit_cast(int, wsv[q]), kt & 63));
         }
-        constexpr int LAG = 2, M = 8 * NX;
+        copy_scales(c, slot_k ^ 1);
+        constexpr int LAG = 3, M = 8 * NX;
         f32x4 part[LAG + 1];
 #pragma unroll
         for (int m = 0; m < M + LAG; ++m) {
@@ -328,7 +377,13 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
                 const int q = (f + 1) >> 2, b = (f + 1) & 3;
                 wf[(f + 1) & 1] = frag(sl + (q * (GATED ? 128 : 64) + 4 * b) * 128, w_addr);
               }
-              copy(f, kt + 1);
+              // The next step's copies early in this one, two at a time (all at
+              // once hold up the reads; spread over the step they come late:
+              // 5 to 20 % slower either way).
+              if (f < 4) {
+                copy(c, 2 * f, slot_k ^ 1);
+                copy(c, 2 * f + 1, slot_k ^ 1);
+              }
             }
             part[m % (LAG + 1)] = mma(wf[f & 1], xf[x]);
           }
@@ -341,21 +396,19 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
           }
           __builtin_amdgcn_sched_barrier(0);
         }
+        advance(c);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       }
-      // The copies past the last step have landed before the LDS is used again
-      // or the wave ends.
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       // ---- epilogue: lane group g = l / 16 holds columns 16 g .. + 15 of a
       // 64-column group, row l % 16 of each row block ----
-      const int g = lane >> 4;
 #pragma unroll
       for (int x = 0; x < NX; ++x) {
-        const int r = rowbase + 16 * x + (lane & 15);
-        if (r < rows) {
-          const int64_t o = static_cast<int64_t>(row_begin + r) * N;
+        const int r = rowbase + 16 * x + i16;
+        if (r < cur.rows) {
+          const int64_t o = static_cast<int64_t>(cur.row + r) * N;
           float v[16];
           if (GATED) {
-            const int c = n0 + 64 * wc + 16 * g;
+            const int c = cur.n0 + 64 * wc + 16 * g;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               v[i] = silu_mul(acc[0][i >> 2][x][i & 3], acc[1][i >> 2][x][i & 3]);
@@ -363,7 +416,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
           } else {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const int c = n0 + 128 * wc + 64 * q + 16 * g;
+              const int c = cur.n0 + 128 * wc + 64 * q + 16 * g;
 #pragma unroll
               for (int i = 0; i < 16; ++i) v[i] = acc[q][i >> 2][x][i & 3];
               if (c < N) store16<KIND>(out, o + c, v);
@@ -372,15 +425,17 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
         }
       }
     };
-    const int nblk = (rows + 15) / 16;
+    const int nblk = (cur.rows + 15) / 16;
     switch ((nblk + 3) / 4) {
       case 4: run(std::integral_constant<int, 4>{}); break;
       case 3: run(std::integral_constant<int, 3>{}); break;
       case 2: run(std::integral_constant<int, 2>{}); break;
       default: run(std::integral_constant<int, 1>{}); break;
     }
-    // Every wave is done with this tile's LDS before the next tile's copies.
-    __syncthreads();
+    if (!has_next) break;
+    first = (first + nk) & 1;
+    cur = next;
+    t += G8;
   }
 }
 
