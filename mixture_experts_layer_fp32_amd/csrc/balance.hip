@@ -52,17 +52,21 @@ __device__ __forceinline__ float group_sum(float v) {
   return group_reduce<L>(v, [](float a, float b) { return a + b; });
 }
 
-// p of one token: e[i] = exp(z - max) on return, the factor 1 / sum returned.
-// A row of -inf alone gives p = 0.
+// A token's logits (-inf past E), loaded without branches.
 template <typename T, int L, int NI>
-__device__ __forceinline__ float softmax_row(const T* __restrict__ z, int E, int l,
-                                             float (&e)[NI]) {
+__device__ __forceinline__ void load_row(const T* __restrict__ z, int E, int l, float (&e)[NI]) {
+#pragma unroll
+  for (int i = 0; i < NI; ++i) e[i] = load_logit(z + min(l + L * i, E - 1));
+#pragma unroll
+  for (int i = 0; i < NI; ++i) e[i] = l + L * i < E ? e[i] : -INFINITY;
+}
+// p of one token: its logits in e, exp(z - max) on return, the factor 1 / sum
+// returned. A row of -inf alone gives p = 0.
+template <int L, int NI>
+__device__ __forceinline__ float softmax_row(float (&e)[NI]) {
   float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    e[i] = l + L * i < E ? load_logit(z + l + L * i) : -INFINITY;
-    m = fmaxf(m, e[i]);
-  }
+  for (int i = 0; i < NI; ++i) m = fmaxf(m, e[i]);
   m = group_max<L>(m);
   if (m == -INFINITY) m = 0.f;  // (fmaxf drops NaN; exp(NaN) brings it back)
   float s = 0.f;
@@ -113,13 +117,26 @@ __global__ __launch_bounds__(kLossThreads) void balance_part_kernel(
   const int64_t t1 = static_cast<int64_t>(Tn) * (blockIdx.x + 1) / parts;
   float acc[NI] = {};
   int tok = 0;
-  for (int64_t t = t0 + g; t < t1; t += G) {
-    if (mask && mask[t] == 0) continue;  // (uniform in the token's lanes)
-    float e[NI];
-    const float r = softmax_row<T, L, NI>(logits + t * E, E, l, e);
+  // Two tokens at a time (fewer registers: one), logits and mask in flight
+  // together; a token that does not count is read and left out.
+  constexpr int U = NI <= 8 ? 2 : 1;
+  for (int64_t t = t0 + g; t < t1; t += U * G) {
+    float e[U][NI];
+    bool on[U];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) acc[i] += e[i] * r;
-    tok += l == 0;
+    for (int u = 0; u < U; ++u) {
+      const int64_t tu = min(t + u * G, t1 - 1);
+      load_row<T, L, NI>(logits + tu * E, E, l, e[u]);
+      on[u] = t + u * G < t1 && !(mask && mask[tu] == 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (on[u]) {  // (uniform in the token's lanes)
+        const float r = softmax_row<L, NI>(e[u]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i] += e[u][i] * r;
+        tok += l == 0;
+      }
   }
   for (int64_t q = t0 * k + tid; q < t1 * k; q += kLossThreads) {
     const int e = topk[q];
@@ -239,10 +256,10 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
     f[i] = l + L * i < E ? static_cast<float>(scale * counts[l + L * i]) : 0.f;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G;
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * G + tid / L; t < Tn; t += step) {
-    float d[NI] = {};
+    float d[NI] = {}, e[NI];
+    load_row<T, L, NI>(logits + t * E, E, l, e);
     if (!(mask && mask[t] == 0)) {
-      float e[NI];
-      const float r = softmax_row<T, L, NI>(logits + t * E, E, l, e);
+      const float r = softmax_row<L, NI>(e);
       float dot = 0.f;
 #pragma unroll
       for (int i = 0; i < NI; ++i) dot += e[i] * f[i];
@@ -259,9 +276,14 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
           if (x == l + L * i) d[i] += v;
       }
     }
+    if (E == L * NI) {
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (l + L * i < E) dlogits[t * E + l + L * i] = d[i];
+      for (int i = 0; i < NI; ++i) dlogits[t * E + l + L * i] = d[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (l + L * i < E) dlogits[t * E + l + L * i] = d[i];
+    }
   }
 }
 
@@ -277,7 +299,9 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
 // NaN.)
 // ---------------------------------------------------------------------------
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
@@ -330,23 +354,29 @@ template <int KC, int MT, int THREADS>
 __global__ __launch_bounds__(THREADS, 1) void router_dx_kernel(
     const float* __restrict__ dz, const float* __restrict__ W, float* __restrict__ dx, int T,
     int E, int D, int cols, int col_tiles, int accumulate) {
-  constexpr int NM = MT / 32, NW = THREADS / 64, NK = KC / 16, kPlane = MT * KC * 2;
+  constexpr int NM = MT / 32, NW = THREADS / 64, NK = KC / 16;
+  constexpr int kPlane = MT * (KC < 64 ? 64 : KC) * 2;  // (rows of 64 at least)
   __shared__ __attribute__((aligned(16))) unsigned char smem[3 * kPlane];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x / col_tiles) * MT;
   const int c_begin = static_cast<int>(blockIdx.x % col_tiles) * cols;
   const int c_end = min(c_begin + cols, D);
   const int half = lane >> 5, l31 = lane & 31;
+  // dz's rows of this workgroup; tokens past T read zeros.
+  const __amdgpu_buffer_rsrc_t z_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(dz + t0 * E), 0, static_cast<int>(min(static_cast<int64_t>(MT), T - t0)) * E * 4,
+      0x00020000);
   for (int e0 = 0; e0 < E; e0 += KC) {
     if (e0 > 0) __syncthreads();
     for (int q = tid; q < MT * (KC / 8); q += THREADS) {
       const int r = q / (KC / 8), c = q % (KC / 8);
+      // (experts past E: the next token's values, replaced by zeros)
+      const int at = (r * E + e0 + 8 * c) * 4;
+      const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(z_rsrc, at, 0, 0));
+      const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(z_rsrc, at + 16, 0, 0));
       float f[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int e = e0 + 8 * c + j;
-        f[j] = t0 + r < T && e < E ? dz[(t0 + r) * E + e] : 0.f;
-      }
+      for (int j = 0; j < 8; ++j) f[j] = e0 + 8 * c + j < E ? (j < 4 ? lo[j & 3] : hi[j & 3]) : 0.f;
       uint4 p[3];
       split8(f, p);
       const int o = (c >> 3) * (MT * 128) + r * 128 +
@@ -438,6 +468,7 @@ struct DwShape {
   static constexpr int NRA = ME == 128 ? 3 : 1;             // row blocks of dz
   static constexpr int MP = ME == 128 ? 2 : 1, MQ = ME == 128 ? 2 : 1;
   static constexpr int SLOT = (NRA + NPB) * BK * ROW;
+  static constexpr int SLOTS = kF32 && ME == 128 ? 1 : 2;   // two workgroups a CU
 };
 __device__ __forceinline__ int t_off(int k, int col) {
   return k * 256 + (((col >> 3) ^ ((k & 3) << 2)) << 4) + ((col & 7) << 1);
@@ -446,9 +477,9 @@ __device__ __forceinline__ int t_off(int k, int col) {
 template <typename TX, int ME>
 __global__ __launch_bounds__(kThreads, 2) void router_dw_kernel(
     const float* __restrict__ dz, const TX* __restrict__ x, float* __restrict__ C, int T, int E,
-    int D, int parts, int vec) {
+    int D, int parts) {
   using S = DwShape<TX, ME>;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * S::SLOT];
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[S::SLOTS * S::SLOT];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int nt = (D + S::BQ - 1) / S::BQ;
   const int m0 = static_cast<int>(blockIdx.x / nt) * ME, n0 = static_cast<int>(blockIdx.x % nt) * S::BQ;
@@ -458,41 +489,48 @@ __global__ __launch_bounds__(kThreads, 2) void router_dw_kernel(
   // dz: thread -> token tid / 8, ME / 8 adjacent experts; x: token tid / 16
   // (and + 16), 8 adjacent columns.
   constexpr int NE = ME / 8;
-  float fz[NE], fx[S::kF32 ? 16 : 1];
-  uint4 ux[2];
+  struct Step {
+    float z[NE], x[S::kF32 ? 16 : 1];
+    uint4 u[2];
+  };
   const int zt = tid >> 3, ze = (tid & 7) * NE, xt = tid >> 4, xc = (tid & 15) * 8;
-  auto fetch = [&](int64_t kb) {
-    const int64_t t = kb + zt;
-    const float* p = dz + t * E + m0 + ze;
+  // (Tokens past the part read zeros; experts past E and columns past D read
+  // what follows in memory: their sums are not stored.)
+  auto fetch = [&](int64_t kb, Step& st) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(S::BK), k1 - kb));
+    const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(dz + kb * E), 0, n * E * 4, 0x00020000);
+    const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(x + kb * D), 0, n * D * static_cast<int>(sizeof(TX)), 0x00020000);
+    const int z_at = (zt * E + m0 + ze) * 4;
 #pragma unroll
     for (int j = 0; j < NE; j += 4) {
-      if (vec) {
-        const float4 v = t < k1 && m0 + ze + j < E ? *reinterpret_cast<const float4*>(p + j)
-                                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-        fz[j] = v.x, fz[j + 1] = v.y, fz[j + 2] = v.z, fz[j + 3] = v.w;
-      } else {
+      const f32x4 v = __builtin_bit_cast(
+          f32x4, __builtin_amdgcn_raw_buffer_load_b128(zr, z_at + 4 * j, 0, 0));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fz[j + i] = t < k1 && m0 + ze + j + i < E ? p[j + i] : 0.f;
-      }
+      for (int i = 0; i < 4; ++i) st.z[j + i] = v[i];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t tx = kb + xt + 16 * i;
-      const bool ok = tx < k1 && n0 + xc < D;
-      const TX* q = x + tx * D + n0 + xc;
+      const int x_at = ((xt + 16 * i) * D + n0 + xc) * static_cast<int>(sizeof(TX));
+      const u32x4 lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, x_at, 0, 0));
       if constexpr (S::kF32) {
-        const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float4 a = ok ? reinterpret_cast<const float4*>(q)[0] : z4;
-        const float4 b = ok ? reinterpret_cast<const float4*>(q)[1] : z4;
-        const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const u32x4 hi = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(xr, x_at + 16, 0, 0));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) fx[8 * i + j] = v[j];
+        for (int j = 0; j < 4; ++j) {
+          st.x[8 * i + j] = __uint_as_float(lo[j]);
+          st.x[8 * i + 4 + j] = __uint_as_float(hi[j]);
+        }
       } else {
-        ux[i] = ok ? *reinterpret_cast<const uint4*>(q) : make_uint4(0, 0, 0, 0);
+        st.u[i] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
     }
   };
-  auto put = [&](int slot) {
+  auto put = [&](int slot, const Step& st) {
+    const auto& fz = st.z;
+    const auto& fx = st.x;
+    const auto& ux = st.u;
     unsigned char* base = smem + slot * S::SLOT;
     if constexpr (ME == 128) {
 #pragma unroll
@@ -552,15 +590,14 @@ __global__ __launch_bounds__(kThreads, 2) void router_dw_kernel(
     for (int j = 0; j < S::MQ; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  if (k0 < k1) {
-    fetch(k0);
-    put(0);
-  }
-  int slot = 0;
-  for (int64_t kb = k0; kb < k1; kb += S::BK, slot ^= 1) {
-    __syncthreads();
-    const bool more = kb + S::BK < k1;
-    if (more) fetch(kb + S::BK);
+  // Steps are fetched two ahead: step i's registers are free once it is in LDS.
+  const int64_t steps = (k1 - k0 + S::BK - 1) / S::BK;
+  Step st[2];
+  if (steps > 0) fetch(k0, st[0]);
+  if (steps > 1) fetch(k0 + S::BK, st[1]);
+  if (steps > 0) put(0, st[0]);
+  if (steps > 2) fetch(k0 + 2 * S::BK, st[0]);
+  auto products = [&](int slot) {
     const unsigned char* za = smem + slot * S::SLOT;
     const unsigned char* xb = za + S::NRA * S::BK * S::ROW;
 #pragma unroll
@@ -589,7 +626,21 @@ __global__ __launch_bounds__(kThreads, 2) void router_dw_kernel(
           }
         }
     }
-    if (more) put(slot ^ 1);
+  };
+  // Step i from slot i % 2, step i + 1 put beside it (or, with one slot, in its
+  // place behind a second barrier); nxt holds step i + 1.
+  auto step = [&](int64_t i, Step& nxt) {
+    __syncthreads();
+    products(S::SLOTS == 2 ? static_cast<int>(i & 1) : 0);
+    if (i + 1 < steps) {
+      if (S::SLOTS == 1) __syncthreads();
+      put(S::SLOTS == 2 ? static_cast<int>((i + 1) & 1) : 0, nxt);
+      if (i + 3 < steps) fetch(k0 + (i + 3) * S::BK, nxt);
+    }
+  };
+  for (int64_t i = 0; i < steps; i += 2) {
+    step(i, st[1]);
+    if (i + 1 < steps) step(i + 1, st[0]);
   }
 #pragma unroll
   for (int i = 0; i < S::MP; ++i)
@@ -603,20 +654,37 @@ __global__ __launch_bounds__(kThreads, 2) void router_dw_kernel(
       }
 }
 
+// The parts of dW added up: 64 float4 of it a workgroup, wave w the parts w,
+// w + 4, ... in order with eight loads in flight, then the waves in order.
 __global__ __launch_bounds__(kThreads) void router_dense_sum_kernel(const float4* __restrict__ part,
                                                                     float4* __restrict__ out,
                                                                     int64_t n4, int parts) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= n4) return;
-  float4 v = part[i];
-  for (int p = 1; p < parts; ++p) {
-    const float4 w = part[p * n4 + i];
-    v.x += w.x;
-    v.y += w.y;
-    v.z += w.z;
-    v.w += w.w;
+  __shared__ float4 s_sum[kThreads];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 64 + lane;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [](float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+  };
+  if (i < n4)
+    for (int p0 = wave; p0 < parts; p0 += 32) {
+      float4 w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = part[min(p0 + 4 * j, parts - 1) * n4 + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (p0 + 4 * j < parts) add(v, w[j]);
+    }
+  s_sum[threadIdx.x] = v;
+  __syncthreads();
+  if (wave == 0 && i < n4) {
+#pragma unroll
+    for (int w = 1; w < 4; ++w) add(v, s_sum[64 * w + lane]);
+    out[i] = v;
   }
-  out[i] = v;
 }
 
 // Workgroups of the forward: some 8 K logits each, at most kMaxParts.
@@ -705,7 +773,10 @@ hipError_t dense_bwd(int T, int E, int D, const float* dlogits, const TX* x, con
           dlogits, w, dx, T, E, D, cols, ct, accumulate);
     };
     using std::integral_constant;
-    if (E <= 64)
+    if (E <= 16)
+      launch(integral_constant<int, 16>{}, integral_constant<int, 128>{},
+             integral_constant<int, 512>{});
+    else if (E <= 64)
       launch(integral_constant<int, 64>{}, integral_constant<int, 128>{},
              integral_constant<int, 512>{});
     else if (E <= 128)
@@ -720,15 +791,13 @@ hipError_t dense_bwd(int T, int E, int D, const float* dlogits, const TX* x, con
     const int parts = T > 0 ? dense_parts(T, E, D) : 1, me = dw_experts(E);
     const dim3 grid(static_cast<unsigned>((E + me - 1) / me * ((D + 127) / 128)),
                     static_cast<unsigned>(parts));
-    const int vec = E % 4 == 0 && (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0;
     auto* k = me == 32 ? router_dw_kernel<TX, 32> : router_dw_kernel<TX, 128>;
-    k<<<grid, kThreads, 0, s>>>(dlogits, x, parts > 1 ? ws : dw, T, E, D, parts, vec);
+    k<<<grid, kThreads, 0, s>>>(dlogits, x, parts > 1 ? ws : dw, T, E, D, parts);
     e = hipGetLastError();
     if (e == hipSuccess && parts > 1) {
       const int64_t n4 = static_cast<int64_t>(E) * D / 4;
-      router_dense_sum_kernel<<<static_cast<unsigned>((n4 + kThreads - 1) / kThreads), kThreads, 0,
-                                s>>>(reinterpret_cast<const float4*>(ws),
-                                     reinterpret_cast<float4*>(dw), n4, parts);
+      router_dense_sum_kernel<<<static_cast<unsigned>((n4 + 63) / 64), kThreads, 0, s>>>(
+          reinterpret_cast<const float4*>(ws), reinterpret_cast<float4*>(dw), n4, parts);
       e = hipGetLastError();
     }
   }
