@@ -35,5 +35,5 @@ from ._binding import (  # noqa: F401
     moe_router_backward_dense, moe_router_backward_dense_workspace_size,
 )
 from .layer import (  # noqa: F401
-    EPRankShareForward, ExpertMuon, LayerForward, LayerForwardMXFP8, LayerTrain,
+    EPRankShareForward, ExpertMuon, LayerForward, LayerForwardFP8, LayerForwardMXFP8, LayerTrain,
 )

@@ -10,6 +10,11 @@ into the layout the grouped GEMMs feed to the matrix cores, once.
 a call routes (fp32 router), permutes the bf16 rows, quantizes them, runs the
 MXFP8 grouped FFN and combines in fp32 into the bf16 residual.
 
+``LayerForwardFP8`` is the layer with the FP8 expert FFN with block scales
+(include/moe_fp8.h): its expert weights, routed and shared, are given as codes
+and scales, as fine-grained MoE weights are distributed, or in bf16 and packed
+once; a call routes, permutes, quantizes the rows, runs the FP8 FFN and combines.
+
 ``LayerTrain`` runs the layer forward through the step entry points, keeping
 what the backward needs (routing, offsets, positions, x_perm, y_perm and, with
 ``save_gu`` (bf16 layers), the fp32 gate and up pre-activations of the routed
@@ -21,7 +26,13 @@ T top_k 2I 4 bytes less memory held between the two passes. With ``norm=True``
 it is the pre-norm block out = x + layer(layer_norm(x)): the forward
 normalises first (``moe_layer_norm``, include/moe_norm.h) and the residual stays
 x; the backward runs the layer's pieces, then ``moe_layer_norm_backward``, which
-joins the residual's gradient in.
+joins the residual's gradient in. With ``ckpt=True`` (bf16 layers) it keeps 8-bit
+checkpoints between the passes (include/moe_ckpt.h): G | U (made in the GEMM's
+epilogue), the rows that enter the experts, once a token, and the expert
+outputs, a quarter of the bytes; the bf16 x_perm and the fp32 y_perm are then
+scratch, restored in the backward, which layers that run one after another
+share (``scratch``). With ``balance`` the forward adds the balance loss
+(include/moe_balance.h), and the backward its gradient.
 
 ``ExpertMuon`` steps the expert matrices of a ``LayerTrain`` from its gradients
 (``moe_muon_update``, include/moe_update.h): gate, up and down matrices of every
@@ -111,9 +122,17 @@ class LayerForward:
 class LayerTrain:
     def __init__(self, desc: B.moe_desc, w_router, w_gate_up, w_down, logit_bias=None,
                  shared_gate_up=None, shared_down=None, device="cuda", save_gu=None,
-                 norm=False, norm_gamma=None, norm_beta=None, norm_eps=1e-5):
+                 norm=False, norm_gamma=None, norm_beta=None, norm_eps=1e-5, ckpt=False,
+                 scratch=None, balance=None):
         """norm: a layer norm in front of the layer; norm_gamma, norm_beta [D]
-        fp32 or None (ones, zeros), their gradients in dnorm_gamma, dnorm_beta."""
+        fp32 or None (ones, zeros), their gradients in dnorm_gamma, dnorm_beta.
+        ckpt: 8-bit checkpoints (bf16 layers) in place of save_gu.
+        scratch: a dict that LayerTrain(ckpt=True) layers of equal sizes share
+        for what no layer needs between its passes (None: the layer's own).
+        balance: the coefficient of the balance loss, None for none; the forward
+        leaves the loss in balance_loss [1] and balance_counts [E] (int32),
+        balance_tokens [1] (int32), balance_prob_sum [E], which ranks of one
+        batch add up (all-reduce) before the backward."""
         self.d = desc
         T, D, E, k, I, Is = desc.T, desc.D, desc.E, desc.top_k, desc.I, desc.I_shared
         M = T * k
@@ -130,12 +149,49 @@ class LayerTrain:
         self.split = torch.empty(desc.ep_size, dtype=i32, device=device)
         self.perm_src = torch.empty(max(M, 1), dtype=i32, device=device)
         self.pos = torch.empty(T, k, dtype=i32, device=device)
-        self.x_perm = torch.empty(M, D, dtype=bf, device=device)
-        self.y_perm = torch.empty(M, D, dtype=f32, device=device)
-        self.shared_out = torch.empty(T, D, dtype=f32, device=device) if Is > 0 else None
+        if ckpt and desc.act_dtype != B.MOE_BF16:
+            raise ValueError("ckpt: bf16 layers only")
+        if ckpt and save_gu:
+            raise ValueError("ckpt keeps G | U in 8 bits: not with save_gu")
+        if scratch is not None and not ckpt:
+            raise ValueError("scratch: only with ckpt=True")
+        self.ckpt, self.balance = ckpt, balance
+        pool = {} if scratch is None else scratch
+
+        def shared(name, *shape, dtype=f32):
+            """A tensor of the scratch (made by the first layer that asks)."""
+            t = pool.get(name)
+            if t is None:
+                t = pool[name] = torch.empty(*shape, dtype=dtype, device=device)
+            if tuple(t.shape) != shape or t.dtype != dtype:
+                raise ValueError(f"scratch: {name} is of a layer of other sizes")
+            return t
+
+        def shared_ws(name, nbytes):
+            t = pool.get(name)
+            if t is None or t.numel() < nbytes:
+                t = pool[name] = B.workspace(nbytes, device)
+            return t
+
+        self.x_perm = shared("x_perm", M, D, dtype=bf)
+        self.y_perm = shared("y_perm", M, D)
+        self.shared_out = shared("shared_out", T, D) if Is > 0 else None
+        if ckpt:
+            # What the layer keeps between its passes, in 8 bits.
+            i8 = torch.int8
+            self.gu_q = torch.empty(M, 2 * I, dtype=i8, device=device)
+            self.gu_s = torch.empty(M, 2 * I // 32, dtype=bf, device=device)
+            self.x_q = torch.empty(T, D, dtype=i8, device=device)
+            self.x_s = torch.empty(T, D // 32, dtype=bf, device=device)
+            self.y_q = torch.empty(M, D, dtype=i8, device=device)
+            self.y_s = torch.empty(M, D // 32, dtype=bf, device=device)
+            if Is > 0:
+                self.gu_sh_q = torch.empty(T, 2 * Is, dtype=i8, device=device)
+                self.gu_sh_s = torch.empty(T, 2 * Is // 32, dtype=bf, device=device)
+            self.x_back = shared("x_back", T, D, dtype=bf)
         # fp32 G | U of the forward (bf16 layers only)
         if save_gu is None:
-            save_gu = desc.act_dtype == B.MOE_BF16
+            save_gu = desc.act_dtype == B.MOE_BF16 and not ckpt
         if save_gu and desc.act_dtype != B.MOE_BF16:
             raise ValueError("save_gu: bf16 layers only")
         self.gu = torch.empty(M, 2 * I, dtype=f32, device=device) if save_gu else None
@@ -143,8 +199,8 @@ class LayerTrain:
                       if save_gu and Is > 0 else None)
         self.ws_route = B.workspace(B.moe_route_workspace_size(desc), device)
         self.ws_perm = B.workspace(B.moe_permute_workspace_size(desc, 0, E), device)
-        self.ws_ffn = B.workspace(B.moe_ffn_workspace_size(desc, I, M), device)
-        self.ws_sh = B.workspace(B.moe_ffn_workspace_size(desc, Is, T), device) if Is > 0 else None
+        self.ws_ffn = shared_ws("ws_ffn", B.moe_ffn_workspace_size(desc, I, M))
+        self.ws_sh = shared_ws("ws_sh", B.moe_ffn_workspace_size(desc, Is, T)) if Is > 0 else None
         # gradients
         self.dx = torch.empty(T, D, dtype=bf, device=device)
         self.dw_router = torch.empty(E, D, dtype=f32, device=device)
@@ -154,51 +210,87 @@ class LayerTrain:
         self.dw_shared_down = torch.empty(Is, D, dtype=f32, device=device) if Is else None
         self.x = None
         self.norm = norm
-        if not norm:
-            if norm_gamma is not None or norm_beta is not None:
-                raise ValueError("norm_gamma, norm_beta: only with norm=True")
+        if not norm and (norm_gamma is not None or norm_beta is not None):
+            raise ValueError("norm_gamma, norm_beta: only with norm=True")
+        if balance is not None:
+            self.logits = torch.empty(T, E, dtype=f32, device=device)
+            self.balance_counts = torch.empty(E, dtype=i32, device=device)
+            self.balance_tokens = torch.empty(1, dtype=i32, device=device)
+            self.balance_prob_sum = torch.empty(E, dtype=f32, device=device)
+            self.balance_loss = torch.empty(1, dtype=f32, device=device)
+            self.ws_balance = B.workspace(B.moe_balance_loss_workspace_size(T, E), device)
+            self.mask = None
+        # Without any of the three, moe_layer_backward does it all.
+        self.pieces = norm or ckpt or balance is not None
+        if not self.pieces:
             self.ws_bwd = B.workspace(B.moe_backward_workspace_size(desc), device)
             return
-        self.norm_gamma, self.norm_beta, self.norm_eps = norm_gamma, norm_beta, norm_eps
-        self.h = torch.empty(T, D, dtype=bf, device=device)
-        self.mean = torch.empty(T, dtype=f32, device=device)
-        self.rstd = torch.empty(T, dtype=f32, device=device)
-        # what the layer's backward leaves between its pieces
-        self.dh = torch.empty(T, D, dtype=bf, device=device)
-        self.dy_perm = torch.empty(M, D, dtype=bf, device=device)
-        self.dx_perm = torch.empty(M, D, dtype=f32, device=device)
-        self.dx_shared = torch.empty(T, D, dtype=f32, device=device) if Is else None
-        self.dlogit = torch.empty(T, k, dtype=f32, device=device)
-        self.dl_perm = torch.empty(max(M, 1), dtype=f32, device=device)
-        self.dnorm_gamma = torch.empty(D, dtype=f32, device=device)
-        self.dnorm_beta = torch.empty(D, dtype=f32, device=device)
         ffn = B.moe_ffn_backward_workspace_size(desc, I, M)
         if Is:
             ffn = max(ffn, B.moe_ffn_backward_workspace_size(desc, Is, T))
-        self.ws_bwd = B.workspace(max(
-            ffn, B.moe_router_backward_workspace_size(desc, M),
-            B.moe_layer_norm_backward_workspace_size(T, D)), device)
+        need = max(ffn, B.moe_router_backward_workspace_size(desc, M))
+        # what the layer's backward leaves between its pieces
+        self.dy_perm = shared("dy_perm", M, D, dtype=bf)
+        self.dx_perm = shared("dx_perm", M, D)
+        self.dx_shared = shared("dx_shared", T, D) if Is or balance is not None else None
+        self.dlogit = shared("dlogit", T, k)
+        self.dl_perm = shared("dl_perm", max(M, 1))
+        if balance is not None:
+            self.dlogits = shared("dlogits", T, E)
+            need = max(need, B.moe_router_backward_dense_workspace_size(T, E, D))
+        if norm:
+            self.norm_gamma, self.norm_beta, self.norm_eps = norm_gamma, norm_beta, norm_eps
+            self.h = shared("h", T, D, dtype=bf)
+            self.mean = torch.empty(T, dtype=f32, device=device)
+            self.rstd = torch.empty(T, dtype=f32, device=device)
+            self.dh = shared("dh", T, D, dtype=bf)
+            self.dnorm_gamma = torch.empty(D, dtype=f32, device=device)
+            self.dnorm_beta = torch.empty(D, dtype=f32, device=device)
+            need = max(need, B.moe_layer_norm_backward_workspace_size(T, D))
+        self.ws_bwd = shared_ws("ws_bwd", need)
 
-    def forward(self, x, stream=None):
+    def forward(self, x, stream=None, mask=None):
+        """mask [T] uint8 or bool: tokens that count in the balance loss (None:
+        all)."""
         d, w = self.d, self.w
         E, I, M = d.E, d.I, d.T * d.top_k
-        self.x = res = x
+        res = x
+        # The backward's input: kept, or restored from its checkpoint.
+        self.x = None if self.ckpt and not self.norm else x
         if self.norm:
             B.moe_layer_norm(x, self.norm_gamma, self.norm_beta, self.norm_eps, self.h, self.mean,
                              self.rstd, stream)
             x = self.h
-        B.moe_route(d, x, w["w_router"], w["logit_bias"], None, None, self.topk_idx, self.topk_w,
+        if mask is not None and self.balance is None:
+            raise ValueError("mask: only with balance")
+        logits = self.logits if self.balance is not None else None
+        B.moe_route(d, x, w["w_router"], w["logit_bias"], logits, None, self.topk_idx, self.topk_w,
                     ws=self.ws_route, stream=stream)
+        if self.balance is not None:
+            self.mask = mask
+            B.moe_balance_loss(logits, self.topk_idx, self.balance, self.balance_counts,
+                               self.balance_tokens, self.balance_prob_sum, self.balance_loss,
+                               self.ws_balance, mask=mask, stream=stream)
         B.moe_permute(d, x, self.topk_idx, 0, E, M, self.counts, self.offsets, self.split,
                       self.perm_src, self.pos, self.x_perm, self.ws_perm, stream)
-        if self.gu is not None:
+        if self.ckpt:
+            B.moe_ckpt_save_rows(x, self.x_q, self.x_s, stream)
+            B.moe_expert_ffn_train_ckpt(d, E, I, M, self.x_perm, self.offsets, w["w_gate_up"],
+                                        w["w_down"], self.y_perm, self.gu_q, self.gu_s,
+                                        self.ws_ffn, stream)
+            B.moe_ckpt_save_rows(self.y_perm, self.y_q, self.y_s, stream)
+        elif self.gu is not None:
             B.moe_expert_ffn_train(d, E, I, M, self.x_perm, self.offsets, w["w_gate_up"],
                                    w["w_down"], self.y_perm, self.gu, self.ws_ffn, stream)
         else:
             B.moe_expert_ffn(d, E, I, M, self.x_perm, self.offsets, w["w_gate_up"], w["w_down"],
                              self.y_perm, self.ws_ffn, stream)
         if self.shared_out is not None:
-            if self.gu_sh is not None:
+            if self.ckpt:
+                B.moe_expert_ffn_train_ckpt(d, 1, d.I_shared, d.T, x, None, w["shared_gate_up"],
+                                            w["shared_down"], self.shared_out, self.gu_sh_q,
+                                            self.gu_sh_s, self.ws_sh, stream)
+            elif self.gu_sh is not None:
                 B.moe_expert_ffn_train(d, 1, d.I_shared, d.T, x, None, w["shared_gate_up"],
                                        w["shared_down"], self.shared_out, self.gu_sh, self.ws_sh,
                                        stream)
@@ -209,33 +301,68 @@ class LayerTrain:
                                 d.T, self.out, stream)
         return self.out
 
-    def _backward_norm(self, dout, stream):
+    def _backward_pieces(self, dout, dloss, stream):
         d, w, ws = self.d, self.w, self.ws_bwd
         E, I, M = d.E, d.I, d.T * d.top_k
+        if self.ckpt:
+            B.moe_ckpt_restore_rows(self.x_q, self.x_s, self.x_back, stream=stream)
+            B.moe_ckpt_restore_rows(self.x_q, self.x_s, self.x_perm, self.perm_src[:M], stream)
+            B.moe_ckpt_restore_rows(self.y_q, self.y_s, self.y_perm, stream=stream)
+            x = self.x_back
+        else:
+            x = self.h if self.norm else self.x
         B.moe_combine_backward(d, dout, self.y_perm, self.pos, self.topk_w, self.dy_perm, None,
                                self.dlogit, self.dl_perm, stream)
-        B.moe_expert_ffn_backward(d, E, I, M, self.x_perm, self.offsets, w["w_gate_up"],
-                                  w["w_down"], self.dy_perm, self.dx_perm, self.dw_gate_up,
-                                  self.dw_down, ws, stream, gu_saved=self.gu)
-        if self.dx_shared is not None:
+        gate_up, down = w["w_gate_up"], w["w_down"]
+        if self.ckpt:
+            B.moe_expert_ffn_backward_ckpt(d, E, I, M, self.x_perm, self.offsets, gate_up, down,
+                                           self.dy_perm, self.gu_q, self.gu_s, self.dx_perm,
+                                           self.dw_gate_up, self.dw_down, ws, stream)
+        else:
+            B.moe_expert_ffn_backward(d, E, I, M, self.x_perm, self.offsets, gate_up, down,
+                                      self.dy_perm, self.dx_perm, self.dw_gate_up, self.dw_down,
+                                      ws, stream, gu_saved=self.gu)
+        if self.shared_out is not None:
             gate_up, down, dgate_up, ddown = (
                 t[None] for t in (w["shared_gate_up"], w["shared_down"], self.dw_shared_gate_up,
                                   self.dw_shared_down))
-            B.moe_expert_ffn_backward(d, 1, d.I_shared, d.T, self.h, None, gate_up, down, dout,
-                                      self.dx_shared, dgate_up, ddown, ws, stream,
-                                      gu_saved=self.gu_sh)
-        B.moe_router_backward(d, M, self.x_perm, self.offsets, self.dl_perm, self.dw_router, ws,
-                              stream)
-        # The residual's gradient joins behind the norm, not here.
-        B.moe_input_backward(d, self.dx_perm, self.pos, self.topk_idx, self.dlogit, w["w_router"],
-                             self.dx_shared, None, self.dh, stream)
-        B.moe_layer_norm_backward(self.x, self.dh, self.norm_gamma, self.mean, self.rstd, dout,
-                                  self.dx, self.dnorm_gamma, self.dnorm_beta, ws, stream)
+            if self.ckpt:
+                B.moe_expert_ffn_backward_ckpt(d, 1, d.I_shared, d.T, x, None, gate_up, down, dout,
+                                               self.gu_sh_q, self.gu_sh_s, self.dx_shared,
+                                               dgate_up, ddown, ws, stream)
+            else:
+                B.moe_expert_ffn_backward(d, 1, d.I_shared, d.T, x, None, gate_up, down, dout,
+                                          self.dx_shared, dgate_up, ddown, ws, stream,
+                                          gu_saved=self.gu_sh)
+        dlogit = self.dlogit
+        if self.balance is not None:
+            # The router's whole gradient, dense: dx goes the way of the shared
+            # expert's.
+            B.moe_balance_loss_backward(self.logits, self.topk_idx, self.balance,
+                                        self.balance_counts, self.balance_tokens, dloss,
+                                        self.dlogits, mask=self.mask, dlogit=dlogit, stream=stream)
+            B.moe_router_backward_dense(self.dlogits, x, w["w_router"], self.dx_shared,
+                                        self.dw_router, ws,
+                                        accumulate=self.shared_out is not None, stream=stream)
+            dlogit = None
+        else:
+            B.moe_router_backward(d, M, self.x_perm, self.offsets, self.dl_perm, self.dw_router,
+                                  ws, stream)
+        # With a norm the residual's gradient joins behind it, not here.
+        B.moe_input_backward(d, self.dx_perm, self.pos, self.topk_idx, dlogit, w["w_router"],
+                             self.dx_shared, None if self.norm else dout,
+                             self.dh if self.norm else self.dx, stream)
+        if self.norm:
+            B.moe_layer_norm_backward(self.x, self.dh, self.norm_gamma, self.mean, self.rstd, dout,
+                                      self.dx, self.dnorm_gamma, self.dnorm_beta, ws, stream)
         return self.dx
 
-    def backward(self, dout, stream=None):
-        if self.norm:
-            return self._backward_norm(dout, stream)
+    def backward(self, dout, stream=None, dloss=None):
+        """dloss [1] fp32: the gradient of balance_loss (None: 1)."""
+        if dloss is not None and self.balance is None:
+            raise ValueError("dloss: only with balance")
+        if self.pieces:
+            return self._backward_pieces(dout, dloss, stream)
         w = self.w
         B.moe_layer_backward(self.d, self.x, w["w_router"], w["w_gate_up"], w["w_down"],
                              w["shared_gate_up"], w["shared_down"], self.topk_idx, self.topk_w,
@@ -448,3 +575,71 @@ class LayerForwardMXFP8:
                                 stream)
         return self.out
 
+
+class LayerForwardFP8:
+    """w_gate_up, w_down (and the shared expert's) are bf16 or fp32 tensors,
+    stacked as for LayerForward and packed here, or pairs (codes, scales) in the
+    layout of include/moe_fp8.h: codes [E, 2I, D] and [E, D, I], scales one for
+    each 128 x 128 block. y_fp16: expert outputs in fp16 (default) or fp32."""
+
+    def __init__(self, desc: B.moe_desc, w_router, w_gate_up, w_down, logit_bias=None,
+                 shared_gate_up=None, shared_down=None, want_logits=False, device="cuda",
+                 y_fp16=True):
+        if desc.act_dtype != B.MOE_BF16:
+            raise ValueError("the FP8 layer takes a bf16 layer")
+        self.d = desc = _layer_desc(desc, False, y_fp16)
+        T, D, E, k, I, Is = desc.T, desc.D, desc.E, desc.top_k, desc.I, desc.I_shared
+        M = T * k
+
+        def pack(w):
+            if isinstance(w, (tuple, list)):
+                return tuple(t if t.dim() == 3 else t[None] for t in w)
+            return B.pack_expert_weights_fp8(w if w.dim() == 3 else w[None])
+
+        self.w_router, self.logit_bias = w_router, logit_bias
+        self.gate_up, self.down = pack(w_gate_up), pack(w_down)
+        u8, i32, f32, bf = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+        ydt = torch.float16 if y_fp16 else f32
+        self.out = torch.empty(T, D, dtype=bf, device=device)
+        self.logits = torch.empty(T, E, dtype=f32, device=device) if want_logits else None
+        self.topk_idx = torch.empty(T, k, dtype=i32, device=device)
+        self.topk_w = torch.empty(T, k, dtype=f32, device=device)
+        self.counts = torch.empty(E, dtype=i32, device=device)
+        self.offsets = torch.empty(E + 1, dtype=i32, device=device)
+        self.split = torch.empty(desc.ep_size, dtype=i32, device=device)
+        self.perm_src = torch.empty(max(M, 1), dtype=i32, device=device)
+        self.pos = torch.empty(T, k, dtype=i32, device=device)
+        self.x_perm = torch.empty(M, D, dtype=bf, device=device)
+        self.xq = torch.empty(M, D, dtype=u8, device=device)
+        self.xs = torch.empty((D + 127) // 128, M, dtype=f32, device=device)
+        self.y_perm = torch.empty(M, D, dtype=ydt, device=device)
+        self.ws_route = B.workspace(B.moe_route_workspace_size(desc), device)
+        self.ws_perm = B.workspace(B.moe_permute_workspace_size(desc, 0, E), device)
+        need = B.moe_ffn_fp8_workspace_size(desc, I, M)
+        self.shared_out = None
+        if Is > 0:
+            self.sh_gate_up, self.sh_down = pack(shared_gate_up), pack(shared_down)
+            self.xq_sh = torch.empty(T, D, dtype=u8, device=device)
+            self.xs_sh = torch.empty((D + 127) // 128, T, dtype=f32, device=device)
+            self.shared_out = torch.empty(T, D, dtype=ydt, device=device)
+            need = max(need, B.moe_ffn_fp8_workspace_size(desc, Is, T))
+        self.ws_ffn = B.workspace(need, device)
+
+    def __call__(self, x, stream=None):
+        d = self.d
+        E, I, M = d.E, d.I, d.T * d.top_k
+        B.moe_route(d, x, self.w_router, self.logit_bias, self.logits, None, self.topk_idx,
+                    self.topk_w, ws=self.ws_route, stream=stream)
+        B.moe_permute(d, x, self.topk_idx, 0, E, M, self.counts, self.offsets, self.split,
+                      self.perm_src, self.pos, self.x_perm, self.ws_perm, stream)
+        B.moe_fp8_quantize_rows(self.x_perm, self.xq, self.xs, stream)
+        B.moe_expert_ffn_fp8(d, E, I, M, self.xq, self.xs, self.offsets, *self.gate_up, *self.down,
+                             self.y_perm, self.ws_ffn, stream)
+        if self.shared_out is not None:
+            B.moe_fp8_quantize_rows(x, self.xq_sh, self.xs_sh, stream)
+            B.moe_expert_ffn_fp8(d, 1, d.I_shared, d.T, self.xq_sh, self.xs_sh, None,
+                                 *self.sh_gate_up, *self.sh_down, self.shared_out, self.ws_ffn,
+                                 stream)
+        B.moe_unpermute_combine(d, self.y_perm, self.pos, self.topk_w, x, self.shared_out, 0, d.T,
+                                self.out, stream)
+        return self.out
