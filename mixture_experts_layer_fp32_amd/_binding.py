@@ -939,13 +939,16 @@ def _public_stream(dev: int) -> int:
 # The handle of torch's current stream of a GPU: without a Stream object where
 # this torch can (1 us less of a call of 7), by its public interface otherwise.
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_stream)
+# The same for the current device (its public form checks each time that torch
+# has begun to use the GPU, as every tensor here shows it has).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _launch(name: str, dev: int, args, stream):
     """Call entry point `name` with GPU dev current, on `stream` (None: torch's
     current stream of dev)."""
     fn = getattr(_lib or load_library(), name)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = fn(*args, _current_stream(dev) if stream is None else _stream(stream))
     else:
         with torch.cuda.device(dev):
