@@ -10,7 +10,9 @@
  * block, the product in fp32, rounded up to bf16. A value's code is the
  * integer nearest to v * fp32(1/s), ties to even, in -127 .. 127; it comes
  * back as code * s, off by at most s / 2: 1/254 of the block's largest
- * magnitude (and 2^-7 of that from the scale's rounding). An equal step
+ * magnitude (and 2^-7 of that from the scale's rounding). The scale is at most
+ * 2^121, so that no value becomes infinite, in bf16 neither; with that scale
+ * codes are those of v * fp32(127/128 2^-121) and values off by up to 1.5 s. An equal step
  * over the block suits values that are summed into gradients better than a
  * floating-point code, whose step grows with the value: for normally
  * distributed values the error is 0.5 % of the standard deviation, that of

@@ -8,15 +8,24 @@
 namespace moe {
 
 // Scale (bf16 bits) of a block whose largest magnitude has these fp32 bits:
-// amax / 127 rounded up to bf16, so that every code fits. A NaN stays one.
+// amax / 127 rounded up to bf16, so that every code fits, at most 2^121: the
+// largest value, 127 times that, is then finite in bf16 too. A NaN stays one.
+constexpr uint32_t kCkptTopScale = 0x7c00u;  // 2^121
 __device__ __forceinline__ uint32_t ckpt_scale_bits(uint32_t amax_bits) {
   const float s = __uint_as_float(amax_bits) * (1.0f / 127.0f);
   const uint32_t b = max(__float_as_uint(s) & 0x7fffffffu, 0x00800000u);
-  return b > 0x7f800000u ? 0x7fc0u : (b + 0xffffu) >> 16;
+  if (b >= 0x7f800000u) return b > 0x7f800000u ? 0x7fc0u : 0x7f80u;
+  return min((b + 0xffffu) >> 16, kCkptTopScale);
+}
+// The factor r of the codes: 1 / s; with the largest scale 127/128 of it, which
+// takes the largest fp32 value to 127.
+__device__ __forceinline__ float ckpt_factor(uint32_t scale_bits) {
+  const float r = 1.0f / __uint_as_float(scale_bits << 16);
+  return scale_bits == kCkptTopScale ? 0x1.fcp-122f : r;
 }
 
 // Four codes: the nearest integers to v r, in -127 .. 127 since r <= 127 / amax
-// up to one rounding. Adding 1.5 * 2^23 rounds to the nearest even integer and
+// up to two roundings. Adding 1.5 * 2^23 rounds to the nearest even integer and
 // leaves it in the low byte. (In a block with a NaN or an infinity the codes
 // mean nothing: its scale is NaN, or infinite with codes 0.)
 __device__ __forceinline__ uint32_t ckpt_codes4(float a, float b, float c, float d, float r) {

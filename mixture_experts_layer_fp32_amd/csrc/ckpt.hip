@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_save_kernel(const void* __restr
     for (int j = 0; j < 16; ++j) amax = max(amax, __float_as_uint(f[j]) & 0x7fffffffu);
     amax = max(amax, static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(amax), 0xB1, 0xF, 0xF, false)));
     const uint32_t s = ckpt_scale_bits(amax);
-    const float r = 1.0f / __uint_as_float(s << 16);
+    const float r = ckpt_factor(s);
     if (v < n_vec) {
       codes[v] = make_uint4(ckpt_codes4(f[0], f[1], f[2], f[3], r),
                             ckpt_codes4(f[4], f[5], f[6], f[7], r),

@@ -872,7 +872,7 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_bf16(
               const auto both = __builtin_amdgcn_permlane32_swap(amax, amax, false, false);
               const uint32_t sb = ckpt_scale_bits(max(static_cast<uint32_t>(both[0]),
                                                       static_cast<uint32_t>(both[1])));
-              const float rs = 1.0f / __uint_as_float(sb << 16);
+              const float rs = ckpt_factor(sb);
               uint32_t w[4];
     #pragma unroll
               for (int g = 0; g < 4; ++g)

@@ -106,9 +106,11 @@ def ckpt_rows(x):
     with np.errstate(all="ignore"):
         s = np.maximum(_abs_max(p, 2) * np.float32(1 / 127), TINY)
         bits = s.view(np.uint32).astype(np.uint64)
-        bits = np.where(np.isnan(s), 0x7FC0, (bits + 0xFFFF) >> 16).astype(np.uint16)
-        sv = bf16_values(bits)
-        v = p * (np.float32(1) / sv)[:, :, None]
+        bits = np.where(np.isnan(s), 0x7FC0, (bits + 0xFFFF) >> 16)
+        bits = np.where(np.isfinite(s), np.minimum(bits, 0x7C00), bits).astype(np.uint16)
+        r = np.float32(1) / bf16_values(bits)
+        r = np.where(bits == 0x7C00, np.float32(127 / 128 * 2.0 ** -121), r)
+        v = p * r[:, :, None]
         codes = np.where(np.isnan(v), 0, np.rint(v)).astype(np.int8)
     return codes.reshape(x.shape), bits
 

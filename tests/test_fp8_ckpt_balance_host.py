@@ -63,6 +63,18 @@ def test_ckpt_error_is_half_a_step():
     assert (fo.bf16_values(bits) * 127 <= top * (1 + 2.0 ** -7)).all()
 
 
+def test_ckpt_of_the_largest_values_is_finite():
+    top = np.finfo(np.float32).max
+    m = np.array([top, -top, 255 * 2.0 ** 120, 127 * 2.0 ** 121, 126.4 * 2.0 ** 121, 2.0 ** 127])
+    x = np.concatenate([np.diag(m), np.outer(m, np.linspace(-1, 1, 26))], 1).astype(np.float32)
+    codes, bits = fo.ckpt_rows(x)
+    back = fo.ckpt_values(codes, bits)
+    s = np.repeat(fo.bf16_values(bits), 32, 1)
+    # half a step, and 1/128 of up to 128 steps with the largest scale
+    assert (np.abs(back.astype(np.float64) - x) <= 1.5 * (1 + 2.0 ** -16) * s).all()
+    assert torch.isfinite(torch.from_numpy(back).to(torch.bfloat16)).all()
+
+
 def test_balance_gradient_against_differences():
     g = np.random.default_rng(3)
     T, E, k, coef = 6, 5, 2, 0.3

@@ -85,6 +85,25 @@ def test_nan_and_infinity_stay_in_their_block():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_largest_values_stay_finite(dtype):
+    """A type's largest value comes back finite, in bf16 too."""
+    top = torch.finfo(dtype).max
+    x = torch.randn(6, 96, generator=torch.Generator().manual_seed(8)).to(dtype)
+    x[0, 3], x[1, 40], x[2, 64] = top, -top, 255 * 2.0 ** 120
+    x[3, :32] = torch.linspace(-1, 1, 32).double().mul(top).to(dtype)
+    x[4, 0], x[5, 95] = 126.4 * 2.0 ** 121, 2.0 ** 127
+    codes, scales = save(x)
+    want_c, want_s = fo.ckpt_rows(x.float().numpy())
+    assert np.array_equal(bits(scales), want_s)
+    assert np.array_equal(codes.cpu().numpy(), want_c)
+    for dt in (torch.float32, BF):
+        out = torch.empty(6, 96, dtype=dt, device="cuda")
+        moe.moe_ckpt_restore_rows(codes, scales, out)
+        assert torch.isfinite(out).all()
+        assert torch.equal(out.cpu(), torch.from_numpy(fo.ckpt_values(want_c, want_s)).to(dt))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
 def test_restore_through_an_index(dtype):
     rows, D, n = 50, 160, 333
     x = rows_of(rows, D, 3, dtype)
