@@ -43,8 +43,8 @@ extern "C" {
  *  x       [rows, D] dtype
  *  codes   [rows, D] int8 out, scales [rows, D / 32] bf16 out
  * x and codes are aligned to 16 bytes. Errors: INVALID_ARG (sizes, NULL,
- * alignment), UNSUPPORTED (dtype, D, rows above INT32_MAX, rows * D of 2^34 or
- * more).
+ * alignment), UNSUPPORTED (dtype, D, rows above INT32_MAX, (rows + 16) * D
+ * above 2^34).
  */
 moe_status moe_ckpt_save_rows(int64_t rows, int32_t D, int32_t dtype, const void* x, void* codes,
                               void* scales, void* stream);

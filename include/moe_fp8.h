@@ -44,7 +44,7 @@ extern "C" {
  *  codes   [rows, K] uint8 out, scales [B(K), rows] fp32 out
  * Pointers are aligned to 16 bytes. Errors: INVALID_ARG (sizes, NULL,
  * alignment), UNSUPPORTED (dtype, K above MOE_MAX_WIDTH, rows above INT32_MAX,
- * rows * K of 2^34 or more).
+ * (rows + 16) * K above 2^34).
  */
 moe_status moe_fp8_quantize_rows(int64_t rows, int32_t K, int32_t dtype, const void* x,
                                  void* codes, float* scales, void* stream);
@@ -108,7 +108,7 @@ moe_status moe_expert_down_fp8(const moe_desc* desc, int32_t n_experts, int32_t 
  *  ws   workspace of at least moe_ffn_fp8_workspace_size() bytes, aligned to
  *       16 bytes (H, its codes and its scales)
  *  other arguments and errors as above; WORKSPACE if ws_bytes is smaller,
- *  UNSUPPORTED also for cap_rows * inter of 2^34 or more
+ *  UNSUPPORTED also for (cap_rows + 16) * inter above 2^34
  */
 moe_status moe_expert_ffn_fp8(const moe_desc* desc, int32_t n_experts, int32_t inter,
                               int64_t cap_rows, const void* xq, const float* xs,

@@ -1148,12 +1148,12 @@ MOE_API moe_status moe_muon_update(int32_t n, int32_t rows, int32_t cols,
 namespace {
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Sizes of a quantizer whose values, codes and grid (at least 4096 values a
-// workgroup) stay within 64-bit offsets and 2^32 threads.
+// Sizes of a quantizer whose grid stays below 2^32 threads (256 a workgroup of
+// 16 rows at least, of 64 columns or more).
 moe_status check_rows(int64_t rows, int32_t D, int32_t multiple, int32_t most, int32_t dtype) {
   if (rows < 0 || D <= 0 || D % multiple != 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
-  if (D > most || rows > INT_MAX || rows >= (int64_t(1) << 34) / D) return MOE_ERR_UNSUPPORTED;
+  if (D > most || rows > INT_MAX || rows > (int64_t(1) << 34) / D - 16) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -1409,8 +1409,8 @@ moe_status check_router_dense(int32_t T, int32_t E, int32_t D, int32_t dtype) {
   if (T < 0 || E < 1 || D <= 0 || D % 64 != 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (E > MOE_MAX_EXPERTS || D > MOE_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
-  // fewer than 2^24 workgroups a launch
-  if ((static_cast<int64_t>(T) + 63) / 64 * (D / 64) >= (int64_t(1) << 24))
+  // fewer than 2^32 threads a launch (512 for 128 tokens, 256 for 64)
+  if ((static_cast<int64_t>(T) + 127) / 128 * (D / 64) >= (int64_t(1) << 23))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

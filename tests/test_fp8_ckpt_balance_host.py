@@ -15,6 +15,17 @@ P = ctypes.c_void_p(0x1000)   # never dereferenced: every call below fails its c
 ODD = ctypes.c_void_p(0x1008)
 
 
+# Sizes whose launch would have 2^32 threads, and sizes past it.
+@pytest.mark.parametrize("rows,K", [(2 ** 28 - 15, 64), (2 ** 28 - 1, 64), (2 ** 28, 64),
+                                    (2 ** 27 - 1, 128)])
+def test_sizes_past_a_launch(lib, rows, K):
+    assert lib.moe_fp8_quantize_rows(rows, K, B.MOE_BF16, P, P, P, None) == B.MOE_ERR_UNSUPPORTED
+    assert lib.moe_ckpt_save_rows(rows, K, B.MOE_BF16, P, P, P, None) == B.MOE_ERR_UNSUPPORTED
+    T = min(2 ** 31 - 1, rows * 8)
+    assert lib.moe_router_backward_dense(T, 8, K, B.MOE_BF16, P, P, P, 0, P, None,
+                                         None, 0, None) == B.MOE_ERR_UNSUPPORTED
+
+
 @pytest.fixture(scope="module")
 def lib():
     if not os.path.exists(B.LIB_PATH):  # build only when nothing is built yet

@@ -103,6 +103,16 @@ def test_fp8_layer(name):
         assert torch.equal(again(dv["x"]), got)
 
 
+def test_fp8_layer_without_tokens():
+    w = wl.Workload("none", T=0, D=64, E=4, k=2, I=64, dtype="bf16", I_shared=64)
+    dv, _ = inputs(w)
+    d = moe.make_desc(T=0, D=64, E=4, top_k=2, I=64, I_shared=64)
+    lay = moe.LayerForwardFP8(d, dv["w_router"], dv["w_gate_up"], dv["w_down"],
+                              shared_gate_up=dv["shared_gate_up"], shared_down=dv["shared_down"])
+    assert lay(dv["x"]).shape == (0, 64)
+    assert not lay.counts.any()
+
+
 def test_fp8_layer_refuses_fp32():
     w = LAYERS["f32"]
     d = moe.make_desc(T=w.T, D=w.D, E=w.E, top_k=w.k, I=w.I, dtype="f32")
@@ -141,6 +151,23 @@ def test_ckpt_step_against_the_plain_one(name, norm):
         got = grads(kept)[k]
         assert torch.isfinite(got).all(), k
         assert rel(got, want) < 0.03, (k, rel(got, want))
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_no_tokens(ckpt, norm):
+    """A step of a rank that got no tokens: zero gradients, zero loss."""
+    w = wl.Workload("none", T=0, D=64, E=4, k=2, I=64, dtype="bf16", I_shared=64)
+    dv, dout = inputs(w)
+    lay = layer(w, dv, ckpt=ckpt, norm=norm, balance=0.1)
+    lay.balance_loss.fill_(7.0)
+    for g in grads(lay).values():
+        g.fill_(7.0)
+    assert lay.forward(dv["x"]).shape == (0, 64)
+    lay.backward(dout)
+    assert lay.balance_loss.item() == 0 and lay.balance_tokens.item() == 0
+    assert not lay.balance_counts.any() and not lay.balance_prob_sum.any()
+    assert not any(g.any() for g in grads(lay).values())
 
 
 def test_layers_that_share_scratch():
