@@ -117,6 +117,13 @@ __global__ __launch_bounds__(kLossThreads) void balance_part_kernel(
   const int64_t t1 = static_cast<int64_t>(Tn) * (blockIdx.x + 1) / parts;
   float acc[NI] = {};
   int tok = 0;
+  // The first slots of this thread, read before the tokens' logits are waited
+  // for.
+  constexpr int kSlots = 4;
+  const int64_t q0 = t0 * k + tid, q1 = t1 * k;
+  int slot[kSlots];
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) slot[i] = topk[min(q0 + i * kLossThreads, q1 - 1)];
   // Two tokens at a time (fewer registers: one), logits and mask in flight
   // together; a token that does not count is read and left out.
   constexpr int U = NI <= 8 ? 2 : 1;
@@ -138,10 +145,15 @@ __global__ __launch_bounds__(kLossThreads) void balance_part_kernel(
         tok += l == 0;
       }
   }
-  for (int64_t q = t0 * k + tid; q < t1 * k; q += kLossThreads) {
-    const int e = topk[q];
-    if (e >= 0 && e < E && !(mask && mask[q / k] == 0)) atomicAdd(&s_count[e], 1);
-  }
+  auto count = [&](int64_t q, int e) {
+    // (a part has fewer than 2^31 slots)
+    if (e >= 0 && e < E && !(mask && mask[t0 + static_cast<uint32_t>(q - t0 * k) / k] == 0))
+      atomicAdd(&s_count[e], 1);
+  };
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i)
+    if (q0 + i * kLossThreads < q1) count(q0 + i * kLossThreads, slot[i]);
+  for (int64_t q = q0 + kSlots * kLossThreads; q < q1; q += kLossThreads) count(q, topk[q]);
   if (tok) atomicAdd(&s_tok, tok);
 #pragma unroll
   for (int i = 0; i < NI; ++i) s_prob[g * EC + l + L * i] = acc[i];
@@ -244,6 +256,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
     const int32_t* __restrict__ tokens, const float* __restrict__ dloss,
     const float* __restrict__ dlogit, float* __restrict__ dlogits) {
   constexpr int G = kThreads / L;
+  constexpr int kSlots = 8;
   const int tid = threadIdx.x, l = tid % L;
   const double N = *tokens;
   // coef E / (k N^2) c: the gradient of the loss for p
@@ -258,6 +271,16 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
   for (int64_t t = static_cast<int64_t>(blockIdx.x) * G + tid / L; t < Tn; t += step) {
     float d[NI] = {}, e[NI];
     load_row<T, L, NI>(logits + t * E, E, l, e);
+    // The first slots, in flight with the logits.
+    int x[kSlots];
+    float v[kSlots];
+    if (dlogit) {
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        x[j] = topk[t * k + min(j, k - 1)];
+        v[j] = dlogit[t * k + min(j, k - 1)];
+      }
+    }
     if (!(mask && mask[t] == 0)) {
       const float r = softmax_row<L, NI>(e);
       float dot = 0.f;
@@ -268,13 +291,15 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(
       for (int i = 0; i < NI; ++i) d[i] = e[i] * r * (f[i] - dot);
     }
     if (dlogit) {
-      for (int j = 0; j < k; ++j) {
-        const int x = topk[t * k + j];
-        const float v = dlogit[t * k + j];
+      auto add = [&](int xj, float vj) {
 #pragma unroll
         for (int i = 0; i < NI; ++i)
-          if (x == l + L * i) d[i] += v;
-      }
+          if (xj == l + L * i) d[i] += vj;
+      };
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j)
+        if (j < k) add(x[j], v[j]);
+      for (int j = kSlots; j < k; ++j) add(topk[t * k + j], dlogit[t * k + j]);
     }
     if (E == L * NI) {
 #pragma unroll
