@@ -165,12 +165,13 @@ __device__ __forceinline__ int find_expert(const int* s_pref, int n_exp, int t, 
 // block of 128) are copied to LDS one step ahead (2 x 64 KB), with the rows'
 // 256 scales; the LDS holds no third slot. One workgroup per CU works through
 // its share of the tile list, which is dealt to the XCDs in contiguous runs.
-// Mixtral-style gate_up (16384 rows, 4096 x 28672): 1.77 ms, 2.17 PFLOP/s,
-// against 2.66 that a library's plain FP8 product of 8192^3 reaches and 3.7 of
-// a loop of the instruction alone (random operands: the clock falls to
-// 2.0 GHz); its steps take 1.9 us, 1.1 of them matrix instructions: what is
-// left is the wait for copies that come one step ahead, and the reads that
-// start a step.
+// Mixtral-style gate_up (16384 rows, 4096 x 28672): 1.79 to 1.89 ms from card
+// to card (their clocks differ), 2.04 to 2.15 PFLOP/s, against 2.66 to 2.77
+// that a library's plain FP8 product of 8192^3 reaches and 3.7 of a loop of the
+// instruction alone (random operands: the clock falls to 2.0 GHz). A step takes
+// 1.9 us, 1.1 of them matrix instructions; a step's first fragments read behind
+// the products of the step before (4 % faster to 3 % slower, by shape and card)
+// and lines touched two steps ahead (2 to 6 % slower) did not shorten the rest.
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 512;
 constexpr int BM = 256, BN = 256, BK = 128;
@@ -447,7 +448,7 @@ __global__ __launch_bounds__(kThreads, 1) void fp8_gemm_kernel(
 // activation fragments straight into registers, a whole block (16 KB of
 // weights) ahead of its use and without a barrier, and add their sums in LDS.
 // Two workgroups a CU keep 128 KB in flight there. One new token on eight
-// experts (7168 x 4096 codes each, 235 MB): 44 us, 5.3 TB/s, what a copy
+// experts (7168 x 4096 codes each, 235 MB): 46 us, 5.1 TB/s, what a copy
 // reaches; 78 us with the large tiles.
 // ---------------------------------------------------------------------------
 constexpr int kSmallThreads = 256, kWaves = kSmallThreads / 64;

