@@ -644,17 +644,22 @@ hipError_t launch_gemm(int n_experts, int64_t cap_rows, int K, int N, const void
                        void* out, hipStream_t s) {
   const int n = offsets ? n_experts : 1;
   const int64_t cus = std::max<int64_t>(kXcds, num_cus() / kXcds * kXcds);
-  // Small tiles read the weights once for each 32 rows, large ones for 256. Up
-  // to 32 rows an expert (of cap_rows: the counts are on the device) small
-  // ones win where K is long or large ones leave CUs idle, to 64 where those
-  // leave half of them idle. Measured, large against small: 32 experts of
-  // 7168 x 4096, 16 rows each, 184 : 168 us; 8 of 14336 x 4096, 64 rows each,
-  // 165 : 141 us (96: 185 : 201); 16 of 2048 x 1024, 4 rows, 17 : 13 us; but 16
-  // of 1024 x 4096 (256 large tiles), 15 : 18 us, 128 of 768 x 2048, 40 : 47 us.
-  const int64_t large =
-      std::min<int64_t>(cap_rows, n) * ((N + BN / (GATED ? 2 : 1) - 1) / (BN / (GATED ? 2 : 1)));
-  const bool small = (cap_rows <= 32 * n && (K >= 2048 || large < cus)) ||
-                     (cap_rows <= 64 * n && 2 * large <= cus);
+  // Small tiles (32 x 128) read the weights once for each 32 rows, large ones
+  // (256 x 256) once for each 256, but large ones alone leave CUs idle, and take
+  // longer over a block of few rows. Small ones win where they number a CU or
+  // less, and, up to 32 rows an expert, where K is long and they are many (of
+  // cap_rows, spread evenly: the counts are on the device). Measured, large
+  // against small: one expert of 1024 rows, 2048 -> 1024 (256 small tiles),
+  // 29 : 15 us; 8 of 14336 -> 4096, 32 rows each (256), 179 : 88; 32 of 7168 ->
+  // 2 x 2048, 16 rows each (1024), 199 : 168; but 64 of 512 -> 512, 40 rows each
+  // (512), 8 : 13, 40 of 1024 -> 1024, 16 rows each (320), 14 : 17, 8 of 1024 ->
+  // 2 x 1024, 96 rows each (384), 12 : 18. (Over 600 such cases the choice is 1 %
+  // slower than the better of the two in the mean, at most 1.34 times.)
+  const int64_t hit = std::min<int64_t>(cap_rows, n);
+  const int64_t small_tiles = hit * ((cap_rows + SM * hit - 1) / (SM * hit)) *
+                              ((N + SN / (GATED ? 2 : 1) - 1) / (SN / (GATED ? 2 : 1)));
+  const bool small = small_tiles <= cus ||
+                     (cap_rows <= SM * hit && K >= 2048 && small_tiles >= 2 * cus);
   const int bm = small ? SM : BM, bn = (small ? SN : BN) / (GATED ? 2 : 1);
   const int64_t mt = std::min<int64_t>(cap_rows, cap_rows / bm + n);
   const int64_t tiles = mt * ((N + bn - 1) / bn);

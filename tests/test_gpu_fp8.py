@@ -283,6 +283,69 @@ def test_rows_past_two_to_the_31_codes():
     assert (out[:-300] == 0).all()
 
 
+# ---- large tiles: buffers of many rows beyond the segments choose them ----
+def widened(p, cap=9000):
+    """p in a buffer of cap rows, those past the segments NaN."""
+    xq, xs, off, wq, ws = p.gpu
+    big_q = torch.full((cap, xq.shape[1]), 0x7F, dtype=torch.uint8, device="cuda")
+    big_q[:p.rows] = xq[:p.rows]
+    big_s = torch.full((xs.shape[0], cap), float("nan"), device="cuda")
+    big_s[:, :p.rows] = xs[:, :p.rows]
+    p.cap, p.gpu = cap, [big_q, big_s, off, wq, ws]
+    p.y, p.err = (np.pad(a[:p.rows], ((0, cap - p.rows), (0, 0))) for a in (p.y, p.err))
+    return p
+
+
+@pytest.mark.parametrize("counts,cap", COUNTS)
+@pytest.mark.parametrize("K,N", [(64, 64), (192, 320), (512, 256), (1088, 448)])
+def test_down_ragged_large_tiles(counts, cap, K, N):
+    p = widened(Product(counts, K, N, None, seed=len(counts) + K))
+    check_down(p, K, N, half=K % 128 == 0)
+
+
+@pytest.mark.parametrize("counts,cap", COUNTS)
+@pytest.mark.parametrize("K,I", [(64, 64), (192, 192), (512, 256), (1088, 320)])
+def test_gate_up_ragged_large_tiles(counts, cap, K, I):
+    check_gate_up(widened(Product(counts, K, 2 * I, None, seed=len(counts) + I)), K, I)
+
+
+def test_large_tiles_many_experts_long_k_and_no_rows():
+    check_down(widened(Product([i % 3 for i in range(130)], 128, 128, seed=1)), 128, 128, False)
+    check_down(widened(Product([7, 90], 8256, 64, seed=2)), 8256, 64, False)
+    check_down(widened(Product([0, 0, 0], 128, 64, 1, seed=1)), 128, 64, True)
+
+
+def test_large_tiles_values_of_another_expert_do_not_leak():
+    counts, K, N = [20, 20, 20], 192, 192
+    p = widened(Product(counts, K, N, seed=4))
+    xq, xs, off, wq, ws = [t.clone() for t in p.gpu]
+    xq[:20], xq[40:] = 0x7F, 0x7F
+    xs[:, :20], xs[:, 40:] = float("inf"), float("nan")
+    wq[0], wq[2] = 0x7F, 0x7F
+    d = moe.make_desc(T=p.cap, D=N, E=3, top_k=1, I=K)
+    out = torch.zeros(p.cap, N, device="cuda")
+    moe.moe_expert_down_fp8(d, 3, K, p.cap, xq, xs, off, wq, ws, out)
+    y = out.cpu().double().numpy()[20:40]
+    assert (np.abs(y - p.y[20:40]) <= p.err[20:40] + 2.0 ** -24 * np.abs(p.y[20:40])).all()
+    assert np.isnan(out[:20].cpu().numpy()).all() and (out[60:] == 0).all()
+
+
+def test_small_and_large_tiles_one_tile_a_cu_apart():
+    """The same rows in buffers whose small tiles number one a CU, and more."""
+    p = Product([100, 28], 320, 1024, seed=7)
+    got = []
+    for cap in (1024, 1025, 4000):   # 8 column tiles: 256 small tiles, 272, ...
+        q = widened(Product([100, 28], 320, 1024, seed=7), cap)
+        d = moe.make_desc(T=cap, D=1024, E=2, top_k=1, I=320)
+        out = torch.zeros(cap, 1024, device="cuda")
+        moe.moe_expert_down_fp8(d, 2, 320, cap, *q.gpu, out)
+        got.append(out[:128].cpu().double().numpy())
+        assert (out[128:] == 0).all()
+    for y in got:
+        assert y.shape == p.y.shape
+        assert (np.abs(y - p.y) <= p.err + 2.0 ** -24 * np.abs(p.y)).all()
+
+
 def test_binding_refuses_wrong_shapes():
     p = Product([4, 4], 128, 64, seed=6)
     xq, xs, off, wq, ws = p.gpu
