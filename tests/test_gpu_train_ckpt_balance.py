@@ -320,3 +320,40 @@ def test_whole_step_replayed():
         for k, v in grads(lay).items():
             assert torch.equal(got[k], v), k
         assert torch.equal(got["loss"], lay.balance_loss)
+
+
+# ---- two streams at once ----
+def test_calls_on_two_streams_at_once():
+    """Layers with buffers of their own, stepped on two streams side by side:
+    the bits of steps one after another."""
+    w = LAYERS["shared"]
+    runs = []
+    for seed in (5, 6):
+        dv, dout = inputs(w, seed)
+        d = moe.make_desc(T=w.T, D=w.D, E=w.E, top_k=w.k, I=w.I, I_shared=w.I_shared)
+        fp8 = moe.LayerForwardFP8(d, dv["w_router"], dv["w_gate_up"], dv["w_down"],
+                                  shared_gate_up=dv["shared_gate_up"],
+                                  shared_down=dv["shared_down"])
+        lay = layer(w, dv, ckpt=True, balance=0.1, norm=True)
+
+        def step(stream=None, dv=dv, dout=dout, fp8=fp8, lay=lay):
+            fp8(dv["x"], stream)
+            lay.forward(dv["x"], stream)
+            lay.backward(dout, stream)
+
+        def results(fp8=fp8, lay=lay):
+            return [t.clone() for t in (fp8.out, lay.out, lay.balance_loss, *grads(lay).values())]
+
+        runs.append((step, results))
+    want = []
+    for step, results in runs:
+        step()
+        want.append(results())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for (step, _), s in zip(runs, streams):
+            step(s)
+    torch.cuda.synchronize()
+    for (_, results), ref in zip(runs, want):
+        assert all(torch.equal(a, b) for a, b in zip(results(), ref))
