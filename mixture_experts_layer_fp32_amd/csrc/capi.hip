@@ -1409,8 +1409,8 @@ moe_status check_router_dense(int32_t T, int32_t E, int32_t D, int32_t dtype) {
   if (T < 0 || E < 1 || D <= 0 || D % 64 != 0) return MOE_ERR_INVALID_ARG;
   if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (E > MOE_MAX_EXPERTS || D > MOE_MAX_WIDTH) return MOE_ERR_UNSUPPORTED;
-  // fewer than 2^32 threads a launch (512 for 128 tokens, 256 for 64)
-  if ((static_cast<int64_t>(T) + 127) / 128 * (D / 64) >= (int64_t(1) << 23))
+  // fewer than 2^32 threads a launch (at most 512 for 64 tokens and 64 columns)
+  if ((static_cast<int64_t>(T) + 63) / 64 * (D / 64) >= (int64_t(1) << 23))
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }

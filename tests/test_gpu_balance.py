@@ -190,7 +190,8 @@ def test_same_bits_every_call_and_graph_replays():
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("T,E,D", [(1, 1, 64), (3, 8, 128), (65, 5, 192), (256, 8, 128),
                                    (1000, 17, 320), (2500, 64, 256), (700, 128, 448),
-                                   (300, 1000, 64), (4097, 130, 64)])
+                                   (300, 1000, 64), (4097, 130, 64), (130, 257, 320),
+                                   (64, 600, 256), (3, 1024, 448), (8200, 300, 320)])
 def test_router_dense(T, E, D, dtype):
     g = torch.Generator().manual_seed(T + E + D)
     dz = torch.randn(T, E, generator=g) * torch.exp(torch.randn(T, 1, generator=g))
