@@ -186,9 +186,10 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_bf16(
     int64_t cap_rows, const uint16_t* __restrict__ W, void* __restrict__ Cout, int K,
     int N_out, const float* __restrict__ dh_in, uint16_t* __restrict__ h_out,
     const uint16_t* const* __restrict__ w_ptrs, float* __restrict__ gu_out, int y_half,
-    float* __restrict__ tail_ws, int ncus, int tail_cap) {
+    float* __restrict__ tail_ws, int ncus, int tail_cap, int row_block) {
   constexpr bool GATED = MODE != kDown;  // gate and up columns paired in a wave
   constexpr int BM = bm_of(WN);
+  const int bm = MODE == kGateUpCkpt ? row_block : BM;  // rows of a tile, at most
   constexpr int kTileA = BM * BK * 2;
   constexpr int NA = BM / 32;            // 1 KB activation copies per wave per step
   constexpr int BNB = 2 * WN;
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_bf16(
         end = static_cast<int>(
             min(max(static_cast<int64_t>(end), static_cast<int64_t>(beg)), cap_rows));
       }
-      const int tiles = ((end - beg + BM - 1) / BM) * NT;
+      const int tiles = ((end - beg + bm - 1) / bm) * NT;
       int incl = tiles;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -358,7 +359,7 @@ __global__ __launch_bounds__(kThreads, 1) void ffn_gemm_bf16(
     const int local = t - __builtin_amdgcn_readfirstlane(s_pref[expert]);
     // The segment's rows are cut into mt near-equal row blocks of at most BM.
     const int cnt = seg_end - seg_beg;
-    const int mt = (cnt + BM - 1) / BM;
+    const int mt = (cnt + bm - 1) / bm;
     const int chunk = (cnt + mt - 1) / mt;
     // An expert's tiles are ordered column block by column block over groups
     // of GR row blocks: all its row blocks in one group when it has at most 8
@@ -1285,7 +1286,7 @@ hipError_t launch_ffn(int n_experts, int64_t cap_rows, int K, int n_out, const v
         static_cast<const uint16_t*>(a), offsets, n_experts, cap_rows,
         static_cast<const uint16_t*>(w), out, K, n_out, dh_in, static_cast<uint16_t*>(h_out),
         reinterpret_cast<const uint16_t* const*>(w_ptrs), gu_out, y_half ? 1 : 0,
-        split ? tail_ws : nullptr, cus, tail_cap);
+        split ? tail_ws : nullptr, cus, tail_cap, bm_of(128));
     if (split) {
       // at most tail_cap / 2 tail tiles (2 parts or more each)
       const hipError_t e = hipGetLastError();
@@ -1300,14 +1301,22 @@ hipError_t launch_ffn(int n_experts, int64_t cap_rows, int K, int n_out, const v
             reinterpret_cast<const float4*>(tail_ws), hdr, static_cast<uint16_t*>(out), n_out);
     }
   } else {
-    const unsigned g =
-        grid_of(tile_bound(cap_rows, offsets, n_experts, n_out, kWideOut / 2, bm_of(64)), true);
+    auto count = [&](int bm) {
+      return tile_bound(cap_rows, offsets, n_experts, n_out, kWideOut / 2, bm);
+    };
+    // kGateUpCkpt: the smallest row blocks of which there is one a CU at most
+    // (5 experts, 777 rows, 320 x 2 * 192: 8.1 us, with blocks of 320 11.7; 200
+    // rows of one, 1024 x 2 * 1024: 13.5 : 19.3).
+    int bm = bm_of(64);
+    if (MODE == kGateUpCkpt)
+      while (bm > 64 && count(bm - 64) <= num_cus()) bm -= 64;
+    const unsigned g = grid_of(count(bm), true);
     ffn_gemm_bf16<MODE, 64, PACKED><<<g, kThreads, 0, s>>>(static_cast<const uint16_t*>(a), offsets,
                                                    n_experts, cap_rows,
                                                    static_cast<const uint16_t*>(w), out, K, n_out,
                                                    dh_in, static_cast<uint16_t*>(h_out),
                                                    reinterpret_cast<const uint16_t* const*>(w_ptrs),
-                                                   gu_out, y_half ? 1 : 0, nullptr, 0, 0);
+                                                   gu_out, y_half ? 1 : 0, nullptr, 0, 0, bm);
   }
   return hipGetLastError();
 }

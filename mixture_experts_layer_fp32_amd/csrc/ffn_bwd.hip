@@ -126,8 +126,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
     const uint16_t* __restrict__ A, const int32_t* __restrict__ offsets, int n_experts,
     int64_t cap_rows, const uint16_t* __restrict__ W, int K, int N_out, float* __restrict__ cf,
     const float* __restrict__ gu, uint16_t* __restrict__ dgu, uint16_t* __restrict__ hout,
-    const uint16_t* __restrict__ gu_scales) {
+    const uint16_t* __restrict__ gu_scales, int row_block) {
   using namespace nt;
+  const int bm = EPI == kSwigluCkpt ? row_block : BM;  // rows of a tile, at most
   constexpr int kLds = 2 * kTileA + NSB * kTileB;
   static_assert(kLds + 2 * (kMaxTableExperts + 1) * 4 <= 160 * 1024, "LDS budget");
   __shared__ __attribute__((aligned(1024))) unsigned char smem[kLds];
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
         end = static_cast<int>(
             min(max(static_cast<int64_t>(end), static_cast<int64_t>(beg)), cap_rows));
       }
-      const int tiles = ((end - beg + BM - 1) / BM) * NT;
+      const int tiles = ((end - beg + bm - 1) / bm) * NT;
       int incl = tiles;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -201,7 +202,7 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_nt_bf16(
     const int seg_end = __builtin_amdgcn_readfirstlane(s_off[expert + 1]);
     const int local = t - __builtin_amdgcn_readfirstlane(s_pref[expert]);
     const int cnt = seg_end - seg_beg;
-    const int mt = (cnt + BM - 1) / BM;
+    const int mt = (cnt + bm - 1) / bm;
     const int chunk = (cnt + mt - 1) / mt;
     const int nb = local / mt, mbk = local - nb * mt;
     const int row_begin = seg_beg + mbk * chunk;
@@ -741,14 +742,22 @@ hipError_t launch_nt(int n_experts, int64_t cap_rows, int K, int n_out, const vo
                      const float* gu = nullptr, void* dgu = nullptr, void* h = nullptr,
                      const void* gu_scales = nullptr) {
   using namespace nt;
-  const int64_t mtiles = (cap_rows + BM - 1) / BM + (offsets ? n_experts : 0);
-  const int64_t tiles = mtiles * ((n_out + BN - 1) / BN);
   const int64_t cus = std::max<int64_t>(kXcds, num_cus_bwd() / kXcds * kXcds);
+  auto count = [&](int bm) {
+    return ((cap_rows + bm - 1) / bm + (offsets ? n_experts : 0)) * ((n_out + BN - 1) / BN);
+  };
+  // kSwigluCkpt: the smallest row blocks of which there is one a CU at most (5
+  // experts, 777 rows, 320 x 192: 9.4 us, with blocks of 320 15.5; 200 rows of
+  // one, 1024 x 1024: 15 : 23; 4096 rows of one, 2048 x 1024: 38 : 46).
+  int bm = BM;
+  if (EPI == kSwigluCkpt)
+    while (bm > 64 && count(bm - 64) <= cus) bm -= 64;
+  const int64_t tiles = count(bm);
   const int64_t g = std::min((tiles + kXcds - 1) / kXcds * kXcds, cus);
   gemm_nt_bf16<EPI><<<static_cast<unsigned>(g), kThreads, 0, s>>>(
       static_cast<const uint16_t*>(a), offsets, n_experts, cap_rows,
       static_cast<const uint16_t*>(w), K, n_out, cf, gu, static_cast<uint16_t*>(dgu),
-      static_cast<uint16_t*>(h), static_cast<const uint16_t*>(gu_scales));
+      static_cast<uint16_t*>(h), static_cast<const uint16_t*>(gu_scales), bm);
   return hipGetLastError();
 }
 

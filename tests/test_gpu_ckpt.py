@@ -161,7 +161,12 @@ CASES = [([5], 128, 64, None), ([0, 3, 0, 40, 1], 320, 192, 50), ([300, 20, 0, 9
          ([700, 2], 256, 128, 800), ([1], 64, 64, 1)]
 
 
-@pytest.mark.parametrize("counts,D,I,cap", CASES)
+# Buffers of many rows choose longer row blocks (up to 320).
+WIDE = [([300, 20, 0, 90], 192, 128, 30000), ([700, 2], 128, 128, 45000),
+        ([1, 650, 33], 64, 192, 70000), ([0, 319, 321, 640], 64, 64, 90000)]
+
+
+@pytest.mark.parametrize("counts,D,I,cap", CASES + WIDE)
 def test_training_forward_codes(counts, D, I, cap):
     """y_perm is the plain training forward's bit for bit, and the codes are
     those of the fp32 G | U that it keeps."""
@@ -188,9 +193,9 @@ def test_training_forward_codes(counts, D, I, cap):
 def reference_backward(L, codes, scales):
     """dgu, h in float64 and dH's error, from the kept values."""
     gu = fo.ckpt_values(codes.cpu().numpy(), bits(scales)).astype(np.float64)[:L.rows]
-    dy, wd = L.dy.double().cpu().numpy(), L.wd.double().cpu().numpy()
+    dy, wd = L.dy[:L.rows].double().cpu().numpy(), L.wd.double().cpu().numpy()
     off = L.off.cpu().numpy()
-    dh, mag = fo.grouped(dy[:L.rows], wd, off)
+    dh, mag = fo.grouped(dy, wd, off)
     dg, du, h = fo.swiglu_backward(gu[:, :L.I], gu[:, L.I:], dh)
     edh = mag * (L.D + 2) * 2.0 ** -24
     eg, eu, _ = fo.swiglu_backward(gu[:, :L.I], gu[:, L.I:], edh)
@@ -199,7 +204,7 @@ def reference_backward(L, codes, scales):
     return ref, err, h
 
 
-@pytest.mark.parametrize("counts,D,I,cap", CASES)
+@pytest.mark.parametrize("counts,D,I,cap", CASES + WIDE)
 def test_backward_from_codes(counts, D, I, cap):
     L = Layer(counts, D, I, cap, seed=1)
     codes, scales = L.kept()
