@@ -178,8 +178,8 @@ __device__ __forceinline__ int find_expert(const int* s_pref, int n_exp, int t, 
 // block of 128) are copied to LDS one step ahead (2 x 64 KB), with the rows'
 // 256 scales; the LDS holds no third slot. One workgroup per CU works through
 // its share of the tile list, which is dealt to the XCDs in contiguous runs.
-// Mixtral-style gate_up (16384 rows, 4096 x 28672): 1.79 to 1.89 ms from card
-// to card (their clocks differ), 2.04 to 2.15 PFLOP/s, against 2.66 to 2.77
+// Mixtral-style gate_up (16384 rows, 4096 x 28672): 1.74 to 1.89 ms from card
+// to card (their clocks differ), 2.04 to 2.21 PFLOP/s, against 2.66 to 2.77
 // that a library's plain FP8 product of 8192^3 reaches and 3.7 of a loop of the
 // instruction alone (random operands: the clock falls to 2.0 GHz). A step takes
 // 1.9 us, 1.1 of them matrix instructions; a step's first fragments read behind
