@@ -56,10 +56,11 @@ constexpr int kOutOfRange = 0x7FFF0000;
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // 16 bytes global -> LDS at lds_base + 16 * lane (M0 holds the LDS base).
-// Out-of-range offsets write zeros. Counted by vmcnt.
+// Out-of-range offsets write zeros. Counted by vmcnt. (s_nop: a copy needs one
+// wait state behind a write of M0, which nobody adds to assembly.)
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
                                       unsigned lds_base) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds_base) : "memory", "m0");
 }
 #pragma clang diagnostic pop

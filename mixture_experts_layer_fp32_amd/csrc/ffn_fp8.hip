@@ -36,15 +36,17 @@ enum OutKind { kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2 };
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // 16 (4) bytes a lane global -> LDS at lds_base + 16 (4) * lane; offsets past
-// the resource write zeros. Counted by vmcnt.
+// the resource write zeros. Counted by vmcnt. (s_nop: a copy needs one wait
+// state behind a write of M0, and five behind the v_readfirstlane that makes a
+// resource's register, which nobody adds to assembly.)
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
                                       unsigned lds_base) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds_base) : "memory", "m0");
 }
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
                                      unsigned lds_base) {
-  asm volatile("s_mov_b32 m0, %3\n\tbuffer_load_dword %0, %1, %2 offen lds"
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds_base) : "memory", "m0");
 }
 #pragma clang diagnostic pop
