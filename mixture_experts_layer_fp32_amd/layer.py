@@ -254,6 +254,14 @@ class LayerTrain:
         all)."""
         d, w = self.d, self.w
         E, I, M = d.E, d.I, d.T * d.top_k
+        if mask is not None and self.balance is None:
+            raise ValueError("mask: only with balance")
+        # Refused before anything that the backward of the step before needs is
+        # replaced.
+        dev = B._device_of(self.out, "out")
+        B._device_of(x, "x")
+        B._ptr_on(dev, x, "x", self.out.dtype, (d.T, d.D))
+        B._mask(dev, mask, d.T)
         res = x
         # The backward's input: kept, or restored from its checkpoint.
         self.x = None if self.ckpt and not self.norm else x
@@ -261,8 +269,6 @@ class LayerTrain:
             B.moe_layer_norm(x, self.norm_gamma, self.norm_beta, self.norm_eps, self.h, self.mean,
                              self.rstd, stream)
             x = self.h
-        if mask is not None and self.balance is None:
-            raise ValueError("mask: only with balance")
         logits = self.logits if self.balance is not None else None
         B.moe_route(d, x, w["w_router"], w["logit_bias"], logits, None, self.topk_idx, self.topk_w,
                     ws=self.ws_route, stream=stream)
