@@ -209,6 +209,7 @@ class LayerTrain:
         self.dw_shared_gate_up = torch.empty(D, 2 * Is, dtype=f32, device=device) if Is else None
         self.dw_shared_down = torch.empty(Is, D, dtype=f32, device=device) if Is else None
         self.x = None
+        self.stepped = False  # a forward has been done
         self.norm = norm
         if not norm and (norm_gamma is not None or norm_beta is not None):
             raise ValueError("norm_gamma, norm_beta: only with norm=True")
@@ -305,6 +306,7 @@ class LayerTrain:
                                  w["shared_down"], self.shared_out, self.ws_sh, stream)
         B.moe_unpermute_combine(d, self.y_perm, self.pos, self.topk_w, res, self.shared_out, 0,
                                 d.T, self.out, stream)
+        self.stepped = True
         return self.out
 
     def _backward_pieces(self, dout, dloss, stream):
@@ -367,6 +369,10 @@ class LayerTrain:
         """dloss [1] fp32: the gradient of balance_loss (None: 1)."""
         if dloss is not None and self.balance is None:
             raise ValueError("dloss: only with balance")
+        if not self.stepped:
+            # (The positions of the routing are not there yet: they say where
+            # gradients are written.)
+            raise RuntimeError("backward: no forward before it")
         if self.pieces:
             return self._backward_pieces(dout, dloss, stream)
         w = self.w

@@ -40,6 +40,15 @@ def test_mask_without_balance_is_refused_first(norm):
     assert lay.x is kept
 
 
+@pytest.mark.parametrize("kw", [dict(), dict(norm=True), dict(ckpt=True), dict(balance=0.1)],
+                         ids=["plain", "norm", "ckpt", "balance"])
+def test_backward_without_a_forward_is_refused(kw):
+    """Without a GPU: it comes before any call. (The routing's positions would
+    be whatever the memory held, and gradients are written through them.)"""
+    with pytest.raises(RuntimeError, match="no forward"):
+        make("cpu", **kw).backward(rows(2, "cpu"))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kw", [dict(), dict(norm=True), dict(ckpt=True, norm=True)],
                          ids=["plain", "norm", "ckpt"])
