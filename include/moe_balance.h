@@ -93,9 +93,9 @@ moe_status moe_balance_loss_backward(int32_t T, int32_t E, int32_t k, int32_t dt
  *  dw_router  [E, D] fp32 out | NULL (zeros when T is 0)
  *  ws         workspace of at least moe_router_backward_dense_workspace_size()
  *             bytes; may be NULL when dw_router is
- * x, w_router, dx and dw_router are aligned to 16 bytes. Errors: INVALID_ARG
- * (sizes, accumulate, NULL, alignment), UNSUPPORTED (dtype, limits),
- * WORKSPACE.
+ * x, w_router, dx, dw_router and ws are aligned to 16 bytes. Errors:
+ * INVALID_ARG (sizes, accumulate, NULL, alignment), UNSUPPORTED (dtype, limits,
+ * ceil(T / 64) * (D / 64) of 2^23 or more), WORKSPACE.
  */
 moe_status moe_router_backward_dense(int32_t T, int32_t E, int32_t D, int32_t dtype,
                                      const float* dlogits, const void* x, const float* w_router,

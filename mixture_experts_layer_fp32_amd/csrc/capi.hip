@@ -1201,7 +1201,9 @@ MOE_API moe_status moe_fp8_pack_weights(int32_t n, int32_t K, int32_t N, int32_t
 }
 
 MOE_API size_t moe_ffn_fp8_workspace_size(const moe_desc* desc, int32_t inter, int64_t cap_rows) {
-  if (check_ffn_args(desc, 1, inter, cap_rows) != MOE_OK || desc->act_dtype != MOE_BF16) return 0;
+  if (check_ffn_args(desc, 1, inter, cap_rows) != MOE_OK || desc->act_dtype != MOE_BF16 ||
+      check_rows(cap_rows, inter, 64, MOE_MAX_WIDTH, MOE_BF16) != MOE_OK)
+    return 0;
   return ffn_fp8_ws(inter, cap_rows);
 }
 
