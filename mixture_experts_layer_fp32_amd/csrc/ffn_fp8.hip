@@ -56,8 +56,9 @@ __device__ __forceinline__ uint32_t f16_sat_bits(float f) {
   return __builtin_bit_cast(unsigned short, static_cast<_Float16>(c));
 }
 
+// (SiLU first: of a large negative g it is 0, where g u may be infinite.)
 __device__ __forceinline__ float silu_mul(float g, float u) {
-  return g * u * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g));
+  return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * g)) * u;
 }
 
 __device__ __forceinline__ f32x4 mma(const i32x8& w, const i32x8& x) {

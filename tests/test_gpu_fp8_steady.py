@@ -152,3 +152,16 @@ def test_mean_error_of_normal_values(counts, K, N, cap):
     err = (p.down(False) - p.y).abs() / p.mag
     assert float(err.mean()) <= 2.0 ** -18
     assert float(err.max()) <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("cap", [None, 9000])   # small tiles, large tiles
+def test_gate_far_below_zero_gives_zero(cap):
+    """SiLU of a gate of -1e24 is 0, whatever the up value, also where their
+    product leaves fp32's range."""
+    p = Operands([3, 14], 192, 256, cap, seed=8)
+    p.xq[:p.rows], p.wq[:, 128:] = 0x38, 0x38    # all ones: gates < 0 < up values
+    p.wq[:, :128] = 0xB8
+    p.xs[:, :p.rows] = 1e23
+    p.ws[:] = 1.0
+    out = p.gate_up()
+    assert out.shape == (17, 128) and (out == 0).all()
