@@ -62,6 +62,7 @@ would produce it). Torch provides only device memory, streams and events.
 """
 from __future__ import annotations
 
+import functools
 from typing import Optional
 
 import torch
@@ -75,6 +76,20 @@ def _layer_desc(desc: B.moe_desc, packed: bool, y_fp16: bool) -> B.moe_desc:
         d.weight_layout = B.MOE_WEIGHTS_PACKED
     d.expert_out_dtype = B.MOE_F16 if y_fp16 else B.MOE_F32
     return d
+
+
+def _on_own_gpu(method):
+    """The method with the GPU of the layer's tensors current. (Of the calls
+    that these layers make, some run on the current GPU and some on that of
+    their tensors: elsewhere they would not wait for one another.)"""
+    @functools.wraps(method)
+    def run(self, *args, **kwargs):
+        dev = self.out.get_device()
+        if dev < 0 or dev == B._current_device():
+            return method(self, *args, **kwargs)
+        with torch.cuda.device(dev):
+            return method(self, *args, **kwargs)
+    return run
 
 
 class LayerForward:
@@ -250,6 +265,7 @@ class LayerTrain:
             need = max(need, B.moe_layer_norm_backward_workspace_size(T, D))
         self.ws_bwd = shared_ws("ws_bwd", need)
 
+    @_on_own_gpu
     def forward(self, x, stream=None, mask=None):
         """mask [T] uint8 or bool: tokens that count in the balance loss (None:
         all)."""
@@ -365,6 +381,7 @@ class LayerTrain:
                                       self.dx, self.dnorm_gamma, self.dnorm_beta, ws, stream)
         return self.dx
 
+    @_on_own_gpu
     def backward(self, dout, stream=None, dloss=None):
         """dloss [1] fp32: the gradient of balance_loss (None: 1)."""
         if dloss is not None and self.balance is None:
@@ -637,6 +654,7 @@ class LayerForwardFP8:
             need = max(need, B.moe_ffn_fp8_workspace_size(desc, Is, T))
         self.ws_ffn = B.workspace(need, device)
 
+    @_on_own_gpu
     def __call__(self, x, stream=None):
         d = self.d
         E, I, M = d.E, d.I, d.T * d.top_k
