@@ -180,10 +180,18 @@ class LayerTrain:
                 t = pool[name] = torch.empty(*shape, dtype=dtype, device=device)
             if tuple(t.shape) != shape or t.dtype != dtype:
                 raise ValueError(f"scratch: {name} is of a layer of other sizes")
+            return same_device(name, t)
+
+        def same_device(name, t):
+            if t.device != self.out.device:
+                raise ValueError(f"scratch: {name} is on {t.device}, the layer on "
+                                 f"{self.out.device}")
             return t
 
         def shared_ws(name, nbytes):
             t = pool.get(name)
+            if t is not None:
+                same_device(name, t)
             if t is None or t.numel() < nbytes:
                 t = pool[name] = B.workspace(nbytes, device)
             return t

@@ -49,6 +49,18 @@ def test_backward_without_a_forward_is_refused(kw):
         make("cpu", **kw).backward(rows(2, "cpu"))
 
 
+def test_scratch_of_another_device_is_refused():
+    """(Some calls do not look where their tensors are.)"""
+    pool = {}
+    make("meta", ckpt=True, scratch=pool)
+    with pytest.raises(ValueError, match="scratch: x_perm is on meta, the layer on cpu"):
+        make("cpu", ckpt=True, scratch=pool)
+    for t in [k for k in pool if not k.startswith("ws_")]:
+        del pool[t]
+    with pytest.raises(ValueError, match="scratch: ws_ffn is on meta"):
+        make("cpu", ckpt=True, scratch=pool)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kw", [dict(), dict(norm=True), dict(ckpt=True, norm=True)],
                          ids=["plain", "norm", "ckpt"])
