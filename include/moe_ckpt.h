@@ -3,7 +3,7 @@
  * training step keeps from its forward for its backward, in 8.5 bits a value,
  * and the backward of the gated expert layer from it. The fp32 pre-activations
  * G | U that moe_expert_ffn_train keeps are the largest thing a layer holds
- * between the two passes (cap_rows * 2 inter * 4 bytes; here a quarter).
+ * between the two passes (cap_rows * 2 inter * 4 bytes; here 17/64 of them).
  *
  * Format. Blocks of 32 columns of a row share a scale s =
  * bf16_up(max(amax * fp32(1/127), 2^-126)), amax the largest magnitude in the

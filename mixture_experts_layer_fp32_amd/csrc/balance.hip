@@ -2,15 +2,18 @@
 // the router's backward from dense logit gradients (formulas in
 // moe_balance.h).
 //
-// Forward and backward are bound by reading the logits (and writing their
-// gradients) once: a token's E logits sit in the registers of L lanes, lane l
-// holding experts l, l + L, ... (NI of them): few lanes a token (L = 4 .. 64,
-// up to 8 logits each) keep several tokens in a wave and the exchanges of
-// maximum and sum short. The forward sums p over a workgroup's tokens in
+// Forward and backward read the logits (and write their gradients) once: a
+// token's E logits sit in the registers of L lanes, lane l holding experts l,
+// l + L, ... (NI of them): few lanes a token (L = 4 .. 64, up to 8 logits each)
+// keep several tokens in a wave and the exchanges of maximum and sum short. The forward sums p over a workgroup's tokens in
 // registers, then over its lane groups in LDS, writes one partial of E values,
 // and a second launch adds the partials in fp64 (one workgroup needs no second
-// launch). 16384 x 128 fp32 logits, k = 8: 10.9 + 6.2 us forward, 10.0 backward,
-// the latency of a few dependent reads (8.4 MB to read take 1.7 us).
+// launch). 16384 x 128 fp32 logits, k = 8: 10.4 + 5.9 us forward, 9.6 backward in
+// a trace with two sets of inputs (12.1 and 7.5 us a call over one set), where
+// the 8.4 MB to read take 1.7 us (the gradient's 16.8 MB 3.3): kMaxParts
+// workgroups leave half of the CUs without work, and the second launch, one
+// workgroup, reads 128 parts. (More parts, and a join without a launch of its
+// own, have not been measured.)
 #include <algorithm>
 #include <type_traits>
 
@@ -834,8 +837,12 @@ int balance_parts(int T, int E) {
 // Experts of a dW tile, and the parts its tokens are cut into: two workgroups
 // for every CU, at least 64 tokens each (two steps). Few tokens stay in one part,
 // which needs no launch to add parts up (in parts against in one: 128 tokens, 8
-// experts, D = 128, 8.7 : 6.1 us, 256 8.5 : 8.0; 256 x 256 x 4096 18.5 : 11.7, but
-// 256 x 64 x 1024 9.0 : 11.3, and 512 x 8 x 128 9.0 : 13.8).
+// experts, D = 128, 8.9 : 6.3 us, 256 8.5 : 7.9; 256 x 256 x 4096 18.7 : 11.8, but
+// 200 x 64 x 1024 11.5 : 15.1, and 512 x 8 x 128 8.7 : 13.7). Over 64 to 800
+// tokens and ten sizes of E x D the two are level near 285 tokens of fp32 x and
+// 580 of bf16 x with up to 32 experts, near 115 to 225 with 64 or 128 in few
+// tiles, near 740 with 64 tiles or more. (With 64 tiles the rule changes too
+// early: 320 x 256 x 7168 26.2 : 14.1.)
 int dw_experts(int E) { return E <= 32 ? 32 : 128; }
 int dense_parts(int T, int E, int D) {
   const int me = dw_experts(E);

@@ -38,7 +38,8 @@ enum OutKind { kOutF32 = 0, kOutF16 = 1, kOutBf16 = 2 };
 // 16 (4) bytes a lane global -> LDS at lds_base + 16 (4) * lane; offsets past
 // the resource write zeros. Counted by vmcnt. (s_nop: a copy needs one wait
 // state behind a write of M0, and five behind the v_readfirstlane that makes a
-// resource's register, which nobody adds to assembly.)
+// resource's register, which nobody adds to assembly; four states more were
+// 0.3 to 1.9 % slower, so that these cost about 1 %.)
 __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rsrc, int voff, int soff,
                                       unsigned lds_base) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"

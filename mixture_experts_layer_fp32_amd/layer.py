@@ -29,9 +29,11 @@ x; the backward runs the layer's pieces, then ``moe_layer_norm_backward``, which
 joins the residual's gradient in. With ``ckpt=True`` (bf16 layers) it keeps 8-bit
 checkpoints between the passes (include/moe_ckpt.h): G | U (made in the GEMM's
 epilogue), the rows that enter the experts, once a token, and the expert
-outputs, a quarter of the bytes; the bf16 x_perm and the fp32 y_perm are then
-scratch, restored in the backward, which layers that run one after another
-share (``scratch``). With ``balance`` the forward adds the balance loss
+outputs; the bf16 x_perm and the fp32 y_perm are then scratch, restored in the
+backward, which layers that run one after another share (``scratch``): what a
+layer keeps is then 0.22 to 0.27 of the plain step's bytes. Without a shared
+scratch it holds x_perm and y_perm beside the codes, and only G | U shrinks.
+With ``balance`` the forward adds the balance loss
 (include/moe_balance.h), and the backward its gradient.
 
 ``ExpertMuon`` steps the expert matrices of a ``LayerTrain`` from its gradients
@@ -276,7 +278,8 @@ class LayerTrain:
     @_on_own_gpu
     def forward(self, x, stream=None, mask=None):
         """mask [T] uint8 or bool: tokens that count in the balance loss (None:
-        all)."""
+        all). x (but for ckpt=True without a norm) and mask are read again by
+        the backward: they stay as they are until then."""
         d, w = self.d, self.w
         E, I, M = d.E, d.I, d.T * d.top_k
         if mask is not None and self.balance is None:
